@@ -300,6 +300,139 @@ PBA_API pba_status pba_backward_noalloc(const pba_attn_desc *desc, const void *q
                                         const float *lse, const void *dout, float *dq, float *dk, float *dv,
                                         void *dbias, void *stream);
 
+/*
+ * relpos_bias_forward -- the learned relative position bias by buckets: the
+ * bias matrix that pba_forward and pba_partial add to the scores, made from a
+ * small table and the tokens' positions (the pages name a pair bias and no
+ * rule for one; these are the two rules in common use).
+ *   out[b][h][i][j] = table[r][h] (+ base[b][h][i][j]),
+ *   rel = k_pos[b][j] - q_pos[b][i],
+ *   PBA_RELPOS_CLIP        r = clamp(rel, -R, R) + R, 2R + 1 buckets
+ *   PBA_RELPOS_LOG         n buckets (even, at least 4), half of them for
+ *                          rel <= 0 and half for rel > 0, by d = |rel|
+ *   PBA_RELPOS_LOG_CAUSAL  n buckets (at least 2), all of them for keys at or
+ *                          behind the query, by d = max(-rel, 0)
+ * where the logarithmic rules number the s buckets of a side as d for d < e,
+ * e = s / 2 (rounded down), and min(s - 1, e + floor((s - e) ln(d / e) /
+ * ln(max_distance / e))) beyond; the borders are found in whole numbers, so a
+ * distance at a border falls where the exact quotient says.
+ * With q_group and k_group (chains, sequences packed into one) a pair of
+ * different groups takes the table's last row, one more than the buckets.
+ */
+typedef enum { PBA_RELPOS_CLIP = 0, PBA_RELPOS_LOG = 1, PBA_RELPOS_LOG_CAUSAL = 2 } pba_relpos_rule;
+
+/*
+ *   B, H, Nq, Nk   as in pba_attn_desc (B position sets; 1 to share a bias);
+ *                  B and H up to 65535, B * Nq up to 2^31 - 1
+ *   dtype          of table, base and out (backward: of dbias)
+ *   rows           rows of the table: the buckets, and one more with groups;
+ *                  at most 1025
+ *   max_distance   logarithmic rules: above e, up to 2^30; else ignored
+ *   *_pos_stride_b, *_group_stride_b   batch strides of the int32 arrays
+ *                  (token stride 1); 0 shares one row with every b
+ *   base_stride, out_stride            (b, h, query row) in elements, key
+ *                  stride 1 (backward: out_stride is dbias's)
+ */
+typedef struct {
+  int64_t B, H, Nq, Nk;
+  int32_t dtype, rule, rows, max_distance;
+  int64_t q_pos_stride_b, k_pos_stride_b, q_group_stride_b, k_group_stride_b;
+  int64_t base_stride[3];
+  int64_t out_stride[3];
+} pba_relpos_desc;
+
+/*
+ *   q_pos [B][Nq], k_pos [B][Nk] int32, device (the whole range of int32)
+ *   q_group, k_group  the same shapes, or both NULL
+ *   table [rows][H] device, desc->dtype, contiguous
+ *   base  [B][H][Nq][Nk] device, desc->dtype, or NULL; may be `out` itself.
+ *         The sum is taken in fp32 and rounded once.
+ *   out   [B][H][Nq][Nk] device, desc->dtype
+ * Rows move as 16-byte words when out (and base) start on 16 bytes and every
+ * stride is a multiple of 16 bytes, element by element otherwise.
+ */
+PBA_API pba_status relpos_bias_forward(const pba_relpos_desc *desc, const int32_t *q_pos, const int32_t *k_pos,
+                                       const int32_t *q_group, const int32_t *k_group, const void *table,
+                                       const void *base, void *out, void *stream);
+
+/*
+ * relpos_bias_backward -- the gradient of the table:
+ *   dtable[r][h] = sum over (b, i, j) of row r of dbias[b][h][i][j]
+ *   dbias   [B][H][Nq][Nk] device, desc->dtype: pba_backward's, for instance
+ *   dtable  [rows][H] float, device, contiguous (rows that no pair has get 0)
+ *   workspace  device, 4-byte aligned, at least as many bytes as
+ *           relpos_bias_backward_workspace gives; nothing in it is read before
+ *           it is written, and two calls that may overlap need two of them
+ * (The gradient of base is dbias itself.)  Sums are taken in fp32 over at
+ * most a few thousand terms each and in 64 bits beyond, always in the same
+ * order: the same call gives the same bits.
+ */
+PBA_API pba_status relpos_bias_backward_workspace(const pba_relpos_desc *desc, int64_t *bytes);
+PBA_API pba_status relpos_bias_backward(const pba_relpos_desc *desc, const int32_t *q_pos, const int32_t *k_pos,
+                                        const int32_t *q_group, const int32_t *k_group, const void *dbias,
+                                        float *dtable, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * block_norm_forward -- the norms before and after a block, fused with the
+ * block's gate and residual scale: what stands between an attention block's
+ * output projection and the next block's projections.
+ *   u = post(f)                            (post_w NULL: u = f)
+ *   h = x + scale * sigmoid(gate) * u      (scale, gate NULL: 1; f NULL: h = x)
+ *   y = pre(h)                             (pre_w NULL: no y)
+ * PBA_NORM_LAYER: norm(v) = (v - mean(v)) / sqrt(var(v) + eps) * w + b
+ * PBA_NORM_RMS:   norm(v) = v / sqrt(mean(v^2) + eps) * w + b
+ * with mean and var over the C channels of a row, all arithmetic in fp32 and
+ * h and y rounded once (y is formed from the unrounded h).
+ */
+typedef enum { PBA_NORM_LAYER = 0, PBA_NORM_RMS = 1 } pba_norm_kind;
+
+/*
+ *   rows, C      rows >= 0, 1 <= C <= 8192
+ *   dtype        of x, f, gate, h, y and their gradients
+ *   param_dtype  of scale, post_w, post_b, pre_w, pre_b
+ *   eps          at least 1e-30
+ *   *_stride     row strides in elements, channel stride 1
+ * Rows move as 16-byte words when every row base and parameter starts on 16
+ * bytes and every stride is a multiple of 16 bytes, else element by element.
+ */
+typedef struct {
+  int64_t rows, C;
+  int32_t dtype, param_dtype, kind;
+  float eps;
+  int64_t x_stride, f_stride, gate_stride, h_stride, y_stride;
+  int64_t dh_stride, dy_stride, dx_stride, df_stride, dgate_stride;
+} pba_norm_desc;
+
+/*
+ *   x, f, gate [rows][C] device (f, gate or NULL; gate without f is an error)
+ *   scale, post_w, post_b, pre_w, pre_b [C] device, or NULL (scale and post_w
+ *     need f, a bias needs its weight; pre_w or f must be there)
+ *   h [rows][C] device: required with f, may be x itself; without f not written
+ *   y [rows][C] device: required with pre_w
+ */
+PBA_API pba_status block_norm_forward(const pba_norm_desc *desc, const void *x, const void *f, const void *gate,
+                                      const void *scale, const void *post_w, const void *post_b, const void *pre_w,
+                                      const void *pre_b, void *h, void *y, void *stream);
+
+/*
+ * block_norm_backward -- gradients of block_norm_forward.
+ *   h      the forward's h (its x when f is NULL); read with pre_w only
+ *   dh     dL/dh from the residual stream, or NULL (zero; pre_w only)
+ *   dy     dL/dy: required with pre_w
+ *   dx     dL/dx (= dL/dh through both paths); may be dh or dy itself
+ *   df, dgate   required with f and with gate; may be f and gate themselves
+ *   dscale, dpost_w, dpost_b, dpre_w, dpre_b [C] float, each or NULL: sums over
+ *     the rows, taken in fp32 over a thread's rows and in 64 bits beyond, in a
+ *     fixed order; not written when their parameter is NULL
+ *   workspace  as for relpos_bias_backward, 4-byte aligned
+ */
+PBA_API pba_status block_norm_backward_workspace(const pba_norm_desc *desc, int64_t *bytes);
+PBA_API pba_status block_norm_backward(const pba_norm_desc *desc, const void *h, const void *f, const void *gate,
+                                       const void *scale, const void *post_w, const void *post_b, const void *pre_w,
+                                       const void *pre_b, const void *dh, const void *dy, void *dx, void *df,
+                                       void *dgate, float *dscale, float *dpost_w, float *dpost_b, float *dpre_w,
+                                       float *dpre_b, void *workspace, int64_t workspace_bytes, void *stream);
+
 /* Human-readable name of a status code (static storage). */
 PBA_API const char *pba_status_string(pba_status status);
 

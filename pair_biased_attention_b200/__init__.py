@@ -15,6 +15,7 @@ along one axis of a pair tensor (tri_attn_forward).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -24,6 +25,7 @@ __all__ = [
     "PbaError", "PBA_OK", "PBA_ERR_INVALID_ARG", "PBA_ERR_UNSUPPORTED", "PBA_ERR_CUDA", "PBA_ERR_TIMEOUT",
     "library_path", "load_library", "pba_forward", "pba_partial", "softmax_merge", "tri_attn_forward", "tri_proj_forward", "tri_out_proj_forward", "pwa_forward", "pba_backward",
     "pba_backward_noalloc", "PBA_BWD_NOALLOC_MAX_ROWS",
+    "relpos_bias_forward", "relpos_bias_backward", "block_norm_forward", "block_norm_backward",
     "pba_last_device_error", "pba_set_wait_timeout_ns", "pba_selftest_wait_timeout", "pba_selftest_exp2",
     "pba_status_string",
 ]
@@ -31,6 +33,8 @@ __all__ = [
 PBA_OK, PBA_ERR_INVALID_ARG, PBA_ERR_UNSUPPORTED, PBA_ERR_CUDA, PBA_ERR_TIMEOUT = 0, 1, 2, 3, 4
 PBA_BF16, PBA_F32 = 0, 1
 PBA_TRI_STARTING, PBA_TRI_ENDING = 0, 1
+PBA_RELPOS_CLIP, PBA_RELPOS_LOG, PBA_RELPOS_LOG_CAUSAL = 0, 1, 2
+PBA_NORM_LAYER, PBA_NORM_RMS = 0, 1
 # rows (B * H * Nq) of the fixed Delta array of pba_backward_noalloc (include/pba.h)
 PBA_BWD_NOALLOC_MAX_ROWS = 1048576
 
@@ -49,6 +53,30 @@ class PbaAttnDesc(ctypes.Structure):
         ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
         ("bias_stride", ctypes.c_int64 * 3), ("mask_stride_b", ctypes.c_int64),
         ("out_stride", ctypes.c_int64 * 3), ("lse_stride", ctypes.c_int64 * 3),
+    ]
+
+
+class PbaRelposDesc(ctypes.Structure):
+    """Mirror of pba_relpos_desc."""
+    _fields_ = [
+        ("B", ctypes.c_int64), ("H", ctypes.c_int64), ("Nq", ctypes.c_int64), ("Nk", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("rule", ctypes.c_int32), ("rows", ctypes.c_int32),
+        ("max_distance", ctypes.c_int32),
+        ("q_pos_stride_b", ctypes.c_int64), ("k_pos_stride_b", ctypes.c_int64),
+        ("q_group_stride_b", ctypes.c_int64), ("k_group_stride_b", ctypes.c_int64),
+        ("base_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3),
+    ]
+
+
+class PbaNormDesc(ctypes.Structure):
+    """Mirror of pba_norm_desc."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("C", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32), ("kind", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("x_stride", ctypes.c_int64), ("f_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64),
+        ("h_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+        ("dh_stride", ctypes.c_int64), ("dy_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64),
+        ("df_stride", ctypes.c_int64), ("dgate_stride", ctypes.c_int64),
     ]
 
 
@@ -94,6 +122,18 @@ def load_library() -> ctypes.CDLL:
     lib.pba_backward.restype = st
     lib.pba_backward_noalloc.argtypes = [desc_p] + [_p] * 13
     lib.pba_backward_noalloc.restype = st
+    i64 = ctypes.c_int64
+    i64_p = ctypes.POINTER(i64)
+    relpos_p, norm_p = ctypes.POINTER(PbaRelposDesc), ctypes.POINTER(PbaNormDesc)
+    for name, args in (
+            ("relpos_bias_forward", [relpos_p] + [_p] * 8),
+            ("relpos_bias_backward_workspace", [relpos_p, i64_p]),
+            ("relpos_bias_backward", [relpos_p] + [_p] * 7 + [i64, _p]),
+            ("block_norm_forward", [norm_p] + [_p] * 11),
+            ("block_norm_backward_workspace", [norm_p, i64_p]),
+            ("block_norm_backward", [norm_p] + [_p] * 19 + [i64, _p])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = st
     lib.pba_status_string.argtypes = [st]
     lib.pba_status_string.restype = ctypes.c_char_p
     lib.pba_last_device_error.argtypes = [_p]
@@ -429,6 +469,236 @@ def pba_backward_noalloc(q, k, v, bias, key_mask, out, lse, dout, softmax_scale=
                                                _ptr(key_mask), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
                                                _ptr(dv), _ptr(dbias), _stream(stream)))
     return dq, dk, dv, dbias
+
+
+def _here(*named):
+    """Checks that the tensors (None ones aside) lie on the current device,
+    whose stream the call goes to."""
+    current = torch.cuda.current_device()
+    for name, t in named:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != current:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{current}")
+
+
+def _alloc_on(stream):
+    """Outputs and workspaces made by a call belong to the stream that it
+    launches on, so that the allocator hands them out again in its order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
+_RELPOS_RULES = {"clip": PBA_RELPOS_CLIP, "log": PBA_RELPOS_LOG, "log_causal": PBA_RELPOS_LOG_CAUSAL}
+
+
+def _relpos_desc(rows, H, dtype, q_pos, k_pos, rule, max_distance, q_group, k_group, B=1):
+    """The descriptor without the strides of the matrices.  B: the batch that
+    those ask for; position arrays of one sequence are shared by a batch."""
+    if rule not in _RELPOS_RULES:
+        raise ValueError(f"rule must be one of {sorted(_RELPOS_RULES)}")
+    if (q_group is None) != (k_group is None):
+        raise ValueError("q_group and k_group go together")
+    Nq, Nk = q_pos.shape[-1], k_pos.shape[-1]
+    strides = []
+    given = [("q_pos", q_pos, Nq), ("k_pos", k_pos, Nk), ("q_group", q_group, Nq), ("k_group", k_group, Nk)]
+    for name, t, n in given:
+        if t is None:
+            continue
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name} must be torch.int32, got {t.dtype}")
+        if t.dim() not in (1, 2) or t.shape[-1] != n or (t.stride(-1) != 1 and n > 1):
+            raise ValueError(f"{name} must be [{n}] or [B, {n}] int32, contiguous along tokens")
+        if t.dim() == 2 and t.shape[0] != 1:
+            if B not in (1, t.shape[0]):
+                raise ValueError(f"{name} has batch {t.shape[0]}, another argument has {B}")
+            B = t.shape[0]
+    for name, t, n in given:
+        strides.append(0 if t is None or t.dim() == 1 or t.shape[0] == 1 else t.stride(0))
+    d = PbaRelposDesc(B, H, Nq, Nk, _dtype_code(dtype), _RELPOS_RULES[rule], rows, int(max_distance), *strides)
+    return d
+
+
+def _matrix_strides(name, t, shape, dtype):
+    if tuple(t.shape) != shape or t.dtype != dtype or (t.stride(3) != 1 and shape[3] > 1):
+        raise ValueError(f"{name} must be a {shape} {dtype} tensor, contiguous along keys")
+    return t.stride()[:3]
+
+
+def relpos_bias_forward(table, q_pos, k_pos, rule="clip", max_distance=0, q_group=None, k_group=None, base=None,
+                        out=None, stream=None):
+    """The learned relative position bias: out[b,h,i,j] = table[r, h] (+ base),
+    r the bucket of k_pos[b,j] - q_pos[b,i]; the bias argument of pba_forward
+    and pba_partial.
+
+    table [rows, H] (bf16 or fp32, contiguous); q_pos [Nq] or [B, Nq], k_pos
+    [Nk] or [B, Nk] int32.  rule "clip": rows = 2R+1, clamp(rel, -R, R) + R;
+    "log" (even) and "log_causal": logarithmic buckets up to max_distance, on
+    both sides or for keys at and behind the query.  With q_group and k_group
+    (int32, shaped as the positions) pairs of different groups take one more
+    row, the table's last.  base [B,H,Nq,Nk] of the table's dtype is added
+    (``out`` may be base itself).  Returns out [B,H,Nq,Nk]."""
+    _here(("table", table), ("q_pos", q_pos), ("k_pos", k_pos), ("q_group", q_group), ("k_group", k_group),
+          ("base", base), ("out", out))
+    if table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table must be a contiguous [rows, H] tensor")
+    rows, H = table.shape
+    B = 1
+    for name, t in (("base", base), ("out", out)):
+        if t is not None:
+            if t.dim() != 4:
+                raise ValueError(f"{name} must be [B,H,Nq,Nk]")
+            B = t.shape[0]
+    d = _relpos_desc(rows, H, table.dtype, q_pos, k_pos, rule, max_distance, q_group, k_group, B)
+    shape = (d.B, H, d.Nq, d.Nk)
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty(shape, dtype=table.dtype, device=table.device)
+    d.out_stride[:] = _matrix_strides("out", out, shape, table.dtype)
+    if base is not None:
+        d.base_stride[:] = _matrix_strides("base", base, shape, table.dtype)
+    _check("relpos_bias_forward", load_library().relpos_bias_forward(
+        ctypes.byref(d), _ptr(q_pos), _ptr(k_pos), _ptr(q_group), _ptr(k_group), _ptr(table), _ptr(base), _ptr(out),
+        _stream(stream)))
+    return out
+
+
+def relpos_bias_backward(dbias, q_pos, k_pos, rows, rule="clip", max_distance=0, q_group=None, k_group=None,
+                         stream=None):
+    """The gradient of relpos_bias_forward's table: dbias [B,H,Nq,Nk] (bf16 or
+    fp32, pba_backward's for instance) summed over the pairs of each of the
+    table's ``rows`` rows.  Position arrays of one sequence are shared by the
+    batch of dbias.  Returns dtable [rows, H] (fp32).  The gradient of base is
+    dbias itself."""
+    _here(("dbias", dbias), ("q_pos", q_pos), ("k_pos", k_pos), ("q_group", q_group), ("k_group", k_group))
+    if dbias.dim() != 4:
+        raise ValueError("dbias must be [B,H,Nq,Nk]")
+    B, H = dbias.shape[:2]
+    d = _relpos_desc(int(rows), H, dbias.dtype, q_pos, k_pos, rule, max_distance, q_group, k_group, B)
+    d.out_stride[:] = _matrix_strides("dbias", dbias, (d.B, H, d.Nq, d.Nk), dbias.dtype)
+    lib = load_library()
+    need = ctypes.c_int64()
+    _check("relpos_bias_backward_workspace", lib.relpos_bias_backward_workspace(ctypes.byref(d), ctypes.byref(need)))
+    with _alloc_on(stream):
+        dtable = torch.empty((d.rows, H), dtype=torch.float32, device=dbias.device)
+        work = torch.empty(need.value, dtype=torch.uint8, device=dbias.device)
+    _check("relpos_bias_backward", lib.relpos_bias_backward(
+        ctypes.byref(d), _ptr(q_pos), _ptr(k_pos), _ptr(q_group), _ptr(k_group), _ptr(dbias), _ptr(dtable),
+        _ptr(work), need.value, _stream(stream)))
+    return dtable
+
+
+_NORM_KINDS = {"layer": PBA_NORM_LAYER, "rms": PBA_NORM_RMS}
+
+
+def _row_stride(name, t, shape, dtype):
+    """Row stride of t [..., C] read as rows of C channels (0 for None)."""
+    if t is None:
+        return 0
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor")
+    if t.is_contiguous():
+        return shape[-1]
+    stride, rows = None, 1
+    if t.stride(-1) == 1 or shape[-1] == 1:
+        for i in range(t.dim() - 2, -1, -1):
+            if t.shape[i] == 1:
+                continue
+            if stride is None:
+                stride = t.stride(i)
+            elif t.stride(i) != stride * rows:
+                break
+            rows *= t.shape[i]
+        else:
+            return shape[-1] if stride is None else stride
+    raise ValueError(f"{name} must be rows of contiguous channels a fixed stride apart")
+
+
+def _norm_desc(ref, kind, eps, post, pre, scale):
+    """The descriptor without its strides, and (post_w, post_b, pre_w, pre_b)."""
+    if kind not in _NORM_KINDS:
+        raise ValueError(f"kind must be one of {sorted(_NORM_KINDS)}")
+    if ref.dim() < 1:
+        raise ValueError("x must have a channel axis")
+    C = ref.shape[-1]
+    params = (*(post or (None, None)), *(pre or (None, None)))
+    if len(params) != 4:
+        raise ValueError("post and pre are pairs (weight, bias or None)")
+    if (post is not None and post[0] is None) or (pre is not None and pre[0] is None):
+        raise ValueError("a norm needs its weight")
+    dtype = None
+    for name, t in zip(("scale", "post weight", "post bias", "pre weight", "pre bias"), (scale, *params)):
+        if t is None:
+            continue
+        if tuple(t.shape) != (C,) or (t.stride(0) != 1 and C > 1) or t.dtype != (dtype or t.dtype):
+            raise ValueError(f"{name} must be a contiguous [{C}] tensor of the other parameters' dtype")
+        dtype = t.dtype
+    d = PbaNormDesc(ref.numel() // C if C else 0, C, _dtype_code(ref.dtype), _dtype_code(dtype or ref.dtype),
+                    _NORM_KINDS[kind], float(eps))
+    return d, params
+
+
+def block_norm_forward(x, f=None, gate=None, scale=None, post=None, pre=None, kind="layer", eps=1e-5, h=None, y=None,
+                       stream=None):
+    """The norms before and after a block with its gate and residual scale:
+    h = x + scale * sigmoid(gate) * post(f), y = pre(h).
+
+    x, f, gate [..., C] (bf16 or fp32); f None: h is x.  post and pre are
+    (weight, bias or None) pairs of [C] tensors or None (no norm there); scale
+    [C] or None; the parameters are all bf16 or all fp32.  kind "layer" or
+    "rms".  ``h`` may be x itself.  Returns h and y (None without pre)."""
+    d, params = _norm_desc(x, kind, eps, post, pre, scale)
+    _here(("x", x), ("f", f), ("gate", gate), ("scale", scale), ("post weight", params[0]),
+          ("post bias", params[1]), ("pre weight", params[2]), ("pre bias", params[3]), ("h", h), ("y", y))
+    with _alloc_on(stream):
+        if h is None and f is not None:
+            h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if y is None and pre is not None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    d.x_stride = _row_stride("x", x, x.shape, x.dtype)
+    d.f_stride = _row_stride("f", f, x.shape, x.dtype)
+    d.gate_stride = _row_stride("gate", gate, x.shape, x.dtype)
+    d.h_stride = _row_stride("h", h, x.shape, x.dtype)
+    d.y_stride = _row_stride("y", y, x.shape, x.dtype)
+    _check("block_norm_forward", load_library().block_norm_forward(
+        ctypes.byref(d), _ptr(x), _ptr(f), _ptr(gate), _ptr(scale), *map(_ptr, params), _ptr(h), _ptr(y),
+        _stream(stream)))
+    return (x if f is None else h), (y if pre is not None else None)
+
+
+def block_norm_backward(h, dh, dy, f=None, gate=None, scale=None, post=None, pre=None, kind="layer", eps=1e-5,
+                        stream=None):
+    """Gradients of block_norm_forward.  h is the forward's h (read with pre
+    only), dh and dy the gradients of h and y (dh None: zero; dy with pre).
+    Returns dx, df, dgate (the inputs' dtype) and dscale, dpost_w, dpost_b,
+    dpre_w, dpre_b ([C], fp32); None for what was not given."""
+    ref = h if h is not None else dh
+    d, params = _norm_desc(ref, kind, eps, post, pre, scale)
+    _here(("h", h), ("dh", dh), ("dy", dy), ("f", f), ("gate", gate), ("scale", scale), ("post weight", params[0]),
+          ("post bias", params[1]), ("pre weight", params[2]), ("pre bias", params[3]))
+    shape, dtype, C = ref.shape, ref.dtype, ref.shape[-1]
+    d.h_stride = _row_stride("h", h, shape, dtype)
+    d.f_stride = _row_stride("f", f, shape, dtype)
+    d.gate_stride = _row_stride("gate", gate, shape, dtype)
+    d.dh_stride = _row_stride("dh", dh, shape, dtype)
+    d.dy_stride = _row_stride("dy", dy, shape, dtype)
+    d.dx_stride = d.df_stride = d.dgate_stride = C
+    lib = load_library()
+    need = ctypes.c_int64()
+    _check("block_norm_backward_workspace", lib.block_norm_backward_workspace(ctypes.byref(d), ctypes.byref(need)))
+    with _alloc_on(stream):
+        dx, df, dgate = (torch.empty(shape, dtype=dtype, device=ref.device) if t is not None else None
+                         for t in (ref, f, gate))
+        sums = tuple(torch.empty(C, dtype=torch.float32, device=ref.device) if t is not None else None
+                     for t in (scale, *params))
+        work = torch.empty(need.value, dtype=torch.uint8, device=ref.device)
+    _check("block_norm_backward", lib.block_norm_backward(
+        ctypes.byref(d), _ptr(h), _ptr(f), _ptr(gate), _ptr(scale), *map(_ptr, params), _ptr(dh), _ptr(dy), _ptr(dx),
+        _ptr(df), _ptr(dgate), *map(_ptr, sums), _ptr(work), need.value, _stream(stream)))
+    return (dx, df, dgate, *sums)
 
 
 def pba_last_device_error(stream=None) -> int:

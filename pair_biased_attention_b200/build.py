@@ -2,9 +2,10 @@
 
     python -m pair_biased_attention_b200.build [--verbose]
 
-The library is one translation unit (csrc/pba_api.cu) linked against the
-static CUDA runtime, so it carries no dependency on the runtime that PyTorch
-loads.  Rebuilds only when a source or the header is newer than the .so.
+Every csrc/*.cu is compiled on its own, all of them at once, and linked
+against the static CUDA runtime, so the library carries no dependency on the
+runtime that PyTorch loads.  Rebuilds only when a source or the header is newer
+than the .so.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,7 +25,7 @@ LIB = os.path.join(PKG, "libpba.so")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-std=c++17", "-lineinfo",
-    "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
+    "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
     "-cudart", "static",
 ]
 
@@ -50,11 +52,17 @@ def needs_build() -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB
-    cmd = [_nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC]
-    if verbose:
-        cmd += ["-Xptxas", "-v"]
-    cmd += ["-o", LIB + ".tmp", os.path.join(CSRC, "pba_api.cu")]
-    subprocess.check_call(cmd)
+    cmd = [_nvcc(), *NVCC_FLAGS]
+    with tempfile.TemporaryDirectory(dir=PKG, prefix="_build_") as tmp:
+        objects, running = [], []
+        for src in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
+            objects.append(os.path.join(tmp, os.path.basename(src) + ".o"))
+            running.append(subprocess.Popen(cmd + (["-Xptxas", "-v"] if verbose else []) +
+                                            ["-I", INCLUDE, "-I", CSRC, "-c", "-o", objects[-1], src]))
+        # every compiler is waited for before the folder goes, also when one has failed
+        if any([p.wait() for p in running]):
+            raise RuntimeError("nvcc failed")
+        subprocess.check_call([*cmd, "-shared", "-o", LIB + ".tmp", *objects])
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

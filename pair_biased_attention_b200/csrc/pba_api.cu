@@ -1,18 +1,14 @@
 // pba_api.cu -- the C ABI declared in include/pba.h: argument checks, Tensor
 // Memory Accelerator descriptors and kernel launches.  Every step of the
 // computation runs in the kernels of pba_attn_sm100.cuh and pba_simt.cuh.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-#include <cuda_runtime.h>
-
 #include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <mutex>
 
 #include "pba.h"
+#include "pba_host.cuh"
 #include "pba_attn_sm100.cuh"
 #include "pba_attn_tf32_sm100.cuh"
 #include "pba_proj_sm100.cuh"
@@ -32,89 +28,22 @@ constexpr int kErrTakeSlots = 64;
 __device__ int g_pba_err_taken[kErrTakeSlots];
 __global__ void pba_take_error_kernel(int slot) { g_pba_err_taken[slot] = atomicExch(&g_pba_err, 0); }
 
-namespace {
+using namespace pba_host;
 
+namespace {
 constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;
 std::atomic<uint64_t> g_timeout_ns{kDefaultTimeoutNs};
+}  // namespace
 
-using EncodeTiledFn = PFN_cuTensorMapEncodeTiled_v12000;
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  });
-  return fn;
-}
-
-pba_status check_device() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PBA_ERR_CUDA;
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return PBA_ERR_CUDA;
-  if (major != 10 || minor != 0) return PBA_ERR_UNSUPPORTED;  // built for sm_100a only
-  return PBA_OK;
-}
-
-int *device_error_word() {
+int *pba_host::device_error_word() {
   void *p = nullptr;
   if (cudaGetSymbolAddress(&p, g_pba_err) != cudaSuccess) return nullptr;
   return static_cast<int *>(p);
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+uint64_t pba_host::wait_timeout_ns() { return g_timeout_ns.load(); }
 
-// One-time per-device kernel set-up (the dynamic shared memory limit is a
-// per-device attribute of a kernel): `setup` runs once for each device it is
-// called on, with that device current, and its result is kept per device.
-constexpr int kMaxDevices = 64;
-struct PerDeviceOnce {
-  std::once_flag flag[kMaxDevices];
-  cudaError_t err[kMaxDevices] = {};
-};
-template <typename F>
-cudaError_t once_per_device(PerDeviceOnce &o, F &&setup) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  std::call_once(o.flag[dev], [&] { o.err[dev] = setup(); });
-  return o.err[dev];
-}
-
-constexpr int64_t kMaxI32 = 2147483647;
-
-// 4-D tiled tensor map of bf16 (or, with f32, fp32) elements.  dims/strides
-// innermost first; strides in bytes for dims 1..3.  A dim of extent 1 gets a
-// harmless positive stride (its coordinate is always 0).
-bool make_map(CUtensorMap *map, const void *base, const uint64_t dims[4], const int64_t strides_bytes[3],
-              const uint32_t box[4], CUtensorMapSwizzle swizzle, bool f32 = false) {
-  EncodeTiledFn enc = encode_fn();
-  if (enc == nullptr) return false;
-  cuuint64_t gdim[4] = {dims[0], dims[1], dims[2], dims[3]};
-  cuuint64_t gstride[3];
-  int64_t prev_extent = int64_t(dims[0]) * (f32 ? 4 : 2);
-  for (int i = 0; i < 3; ++i) {
-    int64_t s = strides_bytes[i];
-    if (dims[i + 1] == 1 || s <= 0) s = (prev_extent + 15) / 16 * 16;
-    gstride[i] = cuuint64_t(s);
-    prev_extent = s * int64_t(dims[i + 1]);
-  }
-  cuuint32_t bdim[4] = {box[0], box[1], box[2], box[3]};
-  cuuint32_t estride[4] = {1, 1, 1, 1};
-  CUresult r = enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), gdim, gstride, bdim, estride,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-bool stride_ok_bf16(int64_t s, int64_t extent) { return extent <= 1 || (s > 0 && s % 8 == 0); }
-bool stride_ok_f32(int64_t s, int64_t extent) { return extent <= 1 || (s > 0 && s % 4 == 0); }
+namespace {
 
 // ------------------------------------------------------------ tensor-core path
 struct TcProblem {
