@@ -301,7 +301,7 @@ PBA_API pba_status pba_backward_noalloc(const pba_attn_desc *desc, const void *q
                                         void *dbias, void *stream);
 
 /*
- * relpos_bias_forward -- the learned relative position bias by buckets: the
+ * pba_relpos_bias_forward -- the learned relative position bias by buckets: the
  * bias matrix that pba_forward and pba_partial add to the scores, made from a
  * small table and the tokens' positions (the pages name a pair bias and no
  * rule for one; these are the two rules in common use).
@@ -351,29 +351,29 @@ typedef struct {
  * Rows move as 16-byte words when out (and base) start on 16 bytes and every
  * stride is a multiple of 16 bytes, element by element otherwise.
  */
-PBA_API pba_status relpos_bias_forward(const pba_relpos_desc *desc, const int32_t *q_pos, const int32_t *k_pos,
+PBA_API pba_status pba_relpos_bias_forward(const pba_relpos_desc *desc, const int32_t *q_pos, const int32_t *k_pos,
                                        const int32_t *q_group, const int32_t *k_group, const void *table,
                                        const void *base, void *out, void *stream);
 
 /*
- * relpos_bias_backward -- the gradient of the table:
+ * pba_relpos_bias_backward -- the gradient of the table:
  *   dtable[r][h] = sum over (b, i, j) of row r of dbias[b][h][i][j]
  *   dbias   [B][H][Nq][Nk] device, desc->dtype: pba_backward's, for instance
  *   dtable  [rows][H] float, device, contiguous (rows that no pair has get 0)
  *   workspace  device, 4-byte aligned, at least as many bytes as
- *           relpos_bias_backward_workspace gives; nothing in it is read before
+ *           pba_relpos_bias_backward_workspace gives; nothing in it is read before
  *           it is written, and two calls that may overlap need two of them
  * (The gradient of base is dbias itself.)  Sums are taken in fp32 over at
  * most a few thousand terms each and in 64 bits beyond, always in the same
  * order: the same call gives the same bits.
  */
-PBA_API pba_status relpos_bias_backward_workspace(const pba_relpos_desc *desc, int64_t *bytes);
-PBA_API pba_status relpos_bias_backward(const pba_relpos_desc *desc, const int32_t *q_pos, const int32_t *k_pos,
+PBA_API pba_status pba_relpos_bias_backward_workspace(const pba_relpos_desc *desc, int64_t *bytes);
+PBA_API pba_status pba_relpos_bias_backward(const pba_relpos_desc *desc, const int32_t *q_pos, const int32_t *k_pos,
                                         const int32_t *q_group, const int32_t *k_group, const void *dbias,
                                         float *dtable, void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
- * block_norm_forward -- the norms before and after a block, fused with the
+ * pba_block_norm_forward -- the norms before and after a block, fused with the
  * block's gate and residual scale: what stands between an attention block's
  * output projection and the next block's projections.
  *   u = post(f)                            (post_w NULL: u = f)
@@ -410,12 +410,12 @@ typedef struct {
  *   h [rows][C] device: required with f, may be x itself; without f not written
  *   y [rows][C] device: required with pre_w
  */
-PBA_API pba_status block_norm_forward(const pba_norm_desc *desc, const void *x, const void *f, const void *gate,
+PBA_API pba_status pba_block_norm_forward(const pba_norm_desc *desc, const void *x, const void *f, const void *gate,
                                       const void *scale, const void *post_w, const void *post_b, const void *pre_w,
                                       const void *pre_b, void *h, void *y, void *stream);
 
 /*
- * block_norm_backward -- gradients of block_norm_forward.
+ * pba_block_norm_backward -- gradients of pba_block_norm_forward.
  *   h      the forward's h (its x when f is NULL); read with pre_w only
  *   dh     dL/dh from the residual stream, or NULL (zero; pre_w only)
  *   dy     dL/dy: required with pre_w
@@ -424,10 +424,10 @@ PBA_API pba_status block_norm_forward(const pba_norm_desc *desc, const void *x, 
  *   dscale, dpost_w, dpost_b, dpre_w, dpre_b [C] float, each or NULL: sums over
  *     the rows, taken in fp32 over a thread's rows and in 64 bits beyond, in a
  *     fixed order; not written when their parameter is NULL
- *   workspace  as for relpos_bias_backward, 4-byte aligned
+ *   workspace  as for pba_relpos_bias_backward, 4-byte aligned
  */
-PBA_API pba_status block_norm_backward_workspace(const pba_norm_desc *desc, int64_t *bytes);
-PBA_API pba_status block_norm_backward(const pba_norm_desc *desc, const void *h, const void *f, const void *gate,
+PBA_API pba_status pba_block_norm_backward_workspace(const pba_norm_desc *desc, int64_t *bytes);
+PBA_API pba_status pba_block_norm_backward(const pba_norm_desc *desc, const void *h, const void *f, const void *gate,
                                        const void *scale, const void *post_w, const void *post_b, const void *pre_w,
                                        const void *pre_b, const void *dh, const void *dy, void *dx, void *df,
                                        void *dgate, float *dscale, float *dpost_w, float *dpost_b, float *dpre_w,

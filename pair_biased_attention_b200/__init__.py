@@ -25,7 +25,7 @@ __all__ = [
     "PbaError", "PBA_OK", "PBA_ERR_INVALID_ARG", "PBA_ERR_UNSUPPORTED", "PBA_ERR_CUDA", "PBA_ERR_TIMEOUT",
     "library_path", "load_library", "pba_forward", "pba_partial", "softmax_merge", "tri_attn_forward", "tri_proj_forward", "tri_out_proj_forward", "pwa_forward", "pba_backward",
     "pba_backward_noalloc", "PBA_BWD_NOALLOC_MAX_ROWS",
-    "relpos_bias_forward", "relpos_bias_backward", "block_norm_forward", "block_norm_backward",
+    "pba_relpos_bias_forward", "pba_relpos_bias_backward", "pba_block_norm_forward", "pba_block_norm_backward",
     "pba_last_device_error", "pba_set_wait_timeout_ns", "pba_selftest_wait_timeout", "pba_selftest_exp2",
     "pba_status_string",
 ]
@@ -126,12 +126,12 @@ def load_library() -> ctypes.CDLL:
     i64_p = ctypes.POINTER(i64)
     relpos_p, norm_p = ctypes.POINTER(PbaRelposDesc), ctypes.POINTER(PbaNormDesc)
     for name, args in (
-            ("relpos_bias_forward", [relpos_p] + [_p] * 8),
-            ("relpos_bias_backward_workspace", [relpos_p, i64_p]),
-            ("relpos_bias_backward", [relpos_p] + [_p] * 7 + [i64, _p]),
-            ("block_norm_forward", [norm_p] + [_p] * 11),
-            ("block_norm_backward_workspace", [norm_p, i64_p]),
-            ("block_norm_backward", [norm_p] + [_p] * 19 + [i64, _p])):
+            ("pba_relpos_bias_forward", [relpos_p] + [_p] * 8),
+            ("pba_relpos_bias_backward_workspace", [relpos_p, i64_p]),
+            ("pba_relpos_bias_backward", [relpos_p] + [_p] * 7 + [i64, _p]),
+            ("pba_block_norm_forward", [norm_p] + [_p] * 11),
+            ("pba_block_norm_backward_workspace", [norm_p, i64_p]),
+            ("pba_block_norm_backward", [norm_p] + [_p] * 19 + [i64, _p])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = st
     lib.pba_status_string.argtypes = [st]
@@ -528,7 +528,7 @@ def _matrix_strides(name, t, shape, dtype):
     return t.stride()[:3]
 
 
-def relpos_bias_forward(table, q_pos, k_pos, rule="clip", max_distance=0, q_group=None, k_group=None, base=None,
+def pba_relpos_bias_forward(table, q_pos, k_pos, rule="clip", max_distance=0, q_group=None, k_group=None, base=None,
                         out=None, stream=None):
     """The learned relative position bias: out[b,h,i,j] = table[r, h] (+ base),
     r the bucket of k_pos[b,j] - q_pos[b,i]; the bias argument of pba_forward
@@ -560,15 +560,15 @@ def relpos_bias_forward(table, q_pos, k_pos, rule="clip", max_distance=0, q_grou
     d.out_stride[:] = _matrix_strides("out", out, shape, table.dtype)
     if base is not None:
         d.base_stride[:] = _matrix_strides("base", base, shape, table.dtype)
-    _check("relpos_bias_forward", load_library().relpos_bias_forward(
+    _check("pba_relpos_bias_forward", load_library().pba_relpos_bias_forward(
         ctypes.byref(d), _ptr(q_pos), _ptr(k_pos), _ptr(q_group), _ptr(k_group), _ptr(table), _ptr(base), _ptr(out),
         _stream(stream)))
     return out
 
 
-def relpos_bias_backward(dbias, q_pos, k_pos, rows, rule="clip", max_distance=0, q_group=None, k_group=None,
+def pba_relpos_bias_backward(dbias, q_pos, k_pos, rows, rule="clip", max_distance=0, q_group=None, k_group=None,
                          stream=None):
-    """The gradient of relpos_bias_forward's table: dbias [B,H,Nq,Nk] (bf16 or
+    """The gradient of pba_relpos_bias_forward's table: dbias [B,H,Nq,Nk] (bf16 or
     fp32, pba_backward's for instance) summed over the pairs of each of the
     table's ``rows`` rows.  Position arrays of one sequence are shared by the
     batch of dbias.  Returns dtable [rows, H] (fp32).  The gradient of base is
@@ -581,11 +581,11 @@ def relpos_bias_backward(dbias, q_pos, k_pos, rows, rule="clip", max_distance=0,
     d.out_stride[:] = _matrix_strides("dbias", dbias, (d.B, H, d.Nq, d.Nk), dbias.dtype)
     lib = load_library()
     need = ctypes.c_int64()
-    _check("relpos_bias_backward_workspace", lib.relpos_bias_backward_workspace(ctypes.byref(d), ctypes.byref(need)))
+    _check("pba_relpos_bias_backward_workspace", lib.pba_relpos_bias_backward_workspace(ctypes.byref(d), ctypes.byref(need)))
     with _alloc_on(stream):
         dtable = torch.empty((d.rows, H), dtype=torch.float32, device=dbias.device)
         work = torch.empty(need.value, dtype=torch.uint8, device=dbias.device)
-    _check("relpos_bias_backward", lib.relpos_bias_backward(
+    _check("pba_relpos_bias_backward", lib.pba_relpos_bias_backward(
         ctypes.byref(d), _ptr(q_pos), _ptr(k_pos), _ptr(q_group), _ptr(k_group), _ptr(dbias), _ptr(dtable),
         _ptr(work), need.value, _stream(stream)))
     return dtable
@@ -641,7 +641,7 @@ def _norm_desc(ref, kind, eps, post, pre, scale):
     return d, params
 
 
-def block_norm_forward(x, f=None, gate=None, scale=None, post=None, pre=None, kind="layer", eps=1e-5, h=None, y=None,
+def pba_block_norm_forward(x, f=None, gate=None, scale=None, post=None, pre=None, kind="layer", eps=1e-5, h=None, y=None,
                        stream=None):
     """The norms before and after a block with its gate and residual scale:
     h = x + scale * sigmoid(gate) * post(f), y = pre(h).
@@ -663,15 +663,15 @@ def block_norm_forward(x, f=None, gate=None, scale=None, post=None, pre=None, ki
     d.gate_stride = _row_stride("gate", gate, x.shape, x.dtype)
     d.h_stride = _row_stride("h", h, x.shape, x.dtype)
     d.y_stride = _row_stride("y", y, x.shape, x.dtype)
-    _check("block_norm_forward", load_library().block_norm_forward(
+    _check("pba_block_norm_forward", load_library().pba_block_norm_forward(
         ctypes.byref(d), _ptr(x), _ptr(f), _ptr(gate), _ptr(scale), *map(_ptr, params), _ptr(h), _ptr(y),
         _stream(stream)))
     return (x if f is None else h), (y if pre is not None else None)
 
 
-def block_norm_backward(h, dh, dy, f=None, gate=None, scale=None, post=None, pre=None, kind="layer", eps=1e-5,
+def pba_block_norm_backward(h, dh, dy, f=None, gate=None, scale=None, post=None, pre=None, kind="layer", eps=1e-5,
                         stream=None):
-    """Gradients of block_norm_forward.  h is the forward's h (read with pre
+    """Gradients of pba_block_norm_forward.  h is the forward's h (read with pre
     only), dh and dy the gradients of h and y (dh None: zero; dy with pre).
     Returns dx, df, dgate (the inputs' dtype) and dscale, dpost_w, dpost_b,
     dpre_w, dpre_b ([C], fp32); None for what was not given."""
@@ -688,14 +688,14 @@ def block_norm_backward(h, dh, dy, f=None, gate=None, scale=None, post=None, pre
     d.dx_stride = d.df_stride = d.dgate_stride = C
     lib = load_library()
     need = ctypes.c_int64()
-    _check("block_norm_backward_workspace", lib.block_norm_backward_workspace(ctypes.byref(d), ctypes.byref(need)))
+    _check("pba_block_norm_backward_workspace", lib.pba_block_norm_backward_workspace(ctypes.byref(d), ctypes.byref(need)))
     with _alloc_on(stream):
         dx, df, dgate = (torch.empty(shape, dtype=dtype, device=ref.device) if t is not None else None
                          for t in (ref, f, gate))
         sums = tuple(torch.empty(C, dtype=torch.float32, device=ref.device) if t is not None else None
                      for t in (scale, *params))
         work = torch.empty(need.value, dtype=torch.uint8, device=ref.device)
-    _check("block_norm_backward", lib.block_norm_backward(
+    _check("pba_block_norm_backward", lib.pba_block_norm_backward(
         ctypes.byref(d), _ptr(h), _ptr(f), _ptr(gate), _ptr(scale), *map(_ptr, params), _ptr(dh), _ptr(dy), _ptr(dx),
         _ptr(df), _ptr(dgate), *map(_ptr, sums), _ptr(work), need.value, _stream(stream)))
     return (dx, df, dgate, *sums)

@@ -271,7 +271,7 @@ void fill_norm(pba::NormParams &p, const pba_norm_desc *d, const void *f, const 
 
 extern "C" {
 
-pba_status relpos_bias_forward(const pba_relpos_desc *desc, const int32_t *q_pos, const int32_t *k_pos,
+pba_status pba_relpos_bias_forward(const pba_relpos_desc *desc, const int32_t *q_pos, const int32_t *k_pos,
                                const int32_t *q_group, const int32_t *k_group, const void *table, const void *base,
                                void *out, void *stream_ptr) {
   pba_status s = check_relpos(desc, q_group != nullptr);
@@ -311,7 +311,7 @@ pba_status relpos_bias_forward(const pba_relpos_desc *desc, const int32_t *q_pos
   return e == cudaSuccess ? PBA_OK : PBA_ERR_CUDA;
 }
 
-pba_status relpos_bias_backward_workspace(const pba_relpos_desc *desc, int64_t *bytes) {
+pba_status pba_relpos_bias_backward_workspace(const pba_relpos_desc *desc, int64_t *bytes) {
   // groups take a row of the table, not of the workspace: either reading of `rows` will do
   pba_status s = check_relpos(desc, false);
   if (s != PBA_OK) s = check_relpos(desc, true);
@@ -321,7 +321,7 @@ pba_status relpos_bias_backward_workspace(const pba_relpos_desc *desc, int64_t *
   return PBA_OK;
 }
 
-pba_status relpos_bias_backward(const pba_relpos_desc *desc, const int32_t *q_pos, const int32_t *k_pos,
+pba_status pba_relpos_bias_backward(const pba_relpos_desc *desc, const int32_t *q_pos, const int32_t *k_pos,
                                 const int32_t *q_group, const int32_t *k_group, const void *dbias, float *dtable,
                                 void *workspace, int64_t workspace_bytes, void *stream_ptr) {
   pba_status s = check_relpos(desc, q_group != nullptr);
@@ -363,7 +363,7 @@ pba_status relpos_bias_backward(const pba_relpos_desc *desc, const int32_t *q_po
   return cudaGetLastError() == cudaSuccess ? PBA_OK : PBA_ERR_CUDA;
 }
 
-pba_status block_norm_forward(const pba_norm_desc *desc, const void *x, const void *f, const void *gate,
+pba_status pba_block_norm_forward(const pba_norm_desc *desc, const void *x, const void *f, const void *gate,
                               const void *scale, const void *post_w, const void *post_b, const void *pre_w,
                               const void *pre_b, void *h, void *y, void *stream_ptr) {
   pba_status s = check_norm(desc, f, gate, scale, post_w, post_b, pre_w, pre_b);
@@ -391,14 +391,14 @@ pba_status block_norm_forward(const pba_norm_desc *desc, const void *x, const vo
   return e == cudaSuccess ? PBA_OK : PBA_ERR_CUDA;
 }
 
-pba_status block_norm_backward_workspace(const pba_norm_desc *desc, int64_t *bytes) {
+pba_status pba_block_norm_backward_workspace(const pba_norm_desc *desc, int64_t *bytes) {
   if (desc == nullptr || bytes == nullptr || desc->rows < 0 || desc->C < 1) return PBA_ERR_INVALID_ARG;
   if (desc->C > pba::kNormMaxC) return PBA_ERR_UNSUPPORTED;
   *bytes = desc->rows == 0 ? 0 : norm_grad_blocks(desc->rows, desc->C) * pba::kNormParams * desc->C * 4;
   return PBA_OK;
 }
 
-pba_status block_norm_backward(const pba_norm_desc *desc, const void *h, const void *f, const void *gate,
+pba_status pba_block_norm_backward(const pba_norm_desc *desc, const void *h, const void *f, const void *gate,
                                const void *scale, const void *post_w, const void *post_b, const void *pre_w,
                                const void *pre_b, const void *dh, const void *dy, void *dx, void *df, void *dgate,
                                float *dscale, float *dpost_w, float *dpost_b, float *dpre_w, float *dpre_b,

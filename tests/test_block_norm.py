@@ -1,4 +1,4 @@
-"""block_norm_forward and block_norm_backward: refusals (CPU), and on the GPU
+"""pba_block_norm_forward and pba_block_norm_backward: refusals (CPU), and on the GPU
 every combination of gate, scale and norms against the fp64 definition (its
 gradients by autograd).
 
@@ -59,8 +59,8 @@ def _desc(**kw):
 ])
 def test_rejects_bad_descriptors(lib, kw, expect):
     d = _desc(**kw)
-    assert lib.block_norm_forward(ctypes.byref(d), *([FAKE] * 10), None) == expect
-    assert lib.block_norm_backward(ctypes.byref(d), *([FAKE] * 19), 1 << 40, None) == expect
+    assert lib.pba_block_norm_forward(ctypes.byref(d), *([FAKE] * 10), None) == expect
+    assert lib.pba_block_norm_backward(ctypes.byref(d), *([FAKE] * 19), 1 << 40, None) == expect
 
 
 def test_rejects_combinations_nulls_and_alignment(lib):
@@ -69,9 +69,9 @@ def test_rejects_combinations_nulls_and_alignment(lib):
     names = ["x", "f", "gate", "scale", "post_w", "post_b", "pre_w", "pre_b", "h", "y"]
 
     def fwd(**kw):
-        return lib.block_norm_forward(d, *[kw.get(n, FAKE) for n in names], None)
+        return lib.pba_block_norm_forward(d, *[kw.get(n, FAKE) for n in names], None)
 
-    assert lib.block_norm_forward(None, *([FAKE] * 10), None) == bad
+    assert lib.pba_block_norm_forward(None, *([FAKE] * 10), None) == bad
     assert fwd(x=None) == bad and fwd(h=None) == bad and fwd(y=None) == bad
     assert fwd(f=None) == bad                                       # a gate without a block
     assert fwd(f=None, gate=None, scale=None) == bad                # a norm after no block
@@ -81,13 +81,13 @@ def test_rejects_combinations_nulls_and_alignment(lib):
     for n in names:
         assert fwd(**{n: ctypes.c_void_p(0x10001)}) == bad
     need = ctypes.c_int64()
-    assert lib.block_norm_backward_workspace(d, ctypes.byref(need)) == pba.PBA_OK and need.value > 0
-    assert lib.block_norm_backward_workspace(d, None) == bad
+    assert lib.pba_block_norm_backward_workspace(d, ctypes.byref(need)) == pba.PBA_OK and need.value > 0
+    assert lib.pba_block_norm_backward_workspace(d, None) == bad
     bn = ["h", "f", "gate", "scale", "post_w", "post_b", "pre_w", "pre_b", "dh", "dy", "dx", "df", "dgate", "dscale",
           "dpost_w", "dpost_b", "dpre_w", "dpre_b", "work"]
 
     def bwd(size=need.value, **kw):
-        return lib.block_norm_backward(d, *[kw.get(n, FAKE) for n in bn], size, None)
+        return lib.pba_block_norm_backward(d, *[kw.get(n, FAKE) for n in bn], size, None)
 
     assert bwd(size=need.value - 1) == bad
     for n in ("h", "dy", "dx", "df", "dgate", "work"):
@@ -101,7 +101,7 @@ def test_no_rows_forward(lib):
     d = _desc(rows=0)
     args = [None] * 10
     args[6] = FAKE
-    assert lib.block_norm_forward(ctypes.byref(d), *args, None) == pba.PBA_OK
+    assert lib.pba_block_norm_forward(ctypes.byref(d), *args, None) == pba.PBA_OK
 
 
 # ------------------------------------------------------------------ GPU
@@ -179,7 +179,7 @@ def test_every_combination(cuda_device, parts, kind, dtype):
     for rows, C in ((5, 64), (3, 300)):
         d, dh, dy = _inputs(rows, C, dtype, parts, kind)
         c = _cuda(d)
-        h, y = pba.block_norm_forward(**c, kind=kind)
+        h, y = pba.pba_block_norm_forward(**c, kind=kind)
         assert (y is None) == ("pre" not in parts) and (h is c["x"]) == ("f" not in parts)
         _check_forward(d, kind, 1e-5, h, y)
         _check_backward(d, dh, dy, kind, 1e-5)
@@ -197,7 +197,7 @@ def test_shapes(cuda_device, rows, C, dtype):
     for kind in ("layer", "rms"):
         d, dh, dy = _inputs(rows, C, dtype, parts, kind, seed=C)
         c = _cuda(d)
-        h, y = pba.block_norm_forward(**c, kind=kind, eps=1e-3)
+        h, y = pba.pba_block_norm_forward(**c, kind=kind, eps=1e-3)
         _check_forward(d, kind, 1e-3, h, y)
         _check_backward(d, dh, dy, kind, 1e-3)
 
@@ -209,7 +209,7 @@ def _check_backward(d, dh, dy, kind, eps, h=None):
     h = d["x"] if h is None else h
     c = _cuda(d)
     pre, post = d["pre"] is not None, d["post"] is not None
-    got = pba.block_norm_backward(h.cuda(), dh.cuda(), dy.cuda() if pre else None, c["f"], c["gate"], c["scale"],
+    got = pba.pba_block_norm_backward(h.cuda(), dh.cuda(), dy.cuda() if pre else None, c["f"], c["gate"], c["scale"],
                                   c["post"], c["pre"], kind, eps)
     r = _d64(d)
     h64, t = R.d64(h), R.d64(dh)
@@ -287,7 +287,7 @@ def test_large_mean_keeps_its_variance(cuda_device):
     """Values near 1000 with a spread of 1: the squares are taken around the mean."""
     d, dh, dy = _inputs(6, 128, torch.float32, ("f", "post", "pre"), "layer", seed=9, mean=1000.0)
     d["f"] = d["f"] + 500.0
-    h, y = pba.block_norm_forward(**_cuda(d), kind="layer")
+    h, y = pba.pba_block_norm_forward(**_cuda(d), kind="layer")
     _check_forward(d, "layer", 1e-5, h, y)
 
 
@@ -296,7 +296,7 @@ def test_fp32_parameters_with_bf16_rows(cuda_device):
     for C in (128, 520):
         d, dh, dy = _inputs(6, C, torch.bfloat16, ("f", "post", "gate", "scale", "pre"), "layer", seed=2,
                             param_dtype=torch.float32)
-        h, y = pba.block_norm_forward(**_cuda(d), kind="layer")
+        h, y = pba.pba_block_norm_forward(**_cuda(d), kind="layer")
         _check_forward(d, "layer", 1e-5, h, y)
         _check_backward(d, dh, dy, "layer", 1e-5, h=h.cpu())
 
@@ -308,7 +308,7 @@ def test_zero_and_huge_rows(cuda_device):
     x[2, 3] = 1e15
     for kind in ("layer", "rms"):
         w = torch.ones(96)
-        h, y = pba.block_norm_forward(x.cuda(), pre=(w.cuda(), None), kind=kind)
+        h, y = pba.pba_block_norm_forward(x.cuda(), pre=(w.cuda(), None), kind=kind)
         ref = R.norm(x.double(), (w.double(), None), kind, 1e-5)
         assert torch.isfinite(y).all() and (y[0] == 0).all()
         # row 1 is constant: its exact layer norm is 0, and 18 u 1e18 off the mean is all that rounding can leave
@@ -320,22 +320,22 @@ def test_zero_and_huge_rows(cuda_device):
 def test_row_strides_views_and_in_place(cuda_device):
     d, dh, dy = _inputs(12, 72, torch.bfloat16, ("f", "post", "gate", "pre"), "rms", seed=4)
     c = _cuda(d)
-    h, y = pba.block_norm_forward(**c, kind="rms")
+    h, y = pba.pba_block_norm_forward(**c, kind="rms")
     wide = torch.full((4, 3, 100), 5.0, dtype=torch.bfloat16, device="cuda")
     for at in (8, 5):  # rows on 16 bytes, and not
         view = wide[..., at:at + 72]
         view.copy_(c["x"].view(4, 3, 72))
-        h2, y2 = pba.block_norm_forward(view, c["f"].view(4, 3, 72), c["gate"].view(4, 3, 72), None, c["post"],
+        h2, y2 = pba.pba_block_norm_forward(view, c["f"].view(4, 3, 72), c["gate"].view(4, 3, 72), None, c["post"],
                                         c["pre"], "rms", h=view)
         assert h2 is view and torch.equal(view.reshape(12, 72), h) and torch.equal(y2.reshape(12, 72), y)
         assert (wide[..., :at] == 5).all() and (wide[..., at + 72:] == 5).all()
         wide.fill_(5.0)
     with pytest.raises(ValueError):
-        pba.block_norm_forward(c["x"].view(4, 3, 72).transpose(0, 1), pre=c["pre"])
-    g1 = pba.block_norm_backward(h, dh.cuda(), dy.cuda(), c["f"], c["gate"], None, c["post"], c["pre"], "rms")
+        pba.pba_block_norm_forward(c["x"].view(4, 3, 72).transpose(0, 1), pre=c["pre"])
+    g1 = pba.pba_block_norm_backward(h, dh.cuda(), dy.cuda(), c["f"], c["gate"], None, c["post"], c["pre"], "rms")
     pad = torch.zeros((12, 80), dtype=torch.bfloat16, device="cuda")
     pad[:, :72] = dy.cuda()
-    g2 = pba.block_norm_backward(h, dh.cuda(), pad[:, :72], c["f"], c["gate"], None, c["post"], c["pre"], "rms")
+    g2 = pba.pba_block_norm_backward(h, dh.cuda(), pad[:, :72], c["f"], c["gate"], None, c["post"], c["pre"], "rms")
     assert all((a is None and b is None) or torch.equal(a, b) for a, b in zip(g1, g2))
 
 
@@ -343,13 +343,13 @@ def test_row_strides_views_and_in_place(cuda_device):
 def test_no_residual_gradient_no_rows_and_only_pre(cuda_device):
     d, dh, dy = _inputs(5, 64, torch.float32, ("f", "pre"), "layer", seed=6)
     c = _cuda(d)
-    a = pba.block_norm_backward(c["x"], None, dy.cuda(), c["f"], None, None, None, c["pre"])
-    b = pba.block_norm_backward(c["x"], torch.zeros_like(dh).cuda(), dy.cuda(), c["f"], None, None, None, c["pre"])
+    a = pba.pba_block_norm_backward(c["x"], None, dy.cuda(), c["f"], None, None, None, c["pre"])
+    b = pba.pba_block_norm_backward(c["x"], torch.zeros_like(dh).cuda(), dy.cuda(), c["f"], None, None, None, c["pre"])
     assert all((p is None and q is None) or torch.equal(p, q) for p, q in zip(a, b))
     none = torch.zeros((0, 64), device="cuda")
-    h, y = pba.block_norm_forward(none, none, pre=c["pre"])
+    h, y = pba.pba_block_norm_forward(none, none, pre=c["pre"])
     assert h.shape == (0, 64) and y.shape == (0, 64)
-    g = pba.block_norm_backward(none, none, none, none, None, None, None, c["pre"])
+    g = pba.pba_block_norm_backward(none, none, none, none, None, None, None, c["pre"])
     assert (g[6] == 0).all() and (g[7] == 0).all()
 
 
@@ -360,8 +360,8 @@ def test_repeatable_other_stream_and_captured(cuda_device):
     dh, dy = dh.cuda(), dy.cuda()
 
     def both(stream=None):
-        h, y = pba.block_norm_forward(**c, stream=stream)
-        return (h, y, *pba.block_norm_backward(h, dh, dy, c["f"], c["gate"], c["scale"], c["post"], c["pre"],
+        h, y = pba.pba_block_norm_forward(**c, stream=stream)
+        return (h, y, *pba.pba_block_norm_backward(h, dh, dy, c["f"], c["gate"], c["scale"], c["post"], c["pre"],
                                                stream=stream))
 
     want = both()
@@ -398,8 +398,8 @@ def test_gradient_against_differences(cuda_device):
 
     eps = 1e-5
     diff = (loss(*[t + eps * v for t, v in zip(flat, dirs)]) - loss(*[t - eps * v for t, v in zip(flat, dirs)])) / (2 * eps)
-    h, _ = pba.block_norm_forward(**c)
-    grads = pba.block_norm_backward(h, dh.cuda(), dy.cuda(), c["f"], c["gate"], c["scale"], c["post"], c["pre"])
+    h, _ = pba.pba_block_norm_forward(**c)
+    grads = pba.pba_block_norm_backward(h, dh.cuda(), dy.cuda(), c["f"], c["gate"], c["scale"], c["post"], c["pre"])
     parts = [(R.d64(a) * v) for a, v in zip(grads, dirs)]
     got, mag = sum(p.sum() for p in parts), sum(p.abs().sum() for p in parts)
     assert abs(got - diff) <= 1e-5 * mag

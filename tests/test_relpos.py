@@ -1,4 +1,4 @@
-"""relpos_bias_forward and relpos_bias_backward: refusals (CPU), and on the GPU
+"""pba_relpos_bias_forward and pba_relpos_bias_backward: refusals (CPU), and on the GPU
 the gathered values, the sum with a base and the table's gradient against the
 fp64 reference.
 
@@ -53,8 +53,8 @@ LOG, CAUSAL = pba.PBA_RELPOS_LOG, pba.PBA_RELPOS_LOG_CAUSAL
 ])
 def test_rejects_bad_descriptors(lib, kw, expect):
     d = _desc(**kw)
-    assert lib.relpos_bias_forward(ctypes.byref(d), FAKE, FAKE, None, None, FAKE, None, FAKE, None) == expect
-    assert lib.relpos_bias_backward(ctypes.byref(d), FAKE, FAKE, None, None, FAKE, FAKE, FAKE, 1 << 40,
+    assert lib.pba_relpos_bias_forward(ctypes.byref(d), FAKE, FAKE, None, None, FAKE, None, FAKE, None) == expect
+    assert lib.pba_relpos_bias_backward(ctypes.byref(d), FAKE, FAKE, None, None, FAKE, FAKE, FAKE, 1 << 40,
                                     None) == expect
 
 
@@ -63,27 +63,27 @@ def test_rejects_nulls_alignment_and_small_workspaces(lib):
     p = ctypes.byref(d)
     bad = pba.PBA_ERR_INVALID_ARG
     odd = ctypes.c_void_p(0x10001)
-    assert lib.relpos_bias_forward(None, FAKE, FAKE, None, None, FAKE, None, FAKE, None) == bad
+    assert lib.pba_relpos_bias_forward(None, FAKE, FAKE, None, None, FAKE, None, FAKE, None) == bad
     for i in (0, 1, 4, 6):  # q_pos, k_pos, table, out
         for value in (None, odd):
             args = [FAKE, FAKE, None, None, FAKE, None, FAKE]
             args[i] = value
-            assert lib.relpos_bias_forward(p, *args, None) == bad
+            assert lib.pba_relpos_bias_forward(p, *args, None) == bad
     d.rows = 10  # one group array alone
-    assert lib.relpos_bias_forward(p, FAKE, FAKE, FAKE, None, FAKE, None, FAKE, None) == bad
+    assert lib.pba_relpos_bias_forward(p, FAKE, FAKE, FAKE, None, FAKE, None, FAKE, None) == bad
     d.rows = 9
     need = ctypes.c_int64()
-    assert lib.relpos_bias_backward_workspace(p, ctypes.byref(need)) == pba.PBA_OK and need.value > 0
-    assert lib.relpos_bias_backward_workspace(p, None) == bad
-    assert lib.relpos_bias_backward(p, FAKE, FAKE, None, None, FAKE, FAKE, FAKE, need.value - 1, None) == bad
+    assert lib.pba_relpos_bias_backward_workspace(p, ctypes.byref(need)) == pba.PBA_OK and need.value > 0
+    assert lib.pba_relpos_bias_backward_workspace(p, None) == bad
+    assert lib.pba_relpos_bias_backward(p, FAKE, FAKE, None, None, FAKE, FAKE, FAKE, need.value - 1, None) == bad
     for i in (0, 1, 4, 5, 6):
         args = [FAKE, FAKE, None, None, FAKE, FAKE, FAKE]
         args[i] = None
-        assert lib.relpos_bias_backward(p, *args, need.value, None) == bad
+        assert lib.pba_relpos_bias_backward(p, *args, need.value, None) == bad
 
 
 def test_empty_forward_writes_nothing(lib):
-    assert lib.relpos_bias_forward(ctypes.byref(_desc(Nq=0)), None, None, None, None, None, None, None,
+    assert lib.pba_relpos_bias_forward(ctypes.byref(_desc(Nq=0)), None, None, None, None, None, None, None,
                                    None) == pba.PBA_OK
 
 
@@ -129,16 +129,16 @@ def _make(case, dtype, device, seed=0):
 def test_forward(cuda_device, case, dtype):
     B, H, Nq, Nk, rule, _, far, _, _ = case
     table, (q, k, qg, kg), index, rows, g = _make(case, dtype, cuda_device)
-    out = pba.relpos_bias_forward(table, q, k, rule, far, qg, kg)
+    out = pba.pba_relpos_bias_forward(table, q, k, rule, far, qg, kg)
     assert torch.equal(out.double().cpu(), R.relpos_bias(table, index).expand(B, H, Nq, Nk))
     base = torch.randn((B, H, Nq, Nk), generator=g).to(dtype).to(cuda_device)
     ref = R.relpos_bias(table, index, base)
-    got = pba.relpos_bias_forward(table, q, k, rule, far, qg, kg, base=base)
+    got = pba.pba_relpos_bias_forward(table, q, k, rule, far, qg, kg, base=base)
     half = torch.finfo(dtype).eps / 2
     bound = (half + 2 ** -24) * ref.abs() + (2 ** -24 * (ref - d_base(base)).abs())
     assert ((got.double().cpu() - ref).abs() <= bound).all()
     # the base itself as output
-    again = pba.relpos_bias_forward(table, q, k, rule, far, qg, kg, base=base, out=base)
+    again = pba.pba_relpos_bias_forward(table, q, k, rule, far, qg, kg, base=base, out=base)
     assert again is base and torch.equal(base, got)
 
 
@@ -153,11 +153,11 @@ def test_table_gradient(cuda_device, case, dtype):
     B, H, Nq, Nk, rule, _, far, _, _ = case
     table, (q, k, qg, kg), index, rows, g = _make(case, dtype, cuda_device, seed=1)
     dbias = torch.randn((B, H, Nq, Nk), generator=g).to(dtype).to(cuda_device)
-    got = pba.relpos_bias_backward(dbias, q, k, rows, rule, far, qg, kg)
+    got = pba.pba_relpos_bias_backward(dbias, q, k, rows, rule, far, qg, kg)
     ref, mag = R.relpos_table_grad(dbias, index, rows)
     assert got.dtype == torch.float32 and tuple(got.shape) == (rows, H)
     assert ((got.double().cpu() - ref).abs() <= 525 * 2 ** -24 * mag).all()
-    assert torch.equal(got, pba.relpos_bias_backward(dbias, q, k, rows, rule, far, qg, kg))
+    assert torch.equal(got, pba.pba_relpos_bias_backward(dbias, q, k, rows, rule, far, qg, kg))
 
 
 @pytest.mark.gpu
@@ -170,17 +170,17 @@ def test_long_columns_and_shared_positions(cuda_device):
     index = R.relpos_rows(pos, pos[:Nk], rows, "clip", 0)
     wide = torch.randn((H, B, Nq, Nk + 24), generator=g).to(torch.bfloat16).cuda()
     dbias = wide[..., 8:8 + Nk].transpose(0, 1)
-    got = pba.relpos_bias_backward(dbias, q, k, rows)
+    got = pba.pba_relpos_bias_backward(dbias, q, k, rows)
     ref, mag = R.relpos_table_grad(dbias, index, rows)
     assert ((got.double().cpu() - ref).abs() <= 525 * 2 ** -24 * mag).all()
     odd = wide[..., 3:3 + Nk].transpose(0, 1)  # not on 16 bytes: element by element
     ref, mag = R.relpos_table_grad(odd, index, rows)
-    assert ((pba.relpos_bias_backward(odd, q, k, rows).double().cpu() - ref).abs() <= 525 * 2 ** -24 * mag).all()
+    assert ((pba.pba_relpos_bias_backward(odd, q, k, rows).double().cpu() - ref).abs() <= 525 * 2 ** -24 * mag).all()
     # forward into a window of a larger matrix: what lies around it stays
     table = torch.randn((rows, H), generator=g).to(torch.bfloat16).cuda()
     for at in (8, 3):
         field = torch.full((1, H, Nq, Nk + 24), 7.0, dtype=torch.bfloat16, device="cuda")
-        pba.relpos_bias_forward(table, q, k, out=field[..., at:at + Nk])
+        pba.pba_relpos_bias_forward(table, q, k, out=field[..., at:at + Nk])
         assert torch.equal(field[..., at:at + Nk].double().cpu(), R.relpos_bias(table, index))
         assert (field[..., :at] == 7).all() and (field[..., at + Nk:] == 7).all()
 
@@ -192,11 +192,11 @@ def test_positions_at_the_ends_of_int32(cuda_device):
     for rule, rows, far in (("clip", 5, 0), ("log", 32, 128), ("log_causal", 16, 1 << 30)):
         table = torch.randn((rows, 2), generator=torch.Generator().manual_seed(1)).cuda()
         index = R.relpos_rows(pos, pos, rows, rule, far)
-        out = pba.relpos_bias_forward(table, pos.cuda(), pos.cuda(), rule, far)
+        out = pba.pba_relpos_bias_forward(table, pos.cuda(), pos.cuda(), rule, far)
         assert torch.equal(out.double().cpu(), R.relpos_bias(table, index))
         dbias = torch.randn((1, 2, 7, 7), generator=torch.Generator().manual_seed(2)).cuda()
         ref, mag = R.relpos_table_grad(dbias, index, rows)
-        got = pba.relpos_bias_backward(dbias, pos.cuda(), pos.cuda(), rows, rule, far).double().cpu()
+        got = pba.pba_relpos_bias_backward(dbias, pos.cuda(), pos.cuda(), rows, rule, far).double().cpu()
         assert ((got - ref).abs() <= 525 * 2 ** -24 * mag).all()
 
 
@@ -208,7 +208,7 @@ def test_every_border_of_the_logarithmic_rule(cuda_device):
                      for o in (-1, 0, 1) if d + o >= 0})
         k = torch.tensor(ds, dtype=torch.int32)
         table = torch.arange(rows, dtype=torch.float32)[:, None].contiguous().cuda()
-        out = pba.relpos_bias_forward(table, torch.zeros(1, dtype=torch.int32, device="cuda"), (-k).cuda(), "log",
+        out = pba.pba_relpos_bias_forward(table, torch.zeros(1, dtype=torch.int32, device="cuda"), (-k).cuda(), "log",
                                       far)
         want = torch.tensor([R.log_row(d, side, far) for d in ds]).double()
         assert torch.equal(out.reshape(-1).double().cpu(), want)
@@ -225,8 +225,8 @@ def test_empty_gradient_is_zero(cuda_device):
     some = torch.zeros((4,), dtype=torch.int32, device="cuda")
     for q, k in ((none, some), (some, none)):
         dbias = torch.zeros((1, 2, q.numel(), k.numel()), device="cuda")
-        assert (pba.relpos_bias_backward(dbias, q, k, 5) == 0).all()
-        assert pba.relpos_bias_forward(torch.zeros((5, 2), device="cuda"), q, k).numel() == 0
+        assert (pba.pba_relpos_bias_backward(dbias, q, k, 5) == 0).all()
+        assert pba.pba_relpos_bias_forward(torch.zeros((5, 2), device="cuda"), q, k).numel() == 0
 
 
 @pytest.mark.gpu
@@ -235,20 +235,20 @@ def test_other_stream_and_captured(cuda_device):
     B, H, Nq, Nk, rule, _, far, _, _ = case
     table, (q, k, qg, kg), index, rows, g = _make(case, torch.bfloat16, cuda_device, seed=3)
     dbias = torch.randn((B, H, Nq, Nk), generator=g).cuda()
-    want = pba.relpos_bias_forward(table, q, k, rule, far, qg, kg), pba.relpos_bias_backward(dbias, q, k, rows, rule,
+    want = pba.pba_relpos_bias_forward(table, q, k, rule, far, qg, kg), pba.pba_relpos_bias_backward(dbias, q, k, rows, rule,
                                                                                              far, qg, kg)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    got = (pba.relpos_bias_forward(table, q, k, rule, far, qg, kg, stream=side),
-           pba.relpos_bias_backward(dbias, q, k, rows, rule, far, qg, kg, stream=side))
+    got = (pba.pba_relpos_bias_forward(table, q, k, rule, far, qg, kg, stream=side),
+           pba.pba_relpos_bias_backward(dbias, q, k, rows, rule, far, qg, kg, stream=side))
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     graphs = []
     for _ in range(2):  # two graphs, replayed in turn
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            r = (pba.relpos_bias_forward(table, q, k, rule, far, qg, kg),
-                 pba.relpos_bias_backward(dbias, q, k, rows, rule, far, qg, kg))
+            r = (pba.pba_relpos_bias_forward(table, q, k, rule, far, qg, kg),
+                 pba.pba_relpos_bias_backward(dbias, q, k, rows, rule, far, qg, kg))
         graphs.append((graph, r))
     for graph, r in graphs + graphs:
         graph.replay()
@@ -262,18 +262,18 @@ def test_binding_refuses(cuda_device):
     table = torch.zeros((5, 2), device="cuda")
     pos = torch.zeros((4,), dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError):
-        pba.relpos_bias_forward(table, pos.long(), pos)
+        pba.pba_relpos_bias_forward(table, pos.long(), pos)
     with pytest.raises(ValueError):
-        pba.relpos_bias_forward(table, pos.cpu(), pos)
+        pba.pba_relpos_bias_forward(table, pos.cpu(), pos)
     with pytest.raises(ValueError):
-        pba.relpos_bias_forward(table, pos, pos, "nearest")
+        pba.pba_relpos_bias_forward(table, pos, pos, "nearest")
     with pytest.raises(ValueError):
-        pba.relpos_bias_forward(table, pos, pos, q_group=pos)
+        pba.pba_relpos_bias_forward(table, pos, pos, q_group=pos)
     with pytest.raises(ValueError):
-        pba.relpos_bias_forward(table, pos, pos, base=torch.zeros((1, 2, 4, 5), device="cuda"))
+        pba.pba_relpos_bias_forward(table, pos, pos, base=torch.zeros((1, 2, 4, 5), device="cuda"))
     with pytest.raises(ValueError):
-        pba.relpos_bias_forward(table.half(), pos, pos)
+        pba.pba_relpos_bias_forward(table.half(), pos, pos)
     with pytest.raises(ValueError):
-        pba.relpos_bias_backward(torch.zeros((2, 2, 4, 4), device="cuda"), pos.expand(3, 4), pos, 5)
+        pba.pba_relpos_bias_backward(torch.zeros((2, 2, 4, 4), device="cuda"), pos.expand(3, 4), pos, 5)
     with pytest.raises(pba.PbaError):
-        pba.relpos_bias_forward(table[:4].contiguous(), pos, pos)
+        pba.pba_relpos_bias_forward(table[:4].contiguous(), pos, pos)
