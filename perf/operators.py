@@ -306,23 +306,23 @@ def run(s):
 
         case = s["case"]
         if op == "relpos":
-            return pba.relpos_bias_forward(s["table"], s["q_pos"], s["k_pos"], case["rule"], case["distance"],
-                                           q_group=s["q_group"], k_group=s["k_group"], base=s["base"])
+            return pba.pba_relpos_bias_forward(s["table"], s["q_pos"], s["k_pos"], case["rule"], case["distance"],
+                                               q_group=s["q_group"], k_group=s["k_group"], base=s["base"])
         if op == "relpos_grad":
-            return pba.relpos_bias_backward(s["dbias"], s["q_pos"], s["k_pos"],
-                                            case["buckets"] + int(case["groups"]), case["rule"], case["distance"],
-                                            q_group=s["q_group"], k_group=s["k_group"])
+            return pba.pba_relpos_bias_backward(s["dbias"], s["q_pos"], s["k_pos"],
+                                                case["buckets"] + int(case["groups"]), case["rule"],
+                                                case["distance"], q_group=s["q_group"], k_group=s["k_group"])
         if op == "norm":
-            return pba.block_norm_forward(s["x"], s["f"], s["gate"], s["scale"], s["post"], s["pre"], case["kind"],
-                                          EPS)
+            return pba.pba_block_norm_forward(s["x"], s["f"], s["gate"], s["scale"], s["post"], s["pre"],
+                                              case["kind"], EPS)
         if op == "norm_grad":
-            return pba.block_norm_backward(s["h"], s["dh"], s["dy"], s["f"], s["gate"], s["scale"], s["post"],
-                                           s["pre"], case["kind"], EPS)
-        out, lse = pba.cross_attn_forward(s["q"], s["k"], s["v"], s["k_len"], s["key_mask"])
+            return pba.pba_block_norm_backward(s["h"], s["dh"], s["dy"], s["f"], s["gate"], s["scale"], s["post"],
+                                               s["pre"], case["kind"], EPS)
+        out, lse = pba.pba_cross_attn_forward(s["q"], s["k"], s["v"], s["k_len"], s["key_mask"])
         if op == "cross":
             return out, lse
-        return out, lse, *pba.cross_attn_backward(s["q"], s["k"], s["v"], out, lse, s["dout"], s["k_len"],
-                                                  s["key_mask"])
+        return out, lse, *pba.pba_cross_attn_backward(s["q"], s["k"], s["v"], out, lse, s["dout"], s["k_len"],
+                                                      s["key_mask"])
     if op == "relpos":
         return _plain_relpos(s)
     if op == "relpos_grad":
