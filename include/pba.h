@@ -433,6 +433,68 @@ PBA_API pba_status pba_block_norm_backward(const pba_norm_desc *desc, const void
                                        void *dgate, float *dscale, float *dpost_w, float *dpost_b, float *dpre_w,
                                        float *dpre_b, void *workspace, int64_t workspace_bytes, void *stream);
 
+/*
+ * pba_cross_attn_forward -- cross attention: the queries of one sequence
+ * against an encoder's keys and values of another length, without a pair bias
+ * (with one, pba_forward takes Nq and Nk of their own).  bf16.
+ *   O_i = sum_j softmax_j( tau q_i.k_j ) v_j  over the keys j < k_len[b] with
+ *         key_mask[b][j] != 0
+ * Heads may be grouped: head h reads key head h / (H / Hkv).
+ *   B, H, Hkv, Nq, Nk, D   H a multiple of Hkv, H <= 65535; Nq, Nk >= 0; D 32,
+ *                  64 or 128
+ *   dtype          PBA_BF16 (of q, k, v, out, dout and the gradients)
+ *   softmax_scale  tau; 0 selects 1/sqrt(D)
+ *   *_stride       (b, h, n) in elements, feature stride 1.  q, k, v, dout:
+ *                  positive multiples of 8 where the axis is longer than 1;
+ *                  out: multiples of 8; lse: any
+ *   mask_stride_b  row stride of key_mask [B][Nk] (key stride 1)
+ * Few query rows per key head (a decoder's new tokens) run on kernels that
+ * split the keys over the card; the result does not depend on the choice
+ * beyond rounding, and every call gives the same bits again.
+ */
+typedef struct {
+  int64_t B, H, Hkv, Nq, Nk, D;
+  int32_t dtype;
+  float softmax_scale;
+  int64_t q_stride[3];
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int64_t mask_stride_b;
+  int64_t out_stride[3];
+  int64_t lse_stride[3];
+  int64_t dout_stride[3];
+} pba_cross_desc;
+
+/*
+ *   q [B][H][Nq][D], k, v [B][Hkv][Nk][D]  bf16, device, 16-byte aligned
+ *   k_len [B] int32, device, or NULL (all Nk): keys behind a sequence's length
+ *         do not count (a length outside [0, Nk] is taken as the nearer end)
+ *   key_mask [B][Nk] uint8, device, or NULL
+ *   out [B][H][Nq][D] bf16, device, 16-byte aligned; lse [B][H][Nq] float or NULL
+ * What keys and values that do not count hold is never used, NaN included.  A
+ * query without any key gets out = 0, lse = -inf.
+ */
+PBA_API pba_status pba_cross_attn_forward(const pba_cross_desc *desc, const void *q, const void *k, const void *v,
+                                          const int32_t *k_len, const uint8_t *key_mask, void *out, float *lse,
+                                          void *stream);
+
+/*
+ * pba_cross_attn_backward -- gradients of pba_cross_attn_forward from its out
+ * and lse and dout = dL/dout (same arguments otherwise):
+ *   dS_ij = P_ij (dout_i . v_j - delta_i),  delta_i = sum_d dout_id out_id
+ *   dq_i = tau sum_j dS_ij k_j   dk_j = tau sum dS_ij q_i   dv_j = sum P_ij dout_i
+ * the last two over the queries of all heads that share the key head.
+ *   dq [B][H][Nq][D], dk, dv [B][Hkv][Nk][D]  bf16, device, contiguous, 16-byte
+ *         aligned; rows of keys that do not count are written as 0
+ *   delta [B][H][Nq] float, device: the caller's buffer for the row sums
+ * Sums are fp32 and rounded once (P and dS enter the products as bf16), in a
+ * fixed order: the same call gives the same bits.
+ */
+PBA_API pba_status pba_cross_attn_backward(const pba_cross_desc *desc, const void *q, const void *k, const void *v,
+                                           const int32_t *k_len, const uint8_t *key_mask, const void *out,
+                                           const float *lse, const void *dout, void *dq, void *dk, void *dv,
+                                           float *delta, void *stream);
+
 /* Human-readable name of a status code (static storage). */
 PBA_API const char *pba_status_string(pba_status status);
 

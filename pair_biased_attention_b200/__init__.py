@@ -26,6 +26,7 @@ __all__ = [
     "library_path", "load_library", "pba_forward", "pba_partial", "softmax_merge", "tri_attn_forward", "tri_proj_forward", "tri_out_proj_forward", "pwa_forward", "pba_backward",
     "pba_backward_noalloc", "PBA_BWD_NOALLOC_MAX_ROWS",
     "pba_relpos_bias_forward", "pba_relpos_bias_backward", "pba_block_norm_forward", "pba_block_norm_backward",
+    "pba_cross_attn_forward", "pba_cross_attn_backward",
     "pba_last_device_error", "pba_set_wait_timeout_ns", "pba_selftest_wait_timeout", "pba_selftest_exp2",
     "pba_status_string",
 ]
@@ -80,6 +81,17 @@ class PbaNormDesc(ctypes.Structure):
     ]
 
 
+class PbaCrossDesc(ctypes.Structure):
+    """Mirror of pba_cross_desc."""
+    _fields_ = [
+        ("B", ctypes.c_int64), ("H", ctypes.c_int64), ("Hkv", ctypes.c_int64), ("Nq", ctypes.c_int64),
+        ("Nk", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+        ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+        ("mask_stride_b", ctypes.c_int64), ("out_stride", ctypes.c_int64 * 3), ("lse_stride", ctypes.c_int64 * 3),
+        ("dout_stride", ctypes.c_int64 * 3),
+    ]
+
+
 class PbaError(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn} returned {pba_status_string(status)} ({status})")
@@ -124,14 +136,16 @@ def load_library() -> ctypes.CDLL:
     lib.pba_backward_noalloc.restype = st
     i64 = ctypes.c_int64
     i64_p = ctypes.POINTER(i64)
-    relpos_p, norm_p = ctypes.POINTER(PbaRelposDesc), ctypes.POINTER(PbaNormDesc)
+    relpos_p, norm_p, cross_p = (ctypes.POINTER(t) for t in (PbaRelposDesc, PbaNormDesc, PbaCrossDesc))
     for name, args in (
             ("pba_relpos_bias_forward", [relpos_p] + [_p] * 8),
             ("pba_relpos_bias_backward_workspace", [relpos_p, i64_p]),
             ("pba_relpos_bias_backward", [relpos_p] + [_p] * 7 + [i64, _p]),
             ("pba_block_norm_forward", [norm_p] + [_p] * 11),
             ("pba_block_norm_backward_workspace", [norm_p, i64_p]),
-            ("pba_block_norm_backward", [norm_p] + [_p] * 19 + [i64, _p])):
+            ("pba_block_norm_backward", [norm_p] + [_p] * 19 + [i64, _p]),
+            ("pba_cross_attn_forward", [cross_p] + [_p] * 8),
+            ("pba_cross_attn_backward", [cross_p] + [_p] * 13)):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = st
     lib.pba_status_string.argtypes = [st]
@@ -699,6 +713,78 @@ def pba_block_norm_backward(h, dh, dy, f=None, gate=None, scale=None, post=None,
         ctypes.byref(d), _ptr(h), _ptr(f), _ptr(gate), _ptr(scale), *map(_ptr, params), _ptr(dh), _ptr(dy), _ptr(dx),
         _ptr(df), _ptr(dgate), *map(_ptr, sums), _ptr(work), need.value, _stream(stream)))
     return (dx, df, dgate, *sums)
+
+
+def _cross_desc(q, k, v, k_len, key_mask, softmax_scale) -> PbaCrossDesc:
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be [B,H,Nq,D], k and v [B,Hkv,Nk,D]")
+    B, H, Nq, D = q.shape
+    Hkv, Nk = k.shape[1:3]
+    if tuple(k.shape) != (B, Hkv, Nk, D) or v.shape != k.shape:
+        raise ValueError("k and v must be [B,Hkv,Nk,D] matching q")
+    d = PbaCrossDesc(B, H, Hkv, Nq, Nk, D, _dtype_code(q.dtype), float(softmax_scale or 0.0))
+    for name, t, stride in (("q", q, d.q_stride), ("k", k, d.k_stride), ("v", v, d.v_stride)):
+        if t.dtype != q.dtype:
+            raise ValueError(f"{name} must be {q.dtype}, got {t.dtype}")
+        stride[:] = _bhn(name, t)
+    if k_len is not None and (k_len.dtype != torch.int32 or tuple(k_len.shape) != (B,) or not k_len.is_contiguous()):
+        raise ValueError(f"k_len must be a contiguous [{B}] int32 tensor")
+    if key_mask is not None:
+        if key_mask.dtype != torch.uint8 or tuple(key_mask.shape) != (B, Nk) or \
+                (key_mask.stride(1) != 1 and Nk > 1):
+            raise ValueError(f"key_mask must be [{B}, {Nk}] uint8, contiguous along keys")
+        d.mask_stride_b = key_mask.stride(0)
+    return d
+
+
+def pba_cross_attn_forward(q, k, v, k_len=None, key_mask=None, out=None, lse=None, softmax_scale=None,
+                           return_lse=True, stream=None):
+    """Cross attention to an encoder's states of another length, bf16, without
+    a pair bias: q [B,H,Nq,D], k and v [B,Hkv,Nk,D] (D 32, 64 or 128; head h
+    reads key head h // (H // Hkv)).  k_len [B] int32: keys of each sequence;
+    key_mask [B,Nk] uint8 (1 = key takes part); either may be None.  Returns
+    out [B,H,Nq,D] and lse [B,H,Nq] (fp32); queries without a key get 0 and
+    -inf."""
+    _here(("q", q), ("k", k), ("v", v), ("k_len", k_len), ("key_mask", key_mask), ("out", out), ("lse", lse))
+    d = _cross_desc(q, k, v, k_len, key_mask, softmax_scale)
+    with _alloc_on(stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None and return_lse:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError(f"out must be a {tuple(q.shape)} {q.dtype} tensor")
+    d.out_stride[:] = _bhn("out", out)
+    if lse is not None:
+        if lse.shape != q.shape[:3] or lse.dtype != torch.float32:
+            raise ValueError(f"lse must be a {tuple(q.shape[:3])} float32 tensor")
+        d.lse_stride[:] = lse.stride()
+    _check("pba_cross_attn_forward", load_library().pba_cross_attn_forward(
+        ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(k_len), _ptr(key_mask), _ptr(out), _ptr(lse),
+        _stream(stream)))
+    return out, lse
+
+
+def pba_cross_attn_backward(q, k, v, out, lse, dout, k_len=None, key_mask=None, softmax_scale=None, stream=None):
+    """Gradients of pba_cross_attn_forward from its out and lse: dq [B,H,Nq,D],
+    dk and dv [B,Hkv,Nk,D] (bf16, contiguous).  The other arguments as for the
+    forward."""
+    _here(("q", q), ("k", k), ("v", v), ("out", out), ("lse", lse), ("dout", dout), ("k_len", k_len),
+          ("key_mask", key_mask))
+    d = _cross_desc(q, k, v, k_len, key_mask, softmax_scale)
+    for name, t, shape, dtype, stride in (("out", out, q.shape, q.dtype, d.out_stride),
+                                          ("dout", dout, q.shape, q.dtype, d.dout_stride),
+                                          ("lse", lse, q.shape[:3], torch.float32, d.lse_stride)):
+        if t.shape != shape or t.dtype != dtype:
+            raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor")
+        stride[:] = _bhn(name, t, t.dim())
+    with _alloc_on(stream):
+        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+        delta = torch.empty(lse.shape, dtype=torch.float32, device=q.device)
+    _check("pba_cross_attn_backward", load_library().pba_cross_attn_backward(
+        ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(k_len), _ptr(key_mask), _ptr(out), _ptr(lse), _ptr(dout),
+        _ptr(dq), _ptr(dk), _ptr(dv), _ptr(delta), _stream(stream)))
+    return dq, dk, dv
 
 
 def pba_last_device_error(stream=None) -> int:

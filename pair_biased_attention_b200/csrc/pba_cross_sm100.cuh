@@ -1,0 +1,574 @@
+// pba_cross_sm100.cuh -- cross attention on the sm_100a tensor cores: queries
+// of one sequence against an encoder's keys and values of another length,
+// without a pair bias.
+//
+//     O_i = sum_j softmax_j( tau q_i.k_j ) v_j   over the keys j < k_len[b]
+//                                                with key_mask[b][j] != 0
+//
+// Heads are grouped: head h reads the keys and values of head h / (H / Hkv).
+// Beside pair-biased attention this is the second attention of a layer that
+// conditions one sequence on another.
+//
+// Persistent: one CTA per SM walks the units u = blockIdx.x, + gridDim.x, ...;
+// a unit is two 128-row query tiles of one (b, h), its keys come 128 at a time.
+//   warps 0-3   softmax warpgroup of query tile 0 (thread t owns row t)
+//   warps 4-7   softmax warpgroup of query tile 1
+//   warp 8      TMA producer of Q (per unit) and of K and V
+//   warp 9      allocates Tensor Memory and issues every tcgen05.mma
+//   warp 10     zeroes the V rows of keys that do not take part
+// Without a bias nothing streams from HBM while a unit runs (K and V of a head
+// stay in L2), so what bounds the kernel is the exponentials: per key tile and
+// SM 2 x 128 x 128 of them, 2048 cycles of the exp2 unit, against 1050 cycles
+// of products at D = 64.
+//
+// Tensor Memory (512 columns x 128 lanes of fp32), D <= 64:
+//   [0,128) S0  [128,256) S1  [256,320) P0  [320,384) P1  [384,+D) O0  [448,+D) O1
+// so that the next score tile is computed while the softmax warps work on this
+// one.  D = 128: O0 and O1 take [256,512) and P lies over its own S, whose next
+// tile then waits for the product with V; the two query tiles alternate.
+//
+// A masked key's score is replaced by -inf and its V row by zeros, so that
+// what lies there, NaN included, does not matter.
+#pragma once
+
+#include <cuda.h>
+
+#include "pba_ptx.cuh"
+
+namespace pba {
+
+constexpr int kXTile = 128;      // query rows and keys per tile
+constexpr int kXQTiles = 2;      // query tiles per unit
+constexpr int kXThreads = 384;
+constexpr int kXWarpProducer = 8;
+constexpr int kXWarpMma = 9;
+constexpr int kXWarpFix = 10;
+constexpr int kXRegsSoftmax = 224;
+constexpr int kXRegsOther = 56;
+constexpr int kXRegSplitTotal = 256 * kXRegsSoftmax + 128 * kXRegsOther;
+constexpr float kXLog2e = 1.4426950408889634f;
+constexpr float kXLn2 = 0.6931471805599453f;
+
+// Shared-memory tile of [128][D] bf16 as TMA and the tensor core see it: one
+// or two slabs of at most 64 features (128 bytes) per row.
+template <int D>
+struct XTileLayout {
+  static_assert(D == 32 || D == 64 || D == 128, "head dimension");
+  static constexpr int kSlabs = D == 128 ? 2 : 1;
+  static constexpr int kSlabCols = D / kSlabs;
+  static constexpr int kRowBytes = kSlabCols * 2;
+  static constexpr int kSwizzleMode = kRowBytes == 128 ? 2 : 4;  // 128- / 64-byte swizzle
+  static constexpr int kAtomBytes = 8 * kRowBytes;
+  static constexpr int kSlabBytes = kXTile * kRowBytes;
+  static constexpr int kBytes = kSlabs * kSlabBytes;
+  static constexpr uint32_t kDescHi = smem_desc_hi(kAtomBytes, kSwizzleMode);
+  // address step (16-byte units) of the K = 16 slice kk of a K-major operand
+  static constexpr __host__ __device__ uint32_t k_step(int kk) {
+    return uint32_t((kk / (kSlabCols / 16)) * kSlabBytes + (kk % (kSlabCols / 16)) * 32) / 16;
+  }
+  // and of an MN-major one (16 rows down)
+  static constexpr __host__ __device__ uint32_t mn_step(int kk) { return uint32_t(kk * 16 * kRowBytes) / 16; }
+  // zeroes row r of a tile at `tile`; `lane` of 32 threads takes a share
+  static __device__ __forceinline__ void zero_row(uint8_t *tile, int r, int lane) {
+    // a row is the same 16-byte chunks whatever their swizzled order
+    if (lane < kSlabs * (kRowBytes / 16)) {
+      const int slab = lane / (kRowBytes / 16), chunk = lane % (kRowBytes / 16);
+      *reinterpret_cast<uint4 *>(tile + slab * kSlabBytes + r * kRowBytes + chunk * 16) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  static __device__ __forceinline__ void load(void *dst, const void *map, uint64_t *bar, int row, int h, int b,
+                                              uint64_t policy) {
+#pragma unroll
+    for (int s = 0; s < kSlabs; ++s)
+      tma_load_4d(static_cast<uint8_t *>(dst) + s * kSlabBytes, map, bar, s * kSlabCols, row, h, b, policy);
+  }
+};
+
+struct CrossParams {
+  CUtensorMap tm_q, tm_k, tm_v;  // (D, n, heads, B) bf16, box {min(D, 64), 128, 1, 1}
+  int32_t B, H, group, Nq, Nk;   // group = H / Hkv
+  int32_t n_qblocks, n_units;
+  float tau;
+  const int32_t *k_len;          // [B] or null
+  const uint8_t *mask;           // [B][Nk] or null
+  int64_t mask_sb;
+  int32_t mask_vec4;             // mask rows readable as aligned 4-byte words
+  uint16_t *out;
+  int64_t out_sb, out_sh, out_sn;
+  float *lse;
+  int64_t lse_sb, lse_sh, lse_sn;
+  int *err;
+  uint64_t timeout_ns;
+};
+
+// Keys of batch b that may take part: k_len, kept inside [0, Nk].
+__device__ __forceinline__ int cross_keys(const int32_t *k_len, int b, int Nk) {
+  return k_len == nullptr ? Nk : min(max(__ldg(k_len + b), 0), Nk);
+}
+
+// Which of the 128 keys of the tile at key0 take part, asked by a whole warp:
+// bit l of word e is key 4 l + e.  `bytes` is what cross_mask_bytes read.
+__device__ __forceinline__ uint32_t cross_mask_bytes(const uint8_t *row, bool vec4, int key0, int keys, int lane) {
+  const int k = key0 + 4 * lane;
+  if (vec4 && k + 3 < keys) return __ldg(reinterpret_cast<const uint32_t *>(row + k));
+  uint32_t v = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (k + e < keys) v |= uint32_t(__ldg(row + k + e)) << (8 * e);
+  return v;
+}
+struct KeepWords {
+  uint32_t w[4];
+  __device__ __forceinline__ bool all() const { return (w[0] & w[1] & w[2] & w[3]) == 0xFFFFFFFFu; }
+  __device__ __forceinline__ bool has(int key) const { return (w[key & 3] >> (key >> 2)) & 1u; }
+};
+__device__ __forceinline__ KeepWords cross_keep(uint32_t bytes) {
+  KeepWords k;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) k.w[e] = __ballot_sync(0xffffffffu, ((bytes >> (8 * e)) & 0xFFu) != 0);
+  return k;
+}
+
+template <int D>
+struct CrossLayout {
+  using T = XTileLayout<D>;
+  static constexpr bool kAlias = D == 128;  // P over S
+  static constexpr int kKVStages = D == 128 ? 2 : 4;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kXQTiles * T::kBytes;
+  static constexpr int kOffV = kOffK + kKVStages * T::kBytes;
+  static constexpr int kOffBar = kOffV + kKVStages * T::kBytes;
+  static constexpr int kBarQFull = 0;
+  static constexpr int kBarQEmpty = 1;
+  static constexpr int kBarKFull = 2;
+  static constexpr int kBarVFull = kBarKFull + kKVStages;
+  static constexpr int kBarKEmpty = kBarVFull + kKVStages;
+  static constexpr int kBarVEmpty = kBarKEmpty + kKVStages;
+  static constexpr int kBarVReady = kBarVEmpty + kKVStages;  // masked rows zeroed
+  static constexpr int kBarSFull = kBarVReady + kKVStages;   // [w]
+  static constexpr int kBarSFree = kBarSFull + kXQTiles;
+  static constexpr int kBarPFull = kBarSFree + kXQTiles;
+  static constexpr int kBarODone = kBarPFull + kXQTiles;
+  static constexpr int kBarOFree = kBarODone + kXQTiles;
+  static constexpr int kBarDrain = kBarOFree + kXQTiles;
+  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
+  static constexpr int kOffAbort = kOffTmemSlot + 4;
+  static constexpr int kBytes = kOffAbort + 4;
+  static constexpr int kSmemAlloc = kBytes + 1024;  // room to align the base to 1024
+  static_assert(kSmemAlloc <= 232448, "shared memory budget");
+  static constexpr __host__ __device__ uint32_t col_s(int w) { return uint32_t(w * kXTile); }
+  static constexpr __host__ __device__ uint32_t col_p(int w) { return kAlias ? col_s(w) : 256u + w * 64; }
+  static constexpr __host__ __device__ uint32_t col_o(int w) { return kAlias ? 256u + w * 128 : 384u + w * 64; }
+};
+
+struct CrossUnit {
+  int b, h, q0, keys, nt;
+};
+__device__ __forceinline__ CrossUnit cross_unit(const CrossParams &p, int u) {
+  const int qblk = u % p.n_qblocks, bh = u / p.n_qblocks;
+  CrossUnit x;
+  x.b = bh / p.H;
+  x.h = bh - x.b * p.H;
+  x.q0 = qblk * (kXQTiles * kXTile);
+  x.keys = cross_keys(p.k_len, x.b, p.Nk);
+  x.nt = (x.keys + kXTile - 1) / kXTile;
+  return x;
+}
+
+// kMasked: a key mask is given.  Key lengths need no variant: they end the
+// loop over the tiles, and the last tile's tail is cut off by its length.
+template <int D, bool kMasked>
+__global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __grid_constant__ CrossParams p) {
+  using L = CrossLayout<D>;
+  using T = typename L::T;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffTmemSlot);
+  int *abort_flag = reinterpret_cast<int *>(smem + L::kOffAbort);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int u_begin = blockIdx.x, u_step = gridDim.x;
+  // V rows past the keys' end are zeros by the tile load itself when the
+  // tensor ends there; otherwise warp 10 looks at every tile
+  const bool fix = kMasked || p.k_len != nullptr;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars[L::kBarQFull], 1);
+    mbar_init(&bars[L::kBarQEmpty], 1);
+    for (int s = 0; s < L::kKVStages; ++s) {
+      mbar_init(&bars[L::kBarKFull + s], 1);
+      mbar_init(&bars[L::kBarVFull + s], 1);
+      mbar_init(&bars[L::kBarKEmpty + s], 1);
+      mbar_init(&bars[L::kBarVEmpty + s], 1);
+      mbar_init(&bars[L::kBarVReady + s], 32);
+    }
+    for (int w = 0; w < kXQTiles; ++w) {
+      mbar_init(&bars[L::kBarSFull + w], 1);
+      mbar_init(&bars[L::kBarSFree + w], kXTile);
+      mbar_init(&bars[L::kBarPFull + w], kXTile);
+      mbar_init(&bars[L::kBarODone + w], 1);
+      mbar_init(&bars[L::kBarOFree + w], kXTile);
+    }
+    mbar_init(&bars[L::kBarDrain], 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kXWarpMma) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == kXWarpProducer && lane == 0) {
+    tma_prefetch_desc(&p.tm_q);
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl wc{abort_flag, p.err, p.timeout_ns};
+  WaitCtl wc_drain = wc;  // clean-up waits: ignore the abort word, keep the time limit
+  int drain_abort = 0;
+  wc_drain.abort_flag = &drain_abort;
+
+  if (warp >= 8) {
+    setmaxnreg_dec<kXRegsOther>();
+    if (warp == kXWarpProducer) {
+      // ============================================================== Q/K/V TMA producer
+      if (lane == 0) {
+        const uint64_t pol_stream = l2_policy_evict_first();
+        const uint64_t pol_keep = l2_policy_evict_last();
+        bool ok = true;
+        int kc = 0, vc = 0, uc = 0;  // K tiles, V tiles, Q loads issued
+        auto load_k = [&](const CrossUnit &un, int j) -> bool {
+          const int s = kc % L::kKVStages;
+          if (kc >= L::kKVStages && !mbar_wait(&bars[L::kBarKEmpty + s], ((kc / L::kKVStages) - 1) & 1, wc))
+            return false;
+          mbar_arrive_expect_tx(&bars[L::kBarKFull + s], T::kBytes);
+          T::load(smem + L::kOffK + s * T::kBytes, &p.tm_k, &bars[L::kBarKFull + s], j * kXTile, un.h / p.group, un.b,
+                  pol_keep);
+          ++kc;
+          return true;
+        };
+        auto load_v = [&](const CrossUnit &un, int j) -> bool {
+          const int s = vc % L::kKVStages;
+          if (vc >= L::kKVStages && !mbar_wait(&bars[L::kBarVEmpty + s], ((vc / L::kKVStages) - 1) & 1, wc))
+            return false;
+          mbar_arrive_expect_tx(&bars[L::kBarVFull + s], T::kBytes);
+          T::load(smem + L::kOffV + s * T::kBytes, &p.tm_v, &bars[L::kBarVFull + s], j * kXTile, un.h / p.group, un.b,
+                  pol_keep);
+          ++vc;
+          return true;
+        };
+        for (int u = u_begin; u < p.n_units && ok; u += u_step) {
+          const CrossUnit un = cross_unit(p, u);
+          if (un.nt == 0) continue;
+          // Q slot: free once the last score MMAs of the previous unit are done
+          if (uc > 0) ok = mbar_wait(&bars[L::kBarQEmpty], (uc - 1) & 1, wc);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bars[L::kBarQFull], kXQTiles * T::kBytes);
+          for (int w = 0; w < kXQTiles; ++w)
+            T::load(smem + L::kOffQ + w * T::kBytes, &p.tm_q, &bars[L::kBarQFull], un.q0 + w * kXTile, un.h, un.b,
+                    pol_stream);
+          ++uc;
+          ok = load_k(un, 0);
+          for (int j = 0; j < un.nt && ok; ++j) {
+            if (j + 1 < un.nt) ok = load_k(un, j + 1);
+            if (ok) ok = load_v(un, j);
+          }
+        }
+        if (!ok) {
+          // every copy already issued lands before the CTA exits; slot s was
+          // armed (n - s + stages - 1) / stages times after n issues
+          if (uc) mbar_wait(&bars[L::kBarQFull], (uc - 1) & 1, wc_drain);
+          for (int s = 0; s < L::kKVStages; ++s) {
+            const int ak = (kc - s + L::kKVStages - 1) / L::kKVStages, av = (vc - s + L::kKVStages - 1) / L::kKVStages;
+            if (ak > 0) mbar_wait(&bars[L::kBarKFull + s], (ak - 1) & 1, wc_drain);
+            if (av > 0) mbar_wait(&bars[L::kBarVFull + s], (av - 1) & 1, wc_drain);
+          }
+        }
+      }
+    } else if (warp == kXWarpMma) {
+      // ============================================================== MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kXTile, kXTile, false);
+        constexpr uint32_t idesc_o = idesc_bf16_f32(kXTile, D, true);
+        const uint32_t sQ = smem_u32(smem + L::kOffQ);
+        const uint32_t sK = smem_u32(smem + L::kOffK);
+        const uint32_t sV = smem_u32(smem + L::kOffV);
+        bool ok = true;
+        int kc = 0, vc = 0;  // K and V tiles consumed
+        int gs = 0, gp = 0;  // score tiles and P V tiles issued per warpgroup
+        int uc = 0;
+        auto issue_s = [&](int w, int s) {
+          const uint32_t a_lo = smem_desc_lo(sQ + w * T::kBytes, 16);
+          const uint32_t b_lo = smem_desc_lo(sK + s * T::kBytes, 16);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_bf16_ss(tmem + L::col_s(w), desc_at(a_lo, T::k_step(kk), T::kDescHi),
+                        desc_at(b_lo, T::k_step(kk), T::kDescHi), idesc_s, kk > 0 ? 1u : 0u);
+          tc_commit(&bars[L::kBarSFull + w]);
+        };
+        auto issue_pv = [&](int w, int s, bool first) {
+          const uint32_t v_lo = smem_desc_lo(sV + s * T::kBytes, T::kSlabBytes);
+#pragma unroll
+          for (int kk = 0; kk < kXTile / 16; ++kk)
+            mma_bf16_ts(tmem + L::col_o(w), tmem + L::col_p(w) + kk * 8, desc_at(v_lo, T::mn_step(kk), T::kDescHi),
+                        idesc_o, (!first || kk > 0) ? 1u : 0u);
+          tc_commit(&bars[L::kBarODone + w]);
+        };
+        // D <= 64, per key tile j: S0(j+1), P0 V(j), S1(j+1), P1 V(j), so that a
+        // warpgroup's next scores are there when it has written P(j).
+        // D = 128 (P over S): P0 V(j), S0(j+1), P1 V(j), S1(j+1), each score
+        // tile once the product that reads P from its columns is done.
+        for (int u = u_begin; u < p.n_units && ok; u += u_step) {
+          const int nt = cross_unit(p, u).nt;
+          if (nt == 0) continue;
+          ok = mbar_wait(&bars[L::kBarQFull], uc & 1, wc);
+          if (ok) ok = mbar_wait(&bars[L::kBarKFull + kc % L::kKVStages], (kc / L::kKVStages) & 1, wc);
+          for (int w = 0; w < kXQTiles && ok; ++w) {
+            if (gs > 0 && !(ok = mbar_wait(&bars[L::kBarSFree + w], (gs - 1) & 1, wc))) break;
+            // P over S: the last P V of the previous unit has read its P
+            if (L::kAlias && gp > 0 && !(ok = mbar_wait(&bars[L::kBarODone + w], (gp - 1) & 1, wc))) break;
+            tc_fence_after_sync();
+            issue_s(w, kc % L::kKVStages);
+          }
+          if (!ok) break;
+          tc_commit(&bars[L::kBarKEmpty + kc % L::kKVStages]);
+          if (nt == 1) tc_commit(&bars[L::kBarQEmpty]);
+          ++kc;
+          ++gs;
+          for (int j = 0; j < nt && ok; ++j) {
+            const bool has_next = j + 1 < nt;
+            const int sk = kc % L::kKVStages;
+            const int sv = vc % L::kKVStages;
+            if (has_next) ok = mbar_wait(&bars[L::kBarKFull + sk], (kc / L::kKVStages) & 1, wc);
+            if (ok) ok = mbar_wait(&bars[L::kBarVFull + sv], (vc / L::kKVStages) & 1, wc);
+            if (ok && fix) ok = mbar_wait(&bars[L::kBarVReady + sv], (vc / L::kKVStages) & 1, wc);
+            for (int w = 0; w < kXQTiles && ok; ++w) {
+              if (!L::kAlias && has_next) {
+                if (!(ok = mbar_wait(&bars[L::kBarSFree + w], (gs - 1) & 1, wc))) break;
+                tc_fence_after_sync();
+                issue_s(w, sk);
+              }
+              if (!(ok = mbar_wait(&bars[L::kBarPFull + w], gp & 1, wc))) break;
+              // the first P V of a unit overwrites O: the epilogue of the
+              // previous unit must have read it
+              if (j == 0 && uc > 0 && !(ok = mbar_wait(&bars[L::kBarOFree + w], (uc - 1) & 1, wc))) break;
+              tc_fence_after_sync();
+              issue_pv(w, sv, j == 0);
+              if (L::kAlias && has_next) {
+                if (!(ok = mbar_wait(&bars[L::kBarODone + w], gp & 1, wc))) break;
+                tc_fence_after_sync();
+                issue_s(w, sk);
+              }
+            }
+            if (!ok) break;
+            if (has_next) {
+              tc_commit(&bars[L::kBarKEmpty + sk]);
+              // after the unit's last score MMAs the Q slot can be refilled
+              if (j + 2 == nt) tc_commit(&bars[L::kBarQEmpty]);
+              ++kc;
+              ++gs;
+            }
+            tc_commit(&bars[L::kBarVEmpty + sv]);
+            ++vc;
+            ++gp;
+          }
+          ++uc;
+        }
+        // every MMA issued above completes before Tensor Memory is released
+        tc_commit(&bars[L::kBarDrain]);
+        mbar_wait(&bars[L::kBarDrain], 0, wc_drain);
+      }
+    } else if (warp == kXWarpFix && fix) {
+      // ============================================================== V rows that do not count
+      bool ok = true;
+      int vc = 0;
+      for (int u = u_begin; u < p.n_units && ok; u += u_step) {
+        const CrossUnit un = cross_unit(p, u);
+        const uint8_t *mrow = kMasked ? p.mask + int64_t(un.b) * p.mask_sb : nullptr;
+        uint32_t next = kMasked && un.nt > 0 ? cross_mask_bytes(mrow, p.mask_vec4, 0, un.keys, lane) : 0u;
+        for (int j = 0; j < un.nt && ok; ++j, ++vc) {
+          const int s = vc % L::kKVStages;
+          KeepWords keep;
+          if (kMasked) {
+            keep = cross_keep(next);
+            if (j + 1 < un.nt) next = cross_mask_bytes(mrow, p.mask_vec4, (j + 1) * kXTile, un.keys, lane);
+          }
+          ok = mbar_wait<false>(&bars[L::kBarVFull + s], (vc / L::kKVStages) & 1, wc);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          uint8_t *tile = smem + L::kOffV + s * T::kBytes;
+          const int n = min(kXTile, un.keys - j * kXTile);
+          const bool any = kMasked ? !keep.all() : n < kXTile;
+          if (any) {
+            for (int r = 0; r < kXTile; ++r) {
+              const bool has = kMasked ? keep.has(r) : r < n;
+              if (!has) T::zero_row(tile, r, lane);
+            }
+            fence_proxy_async_smem();
+          }
+          mbar_arrive(&bars[L::kBarVReady + s]);
+        }
+      }
+    }
+  } else {
+    // ================================================================ softmax warpgroups
+    setmaxnreg_inc<kXRegsSoftmax>();
+    const int w = warp >> 2;          // query tile
+    const int t = threadIdx.x & 127;  // row inside the tile
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + L::col_s(w);
+    const uint32_t tP = tmem + lane_base + L::col_p(w);
+    const uint32_t tO = tmem + lane_base + L::col_o(w);
+    const float c_s = p.tau * kXLog2e;  // scores to log2 units
+    // A row keeps its running maximum until a tile's exceeds it by more than 8
+    // in log2 units, so most tiles skip the rescale of O; the kept maximum is
+    // used for P and l alike, so the result is unchanged.
+    const float slack = fminf(8.f / c_s, 1e30f);
+    bool ok = true;
+    int gt = 0;  // key tiles processed (all units)
+    for (int u = u_begin; u < p.n_units && ok; u += u_step) {
+      const CrossUnit un = cross_unit(p, u);
+      const uint8_t *mrow = kMasked ? p.mask + int64_t(un.b) * p.mask_sb : nullptr;
+      uint32_t next = kMasked && un.nt > 0 ? cross_mask_bytes(mrow, p.mask_vec4, 0, un.keys, lane) : 0u;
+      float m_cur = -INFINITY;  // maximum used for P and l (raw scores)
+      float neg_m = 0.f;        // -m_cur in log2 units (0 while there is none)
+      float l = 0.f;
+      for (int j = 0; j < un.nt && ok; ++j, ++gt) {
+        KeepWords keep;
+        if (kMasked) {
+          keep = cross_keep(next);
+          if (j + 1 < un.nt) next = cross_mask_bytes(mrow, p.mask_vec4, (j + 1) * kXTile, un.keys, lane);
+        }
+        // the loads below are warp-collective: a warp leaves its waits as one
+        ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarSFull + w], gt & 1, wc));
+        if (!ok) break;
+        tc_fence_after_sync();
+        uint32_t sreg[kXTile];
+#pragma unroll
+        for (int c = 0; c < kXTile / 32; ++c)
+          tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sreg[c * 32]));
+        tmem_wait_ld();
+        reg_fence(sreg);
+        tc_fence_before_sync();
+        mbar_arrive(&bars[L::kBarSFree + w]);
+
+        if (kMasked) {
+          if (!keep.all()) {
+#pragma unroll
+            for (int c = 0; c < kXTile; ++c) sreg[c] = keep.has(c) ? sreg[c] : 0xFF800000u;
+          }
+        } else if (un.keys - j * kXTile < kXTile) {
+          const int n = un.keys - j * kXTile;
+#pragma unroll
+          for (int c = 0; c < kXTile; ++c) sreg[c] = c < n ? sreg[c] : 0xFF800000u;
+        }
+        // tile maximum: eight independent chains
+        float m8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m8[i] = fmaxf(__uint_as_float(sreg[2 * i]), __uint_as_float(sreg[2 * i + 1]));
+#pragma unroll
+        for (int i = 8; i < kXTile / 2; ++i)
+          m8[i & 7] = max3f(m8[i & 7], __uint_as_float(sreg[2 * i]), __uint_as_float(sreg[2 * i + 1]));
+        const float mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+        const bool need = mx > m_cur + slack;
+        float alpha = 1.f;
+        if (need) {
+          alpha = (m_cur == -INFINITY) ? 0.f : ex2_approx((m_cur - mx) * c_s);
+          l *= alpha;
+          m_cur = mx;
+          neg_m = -mx * c_s;
+        }
+        const float2 cs2 = make_float2(c_s, c_s), negm2 = make_float2(neg_m, neg_m);
+        uint32_t pk[kXTile / 2];
+        float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < kXTile / 2; ++i) {
+          const float2 a = ffma2(make_float2(__uint_as_float(sreg[2 * i]), __uint_as_float(sreg[2 * i + 1])), cs2,
+                                 negm2);
+          const float2 pv = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+          ls[i & 3] = fadd2(ls[i & 3], pv);
+          pk[i] = pack_bf16x2(pv.x, pv.y);
+        }
+        const float2 lsum2 = fadd2(fadd2(ls[0], ls[1]), fadd2(ls[2], ls[3]));
+        l += lsum2.x + lsum2.y;
+
+        // P(j) overwrites what P V(j-1) read, possibly the last one of the
+        // previous unit, and the rescale needs its sum
+        if (gt > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarODone + w], (gt - 1) & 1, wc));
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (j > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(tO + c, o);
+              tmem_wait_ld();
+              reg_fence(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(tO + c, o);
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < kXTile / 2; c += 32) tmem_st32(tP + c, *reinterpret_cast<uint32_t(*)[32]>(&pk[c]));
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(&bars[L::kBarPFull + w]);
+      }
+
+      // -------------------------------------------------------------- epilogue
+      const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
+      const int row = un.q0 + w * kXTile + t;
+      if (un.nt > 0) {
+        if (!ok) break;
+        ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarODone + w], (gt - 1) & 1, wc));
+        if (!ok) break;
+        tc_fence_after_sync();
+      }
+      uint4 *op = reinterpret_cast<uint4 *>(p.out + un.b * p.out_sb + un.h * p.out_sh + int64_t(row) * p.out_sn);
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t r[32] = {};
+        if (un.nt > 0) {
+          tmem_ld32(tO + c, r);
+          tmem_wait_ld();
+          reg_fence(r);
+        }
+        if (row < p.Nq) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t wv[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              wv[e] = pack_bf16x2(__uint_as_float(r[8 * q + 2 * e]) * inv_l,
+                                  __uint_as_float(r[8 * q + 2 * e + 1]) * inv_l);
+            op[c / 8 + q] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+          }
+        }
+      }
+      if (un.nt > 0) {
+        // O has been read: the next unit's first P V may overwrite it
+        tc_fence_before_sync();
+        mbar_arrive(&bars[L::kBarOFree + w]);
+      }
+      if (row < p.Nq && p.lse != nullptr)
+        p.lse[un.b * p.lse_sb + un.h * p.lse_sh + int64_t(row) * p.lse_sn] =
+            (l > 0.f) ? fmaf(neg_m, -kXLn2, logf(l)) : -INFINITY;
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == kXWarpMma) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace pba
