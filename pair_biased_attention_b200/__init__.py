@@ -167,13 +167,15 @@ def pba_status_string(status: int) -> str:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        # the current stream's handle, without the Python object around it
+        # (3.6 us a call against 0.2)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(fn: str, status: int):
@@ -201,9 +203,10 @@ def _dtype_code(dt) -> int:
 def _bhn(name, t, shape_len=4):
     if t.dim() != shape_len:
         raise ValueError(f"{name} must have {shape_len} dims")
-    if shape_len == 4 and t.stride(3) != 1 and t.shape[3] > 1:
+    stride = t.stride()
+    if shape_len == 4 and stride[3] != 1 and t.shape[3] > 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    return t.stride(0), t.stride(1), t.stride(2)
+    return stride[:3]
 
 
 def _desc(q, k, v, bias, key_mask, out_strides, lse_strides, softmax_scale) -> PbaAttnDesc:
@@ -485,25 +488,32 @@ def pba_backward_noalloc(q, k, v, bias, key_mask, out, lse, dout, softmax_scale=
     return dq, dk, dv, dbias
 
 
-def _here(*named):
+def _here(tensors, names):
     """Checks that the tensors (None ones aside) lie on the current device,
     whose stream the call goes to."""
     current = torch.cuda.current_device()
-    for name, t in named:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.get_device() != current:
+    for i, t in enumerate(tensors):
+        if t is not None and t.get_device() != current:
+            name = names.split()[i]
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
             raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{current}")
+
+
+_ON_CURRENT = contextlib.nullcontext()
 
 
 def _alloc_on(stream):
     """Outputs and workspaces made by a call belong to the stream that it
     launches on, so that the allocator hands them out again in its order."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _ON_CURRENT
     return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
+def _empty_as(t, dtype=None):
+    """A contiguous tensor of t's shape."""
+    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 _RELPOS_RULES = {"clip": PBA_RELPOS_CLIP, "log": PBA_RELPOS_LOG, "log_causal": PBA_RELPOS_LOG_CAUSAL}
@@ -512,34 +522,38 @@ _RELPOS_RULES = {"clip": PBA_RELPOS_CLIP, "log": PBA_RELPOS_LOG, "log_causal": P
 def _relpos_desc(rows, H, dtype, q_pos, k_pos, rule, max_distance, q_group, k_group, B=1):
     """The descriptor without the strides of the matrices.  B: the batch that
     those ask for; position arrays of one sequence are shared by a batch."""
-    if rule not in _RELPOS_RULES:
+    kind = _RELPOS_RULES.get(rule)
+    if kind is None:
         raise ValueError(f"rule must be one of {sorted(_RELPOS_RULES)}")
     if (q_group is None) != (k_group is None):
         raise ValueError("q_group and k_group go together")
     Nq, Nk = q_pos.shape[-1], k_pos.shape[-1]
     strides = []
-    given = [("q_pos", q_pos, Nq), ("k_pos", k_pos, Nk), ("q_group", q_group, Nq), ("k_group", k_group, Nk)]
-    for name, t, n in given:
+    for name, t, n in (("q_pos", q_pos, Nq), ("k_pos", k_pos, Nk), ("q_group", q_group, Nq),
+                       ("k_group", k_group, Nk)):
         if t is None:
+            strides.append(0)
             continue
         if t.dtype != torch.int32:
             raise ValueError(f"{name} must be torch.int32, got {t.dtype}")
-        if t.dim() not in (1, 2) or t.shape[-1] != n or (t.stride(-1) != 1 and n > 1):
+        shape, stride = t.shape, t.stride()
+        if len(shape) not in (1, 2) or shape[-1] != n or (stride[-1] != 1 and n > 1):
             raise ValueError(f"{name} must be [{n}] or [B, {n}] int32, contiguous along tokens")
-        if t.dim() == 2 and t.shape[0] != 1:
-            if B not in (1, t.shape[0]):
-                raise ValueError(f"{name} has batch {t.shape[0]}, another argument has {B}")
-            B = t.shape[0]
-    for name, t, n in given:
-        strides.append(0 if t is None or t.dim() == 1 or t.shape[0] == 1 else t.stride(0))
-    d = PbaRelposDesc(B, H, Nq, Nk, _dtype_code(dtype), _RELPOS_RULES[rule], rows, int(max_distance), *strides)
-    return d
+        if len(shape) == 1 or shape[0] == 1:
+            strides.append(0)
+            continue
+        if B not in (1, shape[0]):
+            raise ValueError(f"{name} has batch {shape[0]}, another argument has {B}")
+        B = shape[0]
+        strides.append(stride[0])
+    return PbaRelposDesc(B, H, Nq, Nk, _dtype_code(dtype), kind, rows, int(max_distance), *strides)
 
 
 def _matrix_strides(name, t, shape, dtype):
-    if tuple(t.shape) != shape or t.dtype != dtype or (t.stride(3) != 1 and shape[3] > 1):
+    stride = t.stride()
+    if t.shape != shape or t.dtype != dtype or (stride[3] != 1 and shape[3] > 1):
         raise ValueError(f"{name} must be a {shape} {dtype} tensor, contiguous along keys")
-    return t.stride()[:3]
+    return stride[:3]
 
 
 def pba_relpos_bias_forward(table, q_pos, k_pos, rule="clip", max_distance=0, q_group=None, k_group=None, base=None,
@@ -555,8 +569,7 @@ def pba_relpos_bias_forward(table, q_pos, k_pos, rule="clip", max_distance=0, q_
     (int32, shaped as the positions) pairs of different groups take one more
     row, the table's last.  base [B,H,Nq,Nk] of the table's dtype is added
     (``out`` may be base itself).  Returns out [B,H,Nq,Nk]."""
-    _here(("table", table), ("q_pos", q_pos), ("k_pos", k_pos), ("q_group", q_group), ("k_group", k_group),
-          ("base", base), ("out", out))
+    _here((table, q_pos, k_pos, q_group, k_group, base, out), "table q_pos k_pos q_group k_group base out")
     if table.dim() != 2 or not table.is_contiguous():
         raise ValueError("table must be a contiguous [rows, H] tensor")
     rows, H = table.shape
@@ -570,7 +583,7 @@ def pba_relpos_bias_forward(table, q_pos, k_pos, rule="clip", max_distance=0, q_
     shape = (d.B, H, d.Nq, d.Nk)
     if out is None:
         with _alloc_on(stream):
-            out = torch.empty(shape, dtype=table.dtype, device=table.device)
+            out = table.new_empty(shape)
     d.out_stride[:] = _matrix_strides("out", out, shape, table.dtype)
     if base is not None:
         d.base_stride[:] = _matrix_strides("base", base, shape, table.dtype)
@@ -587,7 +600,7 @@ def pba_relpos_bias_backward(dbias, q_pos, k_pos, rows, rule="clip", max_distanc
     table's ``rows`` rows.  Position arrays of one sequence are shared by the
     batch of dbias.  Returns dtable [rows, H] (fp32).  The gradient of base is
     dbias itself."""
-    _here(("dbias", dbias), ("q_pos", q_pos), ("k_pos", k_pos), ("q_group", q_group), ("k_group", k_group))
+    _here((dbias, q_pos, k_pos, q_group, k_group), "dbias q_pos k_pos q_group k_group")
     if dbias.dim() != 4:
         raise ValueError("dbias must be [B,H,Nq,Nk]")
     B, H = dbias.shape[:2]
@@ -597,8 +610,8 @@ def pba_relpos_bias_backward(dbias, q_pos, k_pos, rows, rule="clip", max_distanc
     need = ctypes.c_int64()
     _check("pba_relpos_bias_backward_workspace", lib.pba_relpos_bias_backward_workspace(ctypes.byref(d), ctypes.byref(need)))
     with _alloc_on(stream):
-        dtable = torch.empty((d.rows, H), dtype=torch.float32, device=dbias.device)
-        work = torch.empty(need.value, dtype=torch.uint8, device=dbias.device)
+        dtable = dbias.new_empty((d.rows, H), dtype=torch.float32)
+        work = dbias.new_empty(need.value, dtype=torch.uint8)
     _check("pba_relpos_bias_backward", lib.pba_relpos_bias_backward(
         ctypes.byref(d), _ptr(q_pos), _ptr(k_pos), _ptr(q_group), _ptr(k_group), _ptr(dbias), _ptr(dtable),
         _ptr(work), need.value, _stream(stream)))
@@ -633,26 +646,25 @@ def _row_stride(name, t, shape, dtype):
 
 def _norm_desc(ref, kind, eps, post, pre, scale):
     """The descriptor without its strides, and (post_w, post_b, pre_w, pre_b)."""
-    if kind not in _NORM_KINDS:
+    code = _NORM_KINDS.get(kind)
+    if code is None:
         raise ValueError(f"kind must be one of {sorted(_NORM_KINDS)}")
     if ref.dim() < 1:
         raise ValueError("x must have a channel axis")
     C = ref.shape[-1]
-    params = (*(post or (None, None)), *(pre or (None, None)))
-    if len(params) != 4:
-        raise ValueError("post and pre are pairs (weight, bias or None)")
-    if (post is not None and post[0] is None) or (pre is not None and pre[0] is None):
+    post_w, post_b = (None, None) if post is None else post
+    pre_w, pre_b = (None, None) if pre is None else pre
+    if (post is not None and post_w is None) or (pre is not None and pre_w is None):
         raise ValueError("a norm needs its weight")
     dtype = None
-    for name, t in zip(("scale", "post weight", "post bias", "pre weight", "pre bias"), (scale, *params)):
-        if t is None:
-            continue
-        if tuple(t.shape) != (C,) or (t.stride(0) != 1 and C > 1) or t.dtype != (dtype or t.dtype):
-            raise ValueError(f"{name} must be a contiguous [{C}] tensor of the other parameters' dtype")
-        dtype = t.dtype
-    d = PbaNormDesc(ref.numel() // C if C else 0, C, _dtype_code(ref.dtype), _dtype_code(dtype or ref.dtype),
-                    _NORM_KINDS[kind], float(eps))
-    return d, params
+    for t in (scale, post_w, post_b, pre_w, pre_b):
+        if t is not None:
+            dtype = dtype or t.dtype
+            if t.dim() != 1 or t.shape[0] != C or t.dtype != dtype or not t.is_contiguous():
+                raise ValueError(f"scale, weights and biases must be contiguous [{C}] tensors of one dtype")
+    d = PbaNormDesc(ref.numel() // C if C else 0, C, _dtype_code(ref.dtype), _dtype_code(dtype or ref.dtype), code,
+                    eps)
+    return d, (post_w, post_b, pre_w, pre_b)
 
 
 def pba_block_norm_forward(x, f=None, gate=None, scale=None, post=None, pre=None, kind="layer", eps=1e-5, h=None, y=None,
@@ -665,18 +677,18 @@ def pba_block_norm_forward(x, f=None, gate=None, scale=None, post=None, pre=None
     [C] or None; the parameters are all bf16 or all fp32.  kind "layer" or
     "rms".  ``h`` may be x itself.  Returns h and y (None without pre)."""
     d, params = _norm_desc(x, kind, eps, post, pre, scale)
-    _here(("x", x), ("f", f), ("gate", gate), ("scale", scale), ("post weight", params[0]),
-          ("post bias", params[1]), ("pre weight", params[2]), ("pre bias", params[3]), ("h", h), ("y", y))
+    _here((x, f, gate, scale, *params, h, y), "x f gate scale post_w post_b pre_w pre_b h y")
     with _alloc_on(stream):
         if h is None and f is not None:
-            h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            h = _empty_as(x)
         if y is None and pre is not None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    d.x_stride = _row_stride("x", x, x.shape, x.dtype)
-    d.f_stride = _row_stride("f", f, x.shape, x.dtype)
-    d.gate_stride = _row_stride("gate", gate, x.shape, x.dtype)
-    d.h_stride = _row_stride("h", h, x.shape, x.dtype)
-    d.y_stride = _row_stride("y", y, x.shape, x.dtype)
+            y = _empty_as(x)
+    shape, dtype = x.shape, x.dtype
+    d.x_stride = _row_stride("x", x, shape, dtype)
+    d.f_stride = _row_stride("f", f, shape, dtype)
+    d.gate_stride = _row_stride("gate", gate, shape, dtype)
+    d.h_stride = _row_stride("h", h, shape, dtype)
+    d.y_stride = _row_stride("y", y, shape, dtype)
     _check("pba_block_norm_forward", load_library().pba_block_norm_forward(
         ctypes.byref(d), _ptr(x), _ptr(f), _ptr(gate), _ptr(scale), *map(_ptr, params), _ptr(h), _ptr(y),
         _stream(stream)))
@@ -691,8 +703,7 @@ def pba_block_norm_backward(h, dh, dy, f=None, gate=None, scale=None, post=None,
     dpre_w, dpre_b ([C], fp32); None for what was not given."""
     ref = h if h is not None else dh
     d, params = _norm_desc(ref, kind, eps, post, pre, scale)
-    _here(("h", h), ("dh", dh), ("dy", dy), ("f", f), ("gate", gate), ("scale", scale), ("post weight", params[0]),
-          ("post bias", params[1]), ("pre weight", params[2]), ("pre bias", params[3]))
+    _here((h, dh, dy, f, gate, scale, *params), "h dh dy f gate scale post_w post_b pre_w pre_b")
     shape, dtype, C = ref.shape, ref.dtype, ref.shape[-1]
     d.h_stride = _row_stride("h", h, shape, dtype)
     d.f_stride = _row_stride("f", f, shape, dtype)
@@ -704,11 +715,9 @@ def pba_block_norm_backward(h, dh, dy, f=None, gate=None, scale=None, post=None,
     need = ctypes.c_int64()
     _check("pba_block_norm_backward_workspace", lib.pba_block_norm_backward_workspace(ctypes.byref(d), ctypes.byref(need)))
     with _alloc_on(stream):
-        dx, df, dgate = (torch.empty(shape, dtype=dtype, device=ref.device) if t is not None else None
-                         for t in (ref, f, gate))
-        sums = tuple(torch.empty(C, dtype=torch.float32, device=ref.device) if t is not None else None
-                     for t in (scale, *params))
-        work = torch.empty(need.value, dtype=torch.uint8, device=ref.device)
+        dx, df, dgate = (None if t is None else _empty_as(ref) for t in (ref, f, gate))
+        sums = [None if t is None else _empty_as(t, torch.float32) for t in (scale, *params)]
+        work = ref.new_empty(need.value, dtype=torch.uint8)
     _check("pba_block_norm_backward", lib.pba_block_norm_backward(
         ctypes.byref(d), _ptr(h), _ptr(f), _ptr(gate), _ptr(scale), *map(_ptr, params), _ptr(dh), _ptr(dy), _ptr(dx),
         _ptr(df), _ptr(dgate), *map(_ptr, sums), _ptr(work), need.value, _stream(stream)))
@@ -719,19 +728,18 @@ def _cross_desc(q, k, v, k_len, key_mask, softmax_scale) -> PbaCrossDesc:
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q must be [B,H,Nq,D], k and v [B,Hkv,Nk,D]")
     B, H, Nq, D = q.shape
-    Hkv, Nk = k.shape[1:3]
-    if tuple(k.shape) != (B, Hkv, Nk, D) or v.shape != k.shape:
+    Bk, Hkv, Nk, Dk = k.shape
+    if Bk != B or Dk != D or v.shape != k.shape:
         raise ValueError("k and v must be [B,Hkv,Nk,D] matching q")
-    d = PbaCrossDesc(B, H, Hkv, Nq, Nk, D, _dtype_code(q.dtype), float(softmax_scale or 0.0))
-    for name, t, stride in (("q", q, d.q_stride), ("k", k, d.k_stride), ("v", v, d.v_stride)):
-        if t.dtype != q.dtype:
-            raise ValueError(f"{name} must be {q.dtype}, got {t.dtype}")
-        stride[:] = _bhn(name, t)
-    if k_len is not None and (k_len.dtype != torch.int32 or tuple(k_len.shape) != (B,) or not k_len.is_contiguous()):
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError(f"k and v must be {q.dtype}, got {k.dtype} and {v.dtype}")
+    d = PbaCrossDesc(B, H, Hkv, Nq, Nk, D, _dtype_code(q.dtype), softmax_scale or 0.0, _bhn("q", q), _bhn("k", k),
+                     _bhn("v", v))
+    if k_len is not None and (k_len.dtype != torch.int32 or k_len.dim() != 1 or k_len.shape[0] != B or
+                              not k_len.is_contiguous()):
         raise ValueError(f"k_len must be a contiguous [{B}] int32 tensor")
     if key_mask is not None:
-        if key_mask.dtype != torch.uint8 or tuple(key_mask.shape) != (B, Nk) or \
-                (key_mask.stride(1) != 1 and Nk > 1):
+        if key_mask.dtype != torch.uint8 or key_mask.shape != (B, Nk) or (key_mask.stride(1) != 1 and Nk > 1):
             raise ValueError(f"key_mask must be [{B}, {Nk}] uint8, contiguous along keys")
         d.mask_stride_b = key_mask.stride(0)
     return d
@@ -745,13 +753,13 @@ def pba_cross_attn_forward(q, k, v, k_len=None, key_mask=None, out=None, lse=Non
     key_mask [B,Nk] uint8 (1 = key takes part); either may be None.  Returns
     out [B,H,Nq,D] and lse [B,H,Nq] (fp32); queries without a key get 0 and
     -inf."""
-    _here(("q", q), ("k", k), ("v", v), ("k_len", k_len), ("key_mask", key_mask), ("out", out), ("lse", lse))
+    _here((q, k, v, k_len, key_mask, out, lse), "q k v k_len key_mask out lse")
     d = _cross_desc(q, k, v, k_len, key_mask, softmax_scale)
     with _alloc_on(stream):
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = _empty_as(q)
         if lse is None and return_lse:
-            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+            lse = q.new_empty(q.shape[:3], dtype=torch.float32)
     if out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError(f"out must be a {tuple(q.shape)} {q.dtype} tensor")
     d.out_stride[:] = _bhn("out", out)
@@ -769,8 +777,7 @@ def pba_cross_attn_backward(q, k, v, out, lse, dout, k_len=None, key_mask=None, 
     """Gradients of pba_cross_attn_forward from its out and lse: dq [B,H,Nq,D],
     dk and dv [B,Hkv,Nk,D] (bf16, contiguous).  The other arguments as for the
     forward."""
-    _here(("q", q), ("k", k), ("v", v), ("out", out), ("lse", lse), ("dout", dout), ("k_len", k_len),
-          ("key_mask", key_mask))
+    _here((q, k, v, out, lse, dout, k_len, key_mask), "q k v out lse dout k_len key_mask")
     d = _cross_desc(q, k, v, k_len, key_mask, softmax_scale)
     for name, t, shape, dtype, stride in (("out", out, q.shape, q.dtype, d.out_stride),
                                           ("dout", dout, q.shape, q.dtype, d.dout_stride),
@@ -779,8 +786,8 @@ def pba_cross_attn_backward(q, k, v, out, lse, dout, k_len=None, key_mask=None, 
             raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor")
         stride[:] = _bhn(name, t, t.dim())
     with _alloc_on(stream):
-        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
-        delta = torch.empty(lse.shape, dtype=torch.float32, device=q.device)
+        dq, dk, dv = (_empty_as(t) for t in (q, k, v))
+        delta = _empty_as(lse)
     _check("pba_cross_attn_backward", load_library().pba_cross_attn_backward(
         ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(k_len), _ptr(key_mask), _ptr(out), _ptr(lse), _ptr(dout),
         _ptr(dq), _ptr(dk), _ptr(dv), _ptr(delta), _stream(stream)))

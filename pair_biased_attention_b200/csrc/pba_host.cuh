@@ -34,17 +34,6 @@ inline EncodeTiledFn encode_fn() {
   return fn;
 }
 
-inline pba_status check_device() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PBA_ERR_CUDA;
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return PBA_ERR_CUDA;
-  if (major != 10 || minor != 0) return PBA_ERR_UNSUPPORTED;  // built for sm_100a only
-  return PBA_OK;
-}
-
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // One-time per-device kernel set-up (the dynamic shared memory limit is a
@@ -91,6 +80,24 @@ inline bool make_map(CUtensorMap *map, const void *base, const uint64_t dims[4],
 
 inline bool stride_ok_bf16(int64_t s, int64_t extent) { return extent <= 1 || (s > 0 && s % 8 == 0); }
 inline bool stride_ok_f32(int64_t s, int64_t extent) { return extent <= 1 || (s > 0 && s % 4 == 0); }
+
+// Whether the current device is one that the kernels were built for (sm_100a).
+inline pba_status check_device() {
+  static PerDeviceOnce once;
+  static bool fits[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PBA_ERR_CUDA;
+  if (dev >= kMaxDevices) return PBA_ERR_UNSUPPORTED;
+  const cudaError_t e = once_per_device(once, [&] {
+    int major = 0, minor = 0;
+    cudaError_t r = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    if (r == cudaSuccess) r = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    fits[dev] = major == 10 && minor == 0;
+    return r;
+  });
+  if (e != cudaSuccess) return PBA_ERR_CUDA;
+  return fits[dev] ? PBA_OK : PBA_ERR_UNSUPPORTED;
+}
 
 inline int sm_count() {  // of the current device; 0 when it cannot be had
   int dev = 0, sms = 0;
