@@ -22,6 +22,8 @@ namespace {
 constexpr int64_t kPlanSms = 148;
 // Dynamic shared memory that the relative position kernels may ask for.
 constexpr int kRelposSmem = 200 * 1024;
+// Blocks of the table's gradient on an SM.
+constexpr int64_t kRelposGradResident = 5;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t pow2_ceil(int64_t x) {
@@ -76,7 +78,7 @@ int32_t log_border(int e, int m, int t, int far) {
 pba_status check_relpos(const pba_relpos_desc *d, bool groups) {
   if (d == nullptr) return PBA_ERR_INVALID_ARG;
   if (d->B < 1 || d->H < 1 || d->B > 65535 || d->H > 65535 || d->Nq < 0 || d->Nk < 0 || d->Nq > kMaxI32 ||
-      d->Nk > kMaxI32 - 8 || d->B * d->Nq > kMaxI32)
+      d->Nk > kMaxI32 - 512 || d->B * d->Nq > kMaxI32 || d->Nq > (1 << 30))
     return PBA_ERR_INVALID_ARG;
   if (!known_dtype(d->dtype)) return PBA_ERR_UNSUPPORTED;
   const int buckets = d->rows - (groups ? 1 : 0);
@@ -107,7 +109,7 @@ void fill_relpos(pba::RelposParams &p, const pba_relpos_desc *d, const int32_t *
   r.cross = groups ? buckets : -1;
   r.kind = d->rule;
   if (d->rule == PBA_RELPOS_CLIP) {
-    r.radius = buckets / 2;
+    r.far = buckets / 2;
     return;
   }
   r.side = d->rule == PBA_RELPOS_LOG ? buckets / 2 : buckets;
@@ -115,6 +117,7 @@ void fill_relpos(pba::RelposParams &p, const pba_relpos_desc *d, const int32_t *
   r.n_borders = r.side - r.exact - 1;
   for (int t = 1; t <= r.n_borders; ++t)
     r.borders[t - 1] = log_border(r.exact, r.side - r.exact, t, d->max_distance);
+  r.far = r.n_borders > 0 ? r.borders[r.n_borders - 1] : r.exact;
 }
 
 // Rows of 8-element chunks that start on 16 bytes each.
@@ -148,22 +151,25 @@ struct GradPlan {
 };
 GradPlan grad_plan(const pba_relpos_desc *d) {
   GradPlan g;
-  const int borders = pba::kRelposMaxBorders * 4;
-  // as many threads as columns of `rows` floats fit in a block's shared memory
+  // as many threads as columns of `rows` floats and the widest ring fit in a
+  // block's shared memory
+  const int lookup = (pba::kRelposLutFar + 1) * 4;  // the largest
+  const int per_thread = d->rows * 4 + pba::RelposGradRing<pba::F32, false>::kThreadBytes;
   g.threads = pba::kRelposGradThreads;
-  while (g.threads > 32 && d->rows * g.threads * 4 + borders > kRelposSmem) g.threads /= 2;
-  g.smem = d->rows * g.threads * 4 + borders;
+  while (g.threads > 32 && per_thread * g.threads + lookup > kRelposSmem) g.threads /= 2;
+  g.smem = per_thread * g.threads;
   const int64_t chunks = ceil_div(d->Nk, 8);
   const int64_t cols = std::min<int64_t>(g.threads, pow2_ceil(chunks));
   g.cols_log2 = 0;
   while ((int64_t(1) << g.cols_log2) < cols) ++g.cols_log2;
   g.col_blocks = int(ceil_div(chunks, cols));
   const int64_t lanes = g.threads / cols;
-  // queries are split until the card is full, a thread has at least four, and
-  // none has over 512 (which bounds the error of its fp32 sums)
-  const int64_t resident = std::min<int64_t>(8, 227 * 1024 / (g.smem + 1024));
-  const int64_t want = ceil_div(kPlanSms * resident, d->H * d->B * g.col_blocks);
-  const int64_t most = ceil_div(d->Nq, lanes * 4), least = ceil_div(d->Nq, lanes * 512);
+  // queries are split until the card is full once, a thread has at least eight
+  // (a full ring), and none has over 512 (which bounds the error of its fp32
+  // sums)
+  const int64_t resident = std::min<int64_t>(kRelposGradResident, 227 * 1024 / (g.smem + 1024));
+  const int64_t want = kPlanSms * resident / (d->H * d->B * g.col_blocks);
+  const int64_t most = ceil_div(d->Nq, lanes * 8), least = ceil_div(d->Nq, lanes * 512);
   g.row_splits = int(std::max<int64_t>(1, std::max(least, std::min(most, want))));
   g.splits = d->B * g.col_blocks * g.row_splits;
   return g;
@@ -176,7 +182,9 @@ cudaError_t launch_relpos_grad(const pba::RelposParams &p, const GradPlan &g, cu
   const cudaError_t attr_err = once_per_device(
       once, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRelposSmem); });
   if (attr_err != cudaSuccess) return attr_err;
-  kern<<<dim3(unsigned(g.col_blocks * g.row_splits), unsigned(p.H), unsigned(p.B)), g.threads, g.smem, stream>>>(p);
+  const int smem = g.threads * (p.rows * 4 + pba::RelposGradRing<T, kVec>::kThreadBytes) +
+                   pba::relpos_lookup_words(p.rule) * 4;
+  kern<<<dim3(unsigned(g.col_blocks * g.row_splits), unsigned(p.H), unsigned(p.B)), g.threads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -295,14 +303,16 @@ pba_status pba_relpos_bias_forward(const pba_relpos_desc *desc, const int32_t *q
   // Heads per block: all that fit (the rows of the table are found once for
   // them all), fewer when that would leave SMs without a block.
   const int per_word = d.dtype == PBA_BF16 ? 2 : 1;
-  const int64_t fit = (kRelposSmem / 4 - p.rule.n_borders) / d.rows * per_word;
-  const int64_t blocks = ceil_div(d.B * d.Nq * ceil_div(d.Nk, 8), pba::kRelposThreads);
+  const int lookup = pba::relpos_lookup_words(p.rule);
+  const int64_t fit = (kRelposSmem / 4 - lookup) / d.rows * per_word;
+  const int64_t blocks = vec ? ceil_div(d.B * d.Nq * ceil_div(d.Nk, 8), pba::kRelposThreads)
+                             : ceil_div(d.B * d.Nq * ceil_div(d.Nk, 256), pba::kRelposThreads / 32);
   int64_t heads = std::min<int64_t>(d.H, fit);
   if (blocks * ceil_div(d.H, heads) < 2 * kPlanSms)
     heads = std::min(heads, std::max<int64_t>(per_word, d.H * blocks / (2 * kPlanSms) / per_word * per_word));
   if (heads < d.H) heads = std::max<int64_t>(per_word, heads / per_word * per_word);
   p.heads_per_block = int(heads);
-  const int smem = int((p.rule.n_borders + ceil_div(heads, per_word) * d.rows) * 4);
+  const int smem = int((lookup + ceil_div(heads, per_word) * d.rows) * 4);
   // a block stages its table once and then walks over its share of the rows
   const dim3 grid(unsigned(std::min<int64_t>(blocks, 8 * kPlanSms)), unsigned(ceil_div(d.H, heads)));
   cudaStream_t st = static_cast<cudaStream_t>(stream_ptr);

@@ -41,10 +41,10 @@ struct NormParams {
   float *part;               // backward: [blocks][kNormParams][C]
 };
 
-// Channel `c` ... of a per-channel parameter as fp32 (0 past the end).
-// Parameters stay in L1: they are read for every row.
+// A thread's channels of a per-channel parameter as fp32 (0 past the end), in
+// the order of load8.  Parameters stay in L1: they are read for every row.
 template <bool kVec>
-__device__ __forceinline__ void param8(const void *p, bool f32, int c, int n, float (&x)[8]) {
+__device__ __forceinline__ void param8(const void *p, bool f32, int c, int n, int step, float (&x)[8]) {
   if (f32) {
     const float *q = static_cast<const float *>(p) + c;
     if (kVec && n >= 8) {
@@ -52,7 +52,7 @@ __device__ __forceinline__ void param8(const void *p, bool f32, int c, int n, fl
       x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = e < n ? __ldg(q + e) : 0.f;
+      for (int e = 0; e < 8; ++e) x[e] = e < n ? __ldg(q + (kVec ? e : e * step)) : 0.f;
     }
   } else {
     const uint16_t *q = static_cast<const uint16_t *>(p) + c;
@@ -60,9 +60,22 @@ __device__ __forceinline__ void param8(const void *p, bool f32, int c, int n, fl
       unpack8(__ldg(reinterpret_cast<const uint4 *>(q)), x);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = e < n ? Bf16::to_f32(__ldg(q + e)) : 0.f;
+      for (int e = 0; e < 8; ++e) x[e] = e < n ? Bf16::to_f32(__ldg(q + (kVec ? e : e * step))) : 0.f;
     }
   }
+}
+
+// A thread's first channel, and how many of its eight exist (none for a thread
+// past the end, which still takes part in the sums): eight consecutive ones,
+// or every blockDim.x-th.
+template <bool kVec>
+__device__ __forceinline__ int norm_first() {
+  return kVec ? threadIdx.x * 8 : threadIdx.x;
+}
+template <bool kVec>
+__device__ __forceinline__ int norm_count(int C) {
+  const int left = C - norm_first<kVec>();
+  return max(0, kVec ? min(8, left) : (left + int(blockDim.x) - 1) / int(blockDim.x));
 }
 
 // Sums of N values over the threads of a row.  kWide: the row is the block
@@ -126,12 +139,12 @@ __device__ __forceinline__ float centre(float (&x)[8], int n, const NormParams &
 __device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
 template <typename T, bool kVec, int kThreads>
-__global__ void __launch_bounds__(kThreads) block_norm_fwd_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) block_norm_fwd_kernel(const __grid_constant__ NormParams p) {
   using W = typename T::Word;
   constexpr bool kWide = kThreads > kNormNarrowThreads;
   __shared__ float buf[kWide ? 2 * 32 : 1];
   const int lanes = blockDim.x;                        // threads of a row
-  const int c = threadIdx.x * 8, n = min(8, p.C - c);     // may be <= 0: idle, but takes part in the sums
+  const int c = norm_first<kVec>(), n = norm_count<kVec>(p.C);
   RowSum<kWide, 1> sum{buf, lanes, 0};
   const int64_t step = int64_t(gridDim.x) * blockDim.y;
   // every thread of a warp runs the same number of rounds: a row past the
@@ -140,18 +153,18 @@ __global__ void __launch_bounds__(kThreads) block_norm_fwd_kernel(const __grid_c
     const int64_t r = r0 + threadIdx.y;
     const int m = r < p.rows ? n : 0;
     float h[8], u[8], g[8];
-    load8<T, kVec>(static_cast<const W *>(p.x) + r * p.x_s + c, m, h);
+    load8<T, kVec>(static_cast<const W *>(p.x) + r * p.x_s + c, m, lanes, h);
     if (p.f != nullptr) {
-      load8<T, kVec>(static_cast<const W *>(p.f) + r * p.f_s + c, m, u);
-      if (p.gate != nullptr) load8<T, kVec>(static_cast<const W *>(p.gate) + r * p.gate_s + c, m, g);
+      load8<T, kVec>(static_cast<const W *>(p.f) + r * p.f_s + c, m, lanes, u);
+      if (p.gate != nullptr) load8<T, kVec>(static_cast<const W *>(p.gate) + r * p.gate_s + c, m, lanes, g);
       if (p.post_w != nullptr) {
         const float rs = centre(u, m, p, sum);
         float w[8];
-        param8<kVec>(p.post_w, p.param_f32, c, m, w);
+        param8<kVec>(p.post_w, p.param_f32, c, m, lanes, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) u[e] *= rs * w[e];
         if (p.post_b != nullptr) {
-          param8<kVec>(p.post_b, p.param_f32, c, m, w);
+          param8<kVec>(p.post_b, p.param_f32, c, m, lanes, w);
 #pragma unroll
           for (int e = 0; e < 8; ++e) u[e] += w[e];
         }
@@ -161,26 +174,26 @@ __global__ void __launch_bounds__(kThreads) block_norm_fwd_kernel(const __grid_c
         for (int e = 0; e < 8; ++e) u[e] *= sigmoid_f32(g[e]);
       }
       if (p.scale != nullptr) {
-        param8<kVec>(p.scale, p.param_f32, c, m, g);
+        param8<kVec>(p.scale, p.param_f32, c, m, lanes, g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) u[e] *= g[e];
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[e] += u[e];
-      store8<T, kVec>(static_cast<W *>(p.h) + r * p.h_s + c, m, h);
+      store8<T, kVec>(static_cast<W *>(p.h) + r * p.h_s + c, m, lanes, h);
     }
     if (p.pre_w != nullptr) {
       const float rs = centre(h, m, p, sum);
       float w[8];
-      param8<kVec>(p.pre_w, p.param_f32, c, m, w);
+      param8<kVec>(p.pre_w, p.param_f32, c, m, lanes, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[e] *= rs * w[e];
       if (p.pre_b != nullptr) {
-        param8<kVec>(p.pre_b, p.param_f32, c, m, w);
+        param8<kVec>(p.pre_b, p.param_f32, c, m, lanes, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] += w[e];
       }
-      store8<T, kVec>(static_cast<W *>(p.y) + r * p.y_s + c, m, h);
+      store8<T, kVec>(static_cast<W *>(p.y) + r * p.y_s + c, m, lanes, h);
     }
   }
 }
@@ -193,12 +206,12 @@ __global__ void __launch_bounds__(kThreads) block_norm_fwd_kernel(const __grid_c
 // anyway.  Sums over rows stay in each thread's registers for its channels,
 // then per block in shared memory, then in `part`, always in the same order.
 template <typename T, bool kVec, int kThreads>
-__global__ void __launch_bounds__(kThreads) block_norm_bwd_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) block_norm_bwd_kernel(const __grid_constant__ NormParams p) {
   using W = typename T::Word;
   constexpr bool kWide = kThreads > kNormNarrowThreads;
   __shared__ float buf[kWide ? 2 * 2 * 32 : kNormNarrowThreads * 8];
   const int lanes = blockDim.x;
-  const int c = threadIdx.x * 8, n = min(8, p.C - c);
+  const int c = norm_first<kVec>(), n = norm_count<kVec>(p.C);
   RowSum<kWide, 2> sum{buf, lanes, 0};
   const int64_t step = int64_t(gridDim.x) * blockDim.y;
   float acc[kNormParams][8] = {};
@@ -207,22 +220,22 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_kernel(const __grid_c
     const int m = r < p.rows ? n : 0;
     float t[8], h[8], dy[8], f[8], g[8], w[8];
     if (p.dh != nullptr) {
-      load8<T, kVec>(static_cast<const W *>(p.dh) + r * p.dh_s + c, m, t);
+      load8<T, kVec>(static_cast<const W *>(p.dh) + r * p.dh_s + c, m, lanes, t);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) t[e] = 0.f;
     }
     if (p.pre_w != nullptr) {
-      load8<T, kVec>(static_cast<const W *>(p.h) + r * p.h_s + c, m, h);
-      load8<T, kVec>(static_cast<const W *>(p.dy) + r * p.dy_s + c, m, dy);
+      load8<T, kVec>(static_cast<const W *>(p.h) + r * p.h_s + c, m, lanes, h);
+      load8<T, kVec>(static_cast<const W *>(p.dy) + r * p.dy_s + c, m, lanes, dy);
     }
     if (p.f != nullptr) {
-      load8<T, kVec>(static_cast<const W *>(p.f) + r * p.f_s + c, m, f);
-      if (p.gate != nullptr) load8<T, kVec>(static_cast<const W *>(p.gate) + r * p.gate_s + c, m, g);
+      load8<T, kVec>(static_cast<const W *>(p.f) + r * p.f_s + c, m, lanes, f);
+      if (p.gate != nullptr) load8<T, kVec>(static_cast<const W *>(p.gate) + r * p.gate_s + c, m, lanes, g);
     }
     if (p.pre_w != nullptr) {
       const float rs = centre(h, m, p, sum);
-      param8<kVec>(p.pre_w, p.param_f32, c, m, w);
+      param8<kVec>(p.pre_w, p.param_f32, c, m, lanes, w);
       float v[2] = {0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -238,13 +251,13 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_kernel(const __grid_c
 #pragma unroll
       for (int e = 0; e < 8; ++e) t[e] = fmaf(rs, dy[e] - a - h[e] * b, t[e]);
     }
-    store8<T, kVec>(static_cast<W *>(p.dx) + r * p.dx_s + c, m, t);
+    store8<T, kVec>(static_cast<W *>(p.dx) + r * p.dx_s + c, m, lanes, t);
     if (p.f != nullptr) {
       float rs = 1.f;
       float u[8];
       if (p.post_w != nullptr) {
         rs = centre(f, m, p, sum);
-        param8<kVec>(p.post_w, p.param_f32, c, m, w);
+        param8<kVec>(p.post_w, p.param_f32, c, m, lanes, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           f[e] *= rs;
@@ -252,7 +265,7 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_kernel(const __grid_c
         }
         if (p.post_b != nullptr) {
           float pb[8];
-          param8<kVec>(p.post_b, p.param_f32, c, m, pb);
+          param8<kVec>(p.post_b, p.param_f32, c, m, lanes, pb);
 #pragma unroll
           for (int e = 0; e < 8; ++e) u[e] += pb[e];
         }
@@ -262,7 +275,7 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_kernel(const __grid_c
       }
       float sc[8];
       if (p.scale != nullptr) {
-        param8<kVec>(p.scale, p.param_f32, c, m, sc);
+        param8<kVec>(p.scale, p.param_f32, c, m, lanes, sc);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) sc[e] = 1.f;
@@ -276,7 +289,7 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_kernel(const __grid_c
         g[e] = t[e] * u[e] * s * (1.f - s);
         t[e] *= s;
       }
-      if (p.gate != nullptr) store8<T, kVec>(static_cast<W *>(p.dgate) + r * p.dgate_s + c, m, g);
+      if (p.gate != nullptr) store8<T, kVec>(static_cast<W *>(p.dgate) + r * p.dgate_s + c, m, lanes, g);
       if (p.post_w != nullptr) {
         float v[2] = {0.f, 0.f};
 #pragma unroll
@@ -292,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_kernel(const __grid_c
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] = rs * (t[e] - a - f[e] * b);
       }
-      store8<T, kVec>(static_cast<W *>(p.df) + r * p.df_s + c, m, t);
+      store8<T, kVec>(static_cast<W *>(p.df) + r * p.df_s + c, m, lanes, t);
     }
   }
   // the block's sums: its rows' threads of a channel added in order
@@ -318,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_kernel(const __grid_c
     if (kWide || threadIdx.y == 0) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (e < n) dst[e] = acc[k][e];
+        if (e < n) dst[kVec ? e : e * lanes] = acc[k][e];
     }
   }
 }

@@ -20,13 +20,14 @@
 namespace pba {
 
 constexpr int kRelposMaxRows = 1025;     // rows of the table
+constexpr int kRelposLutFar = 2048;      // farthest last border that is looked up by distance
 constexpr int kRelposMaxBorders = 512;   // borders of the logarithmic rows of one side
 constexpr int kRelposThreads = 256;
 constexpr int kRelposGradThreads = 128;
 
 struct RelposRule {
   int32_t kind;       // 0 clipped, 1 logarithmic on both sides, 2 logarithmic, keys behind the query
-  int32_t radius;     // clipped: rows are clamp(rel, -radius, radius) + radius
+  int32_t far;        // a distance at or past it lies in the last row of its side (clipped: the radius)
   int32_t exact;      // logarithmic: distances below it have rows of their own
   int32_t side;       // logarithmic: rows of one side
   int32_t n_borders;  // side - exact - 1
@@ -53,16 +54,30 @@ struct RelposParams {
   RelposRule rule;
 };
 
-// Row of the table for a distance rel = k_pos - q_pos (saturated, so that
-// positions at the ends of the 32-bit range keep their order).
 __device__ __forceinline__ int sub_sat(int a, int b) {
   int r;
   asm("sub.sat.s32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ int relpos_row(const RelposRule &r, const int *borders, int rel) {
-  if (r.kind == 0) return min(max(rel, -r.radius), r.radius) + r.radius;
-  rel = max(rel, -2147483647);
+__device__ __forceinline__ int add_sat(int a, int b) {
+  int r;
+  asm("add.sat.s32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The table's row of a distance rel in [-far, far]; every distance beyond has
+// the row of the nearer end.  Clipped: rel + far.  Logarithmic: looked up in
+// shared memory, by distance where that table is small enough (lut, 2 far + 1
+// entries), else by searching the borders.
+struct RelposLookup {
+  const uint16_t *lut;
+  const int *borders;
+};
+// Words of shared memory that the lookup needs.
+__host__ __device__ inline int relpos_lookup_words(const RelposRule &r) {
+  return r.kind == 0 ? 0 : (r.far <= kRelposLutFar ? r.far + 1 : r.n_borders);
+}
+__device__ __forceinline__ int relpos_search(const RelposRule &r, const int *borders, int rel) {
   const int d = r.kind == 1 ? abs(rel) : max(-rel, 0);
   int row = d;
   if (d >= r.exact) {
@@ -79,19 +94,39 @@ __device__ __forceinline__ int relpos_row(const RelposRule &r, const int *border
   }
   return row + ((r.kind == 1 && rel > 0) ? r.side : 0);
 }
+// Filled by the whole block; the caller synchronises.
+__device__ __forceinline__ RelposLookup relpos_lookup(const RelposRule &r, uint32_t *smem, int tid, int threads) {
+  if (r.kind != 0) {
+    if (r.far <= kRelposLutFar) {
+      for (int i = tid; i <= 2 * r.far; i += threads)
+        reinterpret_cast<uint16_t *>(smem)[i] = uint16_t(relpos_search(r, r.borders, i - r.far));
+    } else {
+      for (int i = tid; i < r.n_borders; i += threads) smem[i] = uint32_t(r.borders[i]);
+    }
+  }
+  return RelposLookup{reinterpret_cast<const uint16_t *>(smem), reinterpret_cast<const int *>(smem)};
+}
+__device__ __forceinline__ int relpos_row(const RelposRule &r, const RelposLookup &look, int rel) {
+  if (r.kind == 0) return rel + r.far;
+  if (r.far <= kRelposLutFar) return look.lut[rel + r.far];
+  return relpos_search(r, look.borders, rel);
+}
 
-// The positions (or groups) of keys c .. c+7, those past Nk as the last key.
+// The positions (or groups) of a thread's eight keys, in the order of load8;
+// those past the row as its last key.
+template <bool kVec>
 __device__ __forceinline__ void load_keys8(const int32_t *p, int c, int Nk, bool vec, int (&k)[8]) {
-  if (vec && c + 8 <= Nk) {
+  if (kVec && vec && c + 8 <= Nk) {
     const int4 a = __ldg(reinterpret_cast<const int4 *>(p + c)), b = __ldg(reinterpret_cast<const int4 *>(p + c + 4));
     k[0] = a.x, k[1] = a.y, k[2] = a.z, k[3] = a.w, k[4] = b.x, k[5] = b.y, k[6] = b.z, k[7] = b.w;
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) k[e] = __ldg(p + min(c + e, Nk - 1));
+    for (int e = 0; e < 8; ++e) k[e] = __ldg(p + min(kVec ? c + e : c + 32 * e, Nk - 1));
   }
 }
 
-// Forward.  A thread owns eight consecutive keys of one (batch, query): it
+// Forward.  A thread owns eight keys of one (batch, query), consecutive ones
+// or, on rows that start anywhere, every 32nd of the 256 that its warp owns: it
 // finds their eight rows once and writes them for every head of the block.
 // The block's columns of the table wait in shared memory, row-contiguous, so
 // that neighbouring distances fall into neighbouring banks; bf16 keeps two
@@ -101,12 +136,11 @@ __global__ void __launch_bounds__(kRelposThreads) relpos_fwd_kernel(const __grid
   constexpr bool kBf = sizeof(typename T::Word) == 2;
   constexpr int kHeadsPerWord = kBf ? 2 : 1;
   extern __shared__ uint32_t relpos_smem[];
-  int *borders = reinterpret_cast<int *>(relpos_smem);
-  uint32_t *tab = relpos_smem + p.rule.n_borders;
+  uint32_t *tab = relpos_smem + relpos_lookup_words(p.rule);
+  const RelposLookup look = relpos_lookup(p.rule, relpos_smem, threadIdx.x, kRelposThreads);
   const int h0 = blockIdx.y * p.heads_per_block;
   const int nh = min(p.heads_per_block, p.H - h0);
   const int words = (nh + kHeadsPerWord - 1) / kHeadsPerWord;
-  for (int i = threadIdx.x; i < p.rule.n_borders; i += kRelposThreads) borders[i] = p.rule.borders[i];
   for (int i = threadIdx.x; i < words * p.rows; i += kRelposThreads) {
     const int w = i / p.rows, r = i - w * p.rows;
     if (kBf) {
@@ -118,26 +152,32 @@ __global__ void __launch_bounds__(kRelposThreads) relpos_fwd_kernel(const __grid
   }
   __syncthreads();
 
-  const int chunks = (p.Nk + 7) >> 3;
+  // a unit is a thread's eight keys, or a warp's 256
+  const int lane = threadIdx.x & 31;
+  const int chunks = kVec ? (p.Nk + 7) >> 3 : (p.Nk + 255) >> 8;
   const int64_t total = int64_t(p.B) * p.Nq * chunks;
-  const int64_t first = int64_t(blockIdx.x) * kRelposThreads + threadIdx.x;
-  const int64_t step = int64_t(gridDim.x) * kRelposThreads;
+  const int units = kVec ? kRelposThreads : kRelposThreads / 32;  // of a block
+  const int64_t first = int64_t(blockIdx.x) * units + (kVec ? threadIdx.x : threadIdx.x >> 5);
+  const int64_t step = int64_t(gridDim.x) * units;
   if (first >= total) return;
   // (batch, query) row and key chunk, advanced without a division
   int row = int(first / chunks), col = int(first - int64_t(row) * chunks);
   const int drow = int(step / chunks), dcol = int(step - int64_t(drow) * chunks);
   for (int64_t at = first; at < total; at += step) {
     const int b = row / p.Nq, i = row - b * p.Nq;
-    const int c = col * 8, n = min(8, p.Nk - c);
+    const int c = kVec ? col * 8 : col * 256 + lane;
+    const int n = kVec ? min(8, p.Nk - c) : max(0, min(8, (p.Nk - c + 31) >> 5));
     int r[8];
     {
       int k[8];
-      load_keys8(p.k_pos + b * p.k_sb, c, p.Nk, p.pos_vec != 0, k);
+      load_keys8<kVec>(p.k_pos + b * p.k_sb, c, p.Nk, p.pos_vec != 0, k);
       const int q = __ldg(p.q_pos + b * p.q_sb + i);
+      // distances are clamped before they are taken: no overflow wherever the positions lie
+      const int q_lo = sub_sat(q, p.rule.far), q_hi = add_sat(q, p.rule.far);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r[e] = relpos_row(p.rule, borders, sub_sat(k[e], q));
+      for (int e = 0; e < 8; ++e) r[e] = relpos_row(p.rule, look, min(max(k[e], q_lo), q_hi) - q);
       if (p.rule.cross >= 0) {
-        load_keys8(p.k_group + b * p.kg_sb, c, p.Nk, p.pos_vec != 0, k);
+        load_keys8<kVec>(p.k_group + b * p.kg_sb, c, p.Nk, p.pos_vec != 0, k);
         const int qg = __ldg(p.q_group + b * p.qg_sb + i);
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[e] = k[e] == qg ? r[e] : p.rule.cross;
@@ -159,13 +199,13 @@ __global__ void __launch_bounds__(kRelposThreads) relpos_fwd_kernel(const __grid
         const int h = w * kHeadsPerWord + s;
         if (h >= nh) break;
         float x[8];
-        if (kBase) load8<T, kVec>(base + h * p.base_s[1], n, x);
+        if (kBase) load8<T, kVec>(base + h * p.base_s[1], n, 32, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float tv = !kBf ? __uint_as_float(v[e]) : (s == 0 ? bf16lo_to_f32(v[e]) : bf16hi_to_f32(v[e]));
           x[e] = kBase ? x[e] + tv : tv;
         }
-        store8<T, kVec>(out + h * p.out_s[1], n, x);
+        store8<T, kVec>(out + h * p.out_s[1], n, 32, x);
       }
     }
     row += drow;
@@ -178,20 +218,38 @@ __global__ void __launch_bounds__(kRelposThreads) relpos_fwd_kernel(const __grid
 }
 
 // Backward.  A block takes one head, a block of keys and a share of the
-// queries; a thread keeps eight keys and walks down the queries.  Most eights
-// lie wholly in one of three rows: past the last border on either side, or in
-// another group.  Their sums stay in three registers.  The others go element
-// by element into the thread's own column of a table in shared memory, so no
-// two threads ever add to the same word and the order of every sum is fixed.
-// The columns are added at the end of the block, the blocks' tables by
-// relpos_grad_sum_kernel.
+// queries; a thread keeps eight consecutive keys and walks down the queries,
+// its next rows on their way into its own ring in shared memory.
+// While the queries' group stays the same, so does the set of the eight that
+// share it: the others' values go to the row of different groups, kept in
+// registers.  The set itself mostly lies past the last border on one side, and
+// those two sums stay in registers as well.  Only near the diagonal are the
+// values added one by one, into the thread's own column of a table in shared
+// memory; a block's queries lie row_splits apart, so that every block meets its
+// share of the diagonal.  No two threads add to the same word, and the order of
+// every sum is fixed.  The columns are added at the end of the block, the
+// blocks' tables by relpos_grad_sum_kernel.
 template <typename T, bool kVec>
-__global__ void relpos_grad_kernel(const __grid_constant__ RelposParams p) {
-  extern __shared__ uint32_t relpos_smem[];
-  int *borders = reinterpret_cast<int *>(relpos_smem);
-  float *hist = reinterpret_cast<float *>(relpos_smem + p.rule.n_borders);
+struct RelposGradRing {
+  using R = Ring8<T, kVec>;
+  static constexpr int kStages = 8;
+  static constexpr int kSlotBytes = R::kSlotWords * 16 + 8;  // and the query's position and group
+  static constexpr int kThreadBytes = kStages * kSlotBytes;
+};
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kRelposGradThreads, 5) relpos_grad_kernel(const __grid_constant__ RelposParams p) {
+  using Ring = RelposGradRing<T, kVec>;
+  using R = typename Ring::R;
+  extern __shared__ __align__(16) uint8_t relpos_grad_smem[];
   const int threads = blockDim.x, tid = threadIdx.x;
-  for (int i = tid; i < p.rule.n_borders; i += threads) borders[i] = p.rule.borders[i];
+  // [stage][word][thread] 16-byte words, [stage][thread] positions and groups,
+  // the lookup, [row][thread] sums
+  uint8_t *ring = relpos_grad_smem + tid * 16;
+  int2 *ring_q = reinterpret_cast<int2 *>(relpos_grad_smem + threads * Ring::kStages * R::kSlotWords * 16) + tid;
+  uint32_t *look_smem = reinterpret_cast<uint32_t *>(relpos_grad_smem + threads * Ring::kThreadBytes);
+  float *hist = reinterpret_cast<float *>(look_smem + relpos_lookup_words(p.rule));
+  const RelposLookup look = relpos_lookup(p.rule, look_smem, tid, threads);
   for (int i = tid; i < p.rows * threads; i += threads) hist[i] = 0.f;
   __syncthreads();
 
@@ -202,67 +260,107 @@ __global__ void relpos_grad_kernel(const __grid_constant__ RelposParams p) {
   const int lanes = threads >> p.cols_log2, lane_row = tid >> p.cols_log2;
   const int n = min(8, p.Nk - c);
   if (n > 0) {
-    // a distance at or past these lies in the last row of its side
     const RelposRule &rule = p.rule;
-    const int far = rule.kind == 0 ? rule.radius : (rule.n_borders > 0 ? rule.borders[rule.n_borders - 1] : rule.exact);
     // one-sided: keys ahead of the query all share row 0
-    const int far_hi = rule.kind == 2 ? 0 : far;
-    const int row_lo = rule.kind == 0 ? 0 : rule.side - 1;
-    const int row_hi = rule.kind == 0 ? 2 * rule.radius : (rule.kind == 1 ? 2 * rule.side - 1 : 0);
-    int k[8], kg[8];
-    load_keys8(p.k_pos + b * p.k_sb, c, p.Nk, p.pos_vec != 0, k);
+    const int far = rule.far, far_hi = rule.kind == 2 ? 0 : far;
     const bool groups = rule.cross >= 0;
-    if (groups) load_keys8(p.k_group + b * p.kg_sb, c, p.Nk, p.pos_vec != 0, kg);
-    int k_min = k[0], k_max = k[0];
-    bool one_group = true;
+    // The keys' positions and groups are read again (from L1) where single
+    // ones are needed; what stays in registers are the weights 1 and 0 of the
+    // eight's members of the queries' group, and the members' range.
+    const int32_t *kp = p.k_pos + b * p.k_sb, *kgp = groups ? p.k_group + b * p.kg_sb : nullptr;
+    float2 in[4] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f), make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
+    int k_min, k_max;
+    {
+      int k[8];
+      load_keys8<true>(kp, c, p.Nk, p.pos_vec != 0, k);
+      k_min = k_max = k[0];
 #pragma unroll
-    for (int e = 1; e < 8; ++e) {
-      k_min = min(k_min, k[e]);
-      k_max = max(k_max, k[e]);
-      if (groups) one_group = one_group && kg[e] == kg[0];
+      for (int e = 1; e < 8; ++e) {
+        k_min = min(k_min, k[e]);
+        k_max = max(k_max, k[e]);
+      }
     }
-    float lo = 0.f, hi = 0.f, cross = 0.f;
-    const int per = (p.Nq + p.row_splits - 1) / p.row_splits;
-    const int i_end = min(p.Nq, (row_split + 1) * per);
+    bool outside = false;  // some are of another group
+    int group = 0;
+    bool first = true;
+    float2 lo[4] = {}, hi[4] = {}, cross[4] = {};
     using W = typename T::Word;
     const W *src = static_cast<const W *>(p.out) + b * p.out_s[0] + h * p.out_s[1] + c;
     const int32_t *qp = p.q_pos + b * p.q_sb, *qgp = groups ? p.q_group + b * p.qg_sb : nullptr;
-    constexpr int kAhead = 4;
-    for (int i0 = row_split * per + lane_row; i0 < i_end; i0 += kAhead * lanes) {
-      float x[kAhead][8];
-      int q[kAhead], qg[kAhead];
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const int i = i0 + a * lanes;
-        if (i < i_end) {
-          load8<T, kVec>(src + int64_t(i) * p.out_s[2], n, x[a]);
-          q[a] = __ldg(qp + i);
-          qg[a] = groups ? __ldg(qgp + i) : 0;
-        }
+    const bool inner = c >= 8 && c + 16 <= p.Nk;
+    const int step = lanes * p.row_splits, begin = row_split * lanes + lane_row;
+    auto fetch = [&](int i, int s) {
+      if (i < p.Nq) {
+        R::fetch(ring + s * R::kSlotWords * threads * 16, threads * 16, src + int64_t(i) * p.out_s[2], n, inner);
+        cp_async4(&ring_q[s * threads].x, qp + i);
+        if (groups) cp_async4(&ring_q[s * threads].y, qgp + i);
       }
+      cp_async_commit();
+    };
+    for (int s = 0; s < Ring::kStages; ++s) fetch(begin + s * step, s);
+    int s = 0;
+    for (int i = begin; i < p.Nq; i += step) {
+      cp_async_wait<Ring::kStages - 1>();
+      const Raw8<T> x = R::take(ring + s * R::kSlotWords * threads * 16, threads * 16,
+                                src + int64_t(i) * p.out_s[2], inner);
+      const int2 qq = ring_q[s * threads];
+      fetch(i + Ring::kStages * step, s);
+      s = s + 1 == Ring::kStages ? 0 : s + 1;
+      if (groups && (first || qq.y != group)) {
+        first = false;
+        group = qq.y;
+        // no member: any place will do, its weights are 0
+        k_min = 2147483647, k_max = -2147483647 - 1;
+        outside = false;
+        int k[8], kg[8];
+        load_keys8<true>(kp, c, p.Nk, p.pos_vec != 0, k);
+        load_keys8<true>(kgp, c, p.Nk, p.pos_vec != 0, kg);
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        if (i0 + a * lanes >= i_end) break;
-        const float sum = ((x[a][0] + x[a][1]) + (x[a][2] + x[a][3])) + ((x[a][4] + x[a][5]) + (x[a][6] + x[a][7]));
-        if (groups && one_group && kg[0] != qg[a]) {
-          cross += sum;
-        } else if ((!groups || one_group) && sub_sat(k_min, q[a]) >= far_hi) {
-          hi += sum;
-        } else if ((!groups || one_group) && sub_sat(k_max, q[a]) <= -far) {
-          lo += sum;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            int r = relpos_row(rule, borders, sub_sat(k[e], q[a]));
-            if (groups && kg[e] != qg[a]) r = rule.cross;
-            hist[r * threads + tid] += x[a][e];
+        for (int e = 0; e < 8; ++e) {
+          const bool member = kg[e] == group;
+          outside = outside || !member;
+          const float weight = member ? 1.f : 0.f;
+          if (e & 1)
+            in[e >> 1].y = weight;
+          else
+            in[e >> 1].x = weight;
+          if (member) {
+            k_min = min(k_min, k[e]);
+            k_max = max(k_max, k[e]);
           }
         }
       }
+      if (outside) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          cross[e] = ffma2(x.pair(e), make_float2(1.f - in[e].x, 1.f - in[e].y), cross[e]);
+      }
+      if (sub_sat(k_min, qq.x) >= far_hi) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) hi[e] = ffma2(x.pair(e), in[e], hi[e]);
+      } else if (sub_sat(k_max, qq.x) <= -far) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) lo[e] = ffma2(x.pair(e), in[e], lo[e]);
+      } else {
+        int k[8], r[8];
+        load_keys8<true>(kp, c, p.Nk, p.pos_vec != 0, k);
+        const int q_lo = sub_sat(qq.x, far), q_hi = add_sat(qq.x, far);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = relpos_row(rule, look, min(max(k[e], q_lo), q_hi) - qq.x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if ((e & 1 ? in[e >> 1].y : in[e >> 1].x) != 0.f)
+            hist[r[e] * threads + tid] += e & 1 ? x.pair(e >> 1).y : x.pair(e >> 1).x;
+      }
     }
-    hist[row_lo * threads + tid] += lo;
-    hist[row_hi * threads + tid] += hi;
-    if (groups) hist[rule.cross * threads + tid] += cross;
+    cp_async_wait<0>();
+    auto add = [&](int r, const float2 (&v)[4]) {
+      const float2 s = fadd2(fadd2(v[0], v[1]), fadd2(v[2], v[3]));
+      hist[r * threads + tid] += s.x + s.y;
+    };
+    add(rule.kind == 0 ? 0 : rule.side - 1, lo);
+    add(rule.kind == 0 ? 2 * rule.far : (rule.kind == 1 ? 2 * rule.side - 1 : 0), hi);
+    if (groups) add(rule.cross, cross);
   }
   __syncthreads();
   const int warp = tid >> 5, lane = tid & 31, warps = threads >> 5;
