@@ -23,7 +23,7 @@ constexpr int64_t kPlanSms = 148;
 // Dynamic shared memory that the relative position kernels may ask for.
 constexpr int kRelposSmem = 200 * 1024;
 // Blocks of the table's gradient on an SM.
-constexpr int64_t kRelposGradResident = 5;
+constexpr int64_t kRelposGradResident = 4;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t pow2_ceil(int64_t x) {
@@ -146,7 +146,7 @@ cudaError_t dispatch_relpos(const pba::RelposParams &p, bool vec, dim3 grid, int
 
 // Launch shape of the table's gradient.
 struct GradPlan {
-  int threads, cols_log2, col_blocks, row_splits, smem;
+  int threads, cols_log2, col_blocks, row_splits;
   int64_t splits;  // tables per head
 };
 GradPlan grad_plan(const pba_relpos_desc *d) {
@@ -157,7 +157,6 @@ GradPlan grad_plan(const pba_relpos_desc *d) {
   const int per_thread = d->rows * 4 + pba::RelposGradRing<pba::F32, false>::kThreadBytes;
   g.threads = pba::kRelposGradThreads;
   while (g.threads > 32 && per_thread * g.threads + lookup > kRelposSmem) g.threads /= 2;
-  g.smem = per_thread * g.threads;
   const int64_t chunks = ceil_div(d->Nk, 8);
   const int64_t cols = std::min<int64_t>(g.threads, pow2_ceil(chunks));
   g.cols_log2 = 0;
@@ -167,7 +166,10 @@ GradPlan grad_plan(const pba_relpos_desc *d) {
   // queries are split until the card is full once, a thread has at least eight
   // (a full ring), and none has over 512 (which bounds the error of its fp32
   // sums)
-  const int64_t resident = std::min<int64_t>(kRelposGradResident, 227 * 1024 / (g.smem + 1024));
+  const int ring = d->dtype == PBA_BF16 ? pba::RelposGradRing<pba::Bf16, true>::kThreadBytes
+                                        : pba::RelposGradRing<pba::F32, true>::kThreadBytes;
+  const int64_t resident =
+      std::min<int64_t>(kRelposGradResident, 227 * 1024 / (g.threads * (d->rows * 4 + ring) + 1024));
   const int64_t want = kPlanSms * resident / (d->H * d->B * g.col_blocks);
   const int64_t most = ceil_div(d->Nq, lanes * 8), least = ceil_div(d->Nq, lanes * 512);
   g.row_splits = int(std::max<int64_t>(1, std::max(least, std::min(most, want))));

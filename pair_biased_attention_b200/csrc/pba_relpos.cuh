@@ -233,20 +233,19 @@ template <typename T, bool kVec>
 struct RelposGradRing {
   using R = Ring8<T, kVec>;
   static constexpr int kStages = 8;
-  static constexpr int kSlotBytes = R::kSlotWords * 16 + 8;  // and the query's position and group
-  static constexpr int kThreadBytes = kStages * kSlotBytes;
+  static constexpr int kThreadBytes = kStages * R::kSlotWords * 16 + 64;  // and the eight keys' positions and groups
 };
 
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kRelposGradThreads, 5) relpos_grad_kernel(const __grid_constant__ RelposParams p) {
+__global__ void __launch_bounds__(kRelposGradThreads, 4) relpos_grad_kernel(const __grid_constant__ RelposParams p) {
   using Ring = RelposGradRing<T, kVec>;
   using R = typename Ring::R;
   extern __shared__ __align__(16) uint8_t relpos_grad_smem[];
   const int threads = blockDim.x, tid = threadIdx.x;
-  // [stage][word][thread] 16-byte words, [stage][thread] positions and groups,
+  // [stage][word][thread] 16-byte words, [key][thread] positions and groups,
   // the lookup, [row][thread] sums
   uint8_t *ring = relpos_grad_smem + tid * 16;
-  int2 *ring_q = reinterpret_cast<int2 *>(relpos_grad_smem + threads * Ring::kStages * R::kSlotWords * 16) + tid;
+  int2 *keys = reinterpret_cast<int2 *>(relpos_grad_smem + threads * Ring::kStages * R::kSlotWords * 16) + tid;
   uint32_t *look_smem = reinterpret_cast<uint32_t *>(relpos_grad_smem + threads * Ring::kThreadBytes);
   float *hist = reinterpret_cast<float *>(look_smem + relpos_lookup_words(p.rule));
   const RelposLookup look = relpos_lookup(p.rule, look_smem, tid, threads);
@@ -264,18 +263,20 @@ __global__ void __launch_bounds__(kRelposGradThreads, 5) relpos_grad_kernel(cons
     // one-sided: keys ahead of the query all share row 0
     const int far = rule.far, far_hi = rule.kind == 2 ? 0 : far;
     const bool groups = rule.cross >= 0;
-    // The keys' positions and groups are read again (from L1) where single
+    // The keys' positions and groups wait in shared memory for where single
     // ones are needed; what stays in registers are the weights 1 and 0 of the
     // eight's members of the queries' group, and the members' range.
-    const int32_t *kp = p.k_pos + b * p.k_sb, *kgp = groups ? p.k_group + b * p.kg_sb : nullptr;
-    float2 in[4] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f), make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
-    int k_min, k_max;
-    {
-      int k[8];
-      load_keys8<true>(kp, c, p.Nk, p.pos_vec != 0, k);
-      k_min = k_max = k[0];
+    float2 in[4], ex[4] = {};  // and of the others
 #pragma unroll
-      for (int e = 1; e < 8; ++e) {
+    for (int e = 0; e < 4; ++e) in[e] = make_float2(1.f, 1.f);
+    int k_min = 2147483647, k_max = -2147483647 - 1;
+    {
+      int k[8], kg[8] = {};
+      load_keys8<true>(p.k_pos + b * p.k_sb, c, p.Nk, p.pos_vec != 0, k);
+      if (groups) load_keys8<true>(p.k_group + b * p.kg_sb, c, p.Nk, p.pos_vec != 0, kg);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        keys[e * threads] = make_int2(k[e], kg[e]);
         k_min = min(k_min, k[e]);
         k_max = max(k_max, k[e]);
       }
@@ -289,69 +290,73 @@ __global__ void __launch_bounds__(kRelposGradThreads, 5) relpos_grad_kernel(cons
     const int32_t *qp = p.q_pos + b * p.q_sb, *qgp = groups ? p.q_group + b * p.qg_sb : nullptr;
     const bool inner = c >= 8 && c + 16 <= p.Nk;
     const int step = lanes * p.row_splits, begin = row_split * lanes + lane_row;
-    auto fetch = [&](int i, int s) {
-      if (i < p.Nq) {
-        R::fetch(ring + s * R::kSlotWords * threads * 16, threads * 16, src + int64_t(i) * p.out_s[2], n, inner);
-        cp_async4(&ring_q[s * threads].x, qp + i);
-        if (groups) cp_async4(&ring_q[s * threads].y, qgp + i);
-      }
+    const int64_t row_step = int64_t(step) * p.out_s[2];
+    const W *row = src + int64_t(begin) * p.out_s[2];   // this row's eight
+    int ahead = begin;                                  // the row to be fetched next, and its eight
+    const W *ahead_row = row;
+    uint8_t *slot = ring;
+    const int slot_bytes = R::kSlotWords * threads * 16;
+    auto fetch = [&](uint8_t *to) {
+      if (ahead < p.Nq) R::fetch(to, threads * 16, ahead_row, n, inner);
       cp_async_commit();
+      ahead += step;
+      ahead_row += row_step;
     };
-    for (int s = 0; s < Ring::kStages; ++s) fetch(begin + s * step, s);
-    int s = 0;
+    for (int s = 0; s < Ring::kStages; ++s) fetch(ring + s * slot_bytes);
+    int q = begin < p.Nq ? __ldg(qp + begin) : 0, qg = groups && begin < p.Nq ? __ldg(qgp + begin) : 0;
     for (int i = begin; i < p.Nq; i += step) {
+      const int2 qq = make_int2(q, qg);
+      const int next = min(i + step, p.Nq - 1);
+      q = __ldg(qp + next);
+      if (groups) qg = __ldg(qgp + next);
       cp_async_wait<Ring::kStages - 1>();
-      const Raw8<T> x = R::take(ring + s * R::kSlotWords * threads * 16, threads * 16,
-                                src + int64_t(i) * p.out_s[2], inner);
-      const int2 qq = ring_q[s * threads];
-      fetch(i + Ring::kStages * step, s);
-      s = s + 1 == Ring::kStages ? 0 : s + 1;
+      const Raw8<T> x = R::take(slot, threads * 16, row, inner);
       if (groups && (first || qq.y != group)) {
         first = false;
         group = qq.y;
         // no member: any place will do, its weights are 0
         k_min = 2147483647, k_max = -2147483647 - 1;
         outside = false;
-        int k[8], kg[8];
-        load_keys8<true>(kp, c, p.Nk, p.pos_vec != 0, k);
-        load_keys8<true>(kgp, c, p.Nk, p.pos_vec != 0, kg);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const bool member = kg[e] == group;
+          const int2 key = keys[e * threads];
+          const bool member = key.y == group;
           outside = outside || !member;
           const float weight = member ? 1.f : 0.f;
           if (e & 1)
-            in[e >> 1].y = weight;
+            in[e >> 1].y = weight, ex[e >> 1].y = 1.f - weight;
           else
-            in[e >> 1].x = weight;
+            in[e >> 1].x = weight, ex[e >> 1].x = 1.f - weight;
           if (member) {
-            k_min = min(k_min, k[e]);
-            k_max = max(k_max, k[e]);
+            k_min = min(k_min, key.x);
+            k_max = max(k_max, key.x);
           }
         }
       }
       if (outside) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          cross[e] = ffma2(x.pair(e), make_float2(1.f - in[e].x, 1.f - in[e].y), cross[e]);
+          cross[e] = ffma2(x.pair(e), ex[e], cross[e]);
       }
-      if (sub_sat(k_min, qq.x) >= far_hi) {
+      // (a sum that saturates is never passed, so the comparisons hold at the ends of the range)
+      if (k_min > add_sat(qq.x, far_hi - 1)) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) hi[e] = ffma2(x.pair(e), in[e], hi[e]);
-      } else if (sub_sat(k_max, qq.x) <= -far) {
+      } else if (k_max < sub_sat(qq.x, far - 1)) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) lo[e] = ffma2(x.pair(e), in[e], lo[e]);
       } else {
-        int k[8], r[8];
-        load_keys8<true>(kp, c, p.Nk, p.pos_vec != 0, k);
         const int q_lo = sub_sat(qq.x, far), q_hi = add_sat(qq.x, far);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] = relpos_row(rule, look, min(max(k[e], q_lo), q_hi) - qq.x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if ((e & 1 ? in[e >> 1].y : in[e >> 1].x) != 0.f)
-            hist[r[e] * threads + tid] += e & 1 ? x.pair(e >> 1).y : x.pair(e >> 1).x;
+#pragma unroll 4
+        for (int e = 0; e < 8; ++e) {
+          const int2 key = keys[e * threads];
+          const int r = relpos_row(rule, look, min(max(key.x, q_lo), q_hi) - qq.x);
+          if (!groups || key.y == group) hist[r * threads + tid] += R::one(slot, threads * 16, row, inner, e);
+        }
       }
+      fetch(slot);
+      row += row_step;
+      slot = slot + slot_bytes == ring + Ring::kStages * slot_bytes ? ring : slot + slot_bytes;
     }
     cp_async_wait<0>();
     auto add = [&](int r, const float2 (&v)[4]) {
