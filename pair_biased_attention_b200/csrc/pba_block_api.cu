@@ -163,16 +163,16 @@ GradPlan grad_plan(const pba_relpos_desc *d) {
   while ((int64_t(1) << g.cols_log2) < cols) ++g.cols_log2;
   g.col_blocks = int(ceil_div(chunks, cols));
   const int64_t lanes = g.threads / cols;
-  // queries are split until the card is full once, a thread has at least eight
-  // (a full ring), and none has over 512 (which bounds the error of its fp32
-  // sums)
+  // Queries are split until the card is full once (or twice, three times, ...:
+  // no thread takes over 512, which bounds the error of its fp32 sums), and not
+  // further than eight to a thread.
   const int ring = d->dtype == PBA_BF16 ? pba::RelposGradRing<pba::Bf16, true>::kThreadBytes
                                         : pba::RelposGradRing<pba::F32, true>::kThreadBytes;
   const int64_t resident =
       std::min<int64_t>(kRelposGradResident, 227 * 1024 / (g.threads * (d->rows * 4 + ring) + 1024));
-  const int64_t want = kPlanSms * resident / (d->H * d->B * g.col_blocks);
+  const int64_t fill = std::max<int64_t>(1, kPlanSms * resident / (d->H * d->B * g.col_blocks));
   const int64_t most = ceil_div(d->Nq, lanes * 8), least = ceil_div(d->Nq, lanes * 512);
-  g.row_splits = int(std::max<int64_t>(1, std::max(least, std::min(most, want))));
+  g.row_splits = int(std::max(least, std::min(most, fill * ceil_div(least, fill))));
   g.splits = d->B * g.col_blocks * g.row_splits;
   return g;
 }

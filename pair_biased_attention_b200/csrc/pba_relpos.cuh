@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kRelposThreads) relpos_fwd_kernel(const __grid
 template <typename T, bool kVec>
 struct RelposGradRing {
   using R = Ring8<T, kVec>;
-  static constexpr int kStages = 8;
+  static constexpr int kStages = 4;
   static constexpr int kThreadBytes = kStages * R::kSlotWords * 16 + 64;  // and the eight keys' positions and groups
 };
 
@@ -281,6 +281,10 @@ __global__ void __launch_bounds__(kRelposGradThreads, 4) relpos_grad_kernel(cons
         k_max = max(k_max, k[e]);
       }
     }
+    // queries below q_hi have all members past the border ahead, those above
+    // q_lo behind (a bound that saturates is never passed, so this holds at the
+    // ends of the range, where a few more values go one by one)
+    int q_hi = sub_sat(k_min, far_hi - 1), q_lo = add_sat(k_max, far - 1);
     bool outside = false;  // some are of another group
     int group = 0;
     bool first = true;
@@ -332,25 +336,26 @@ __global__ void __launch_bounds__(kRelposGradThreads, 4) relpos_grad_kernel(cons
             k_max = max(k_max, key.x);
           }
         }
+        q_hi = sub_sat(k_min, far_hi - 1);
+        q_lo = add_sat(k_max, far - 1);
       }
       if (outside) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           cross[e] = ffma2(x.pair(e), ex[e], cross[e]);
       }
-      // (a sum that saturates is never passed, so the comparisons hold at the ends of the range)
-      if (k_min > add_sat(qq.x, far_hi - 1)) {
+      if (qq.x < q_hi) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) hi[e] = ffma2(x.pair(e), in[e], hi[e]);
-      } else if (k_max < sub_sat(qq.x, far - 1)) {
+      } else if (qq.x > q_lo) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) lo[e] = ffma2(x.pair(e), in[e], lo[e]);
       } else {
-        const int q_lo = sub_sat(qq.x, far), q_hi = add_sat(qq.x, far);
+        const int k_lo = sub_sat(qq.x, far), k_hi = add_sat(qq.x, far);
 #pragma unroll 4
         for (int e = 0; e < 8; ++e) {
           const int2 key = keys[e * threads];
-          const int r = relpos_row(rule, look, min(max(key.x, q_lo), q_hi) - qq.x);
+          const int r = relpos_row(rule, look, min(max(key.x, k_lo), k_hi) - qq.x);
           if (!groups || key.y == group) hist[r * threads + tid] += R::one(slot, threads * 16, row, inner, e);
         }
       }
