@@ -22,6 +22,8 @@ namespace {
 constexpr int64_t kPlanSms = 148;
 // Dynamic shared memory that the relative position kernels may ask for.
 constexpr int kRelposSmem = 200 * 1024;
+// And the block norms' ring of rows.
+constexpr int kNormSmem = 200 * 1024;
 // Blocks of the table's gradient on an SM.
 constexpr int64_t kRelposGradResident = 4;
 
@@ -204,24 +206,30 @@ pba_status check_norm(const pba_norm_desc *d, const void *f, const void *gate, c
   return PBA_OK;
 }
 
-// Threads of a row (eight channels each) and rows of a block.
-dim3 norm_block(int64_t C) {
-  const int64_t lanes = ceil_div(C, 8);
-  if (C > pba::kNormNarrowC) return dim3(unsigned(ceil_div(lanes, 32) * 32), 1);
+// Threads of a row, `channels` each, and rows of a block: a power of two of
+// lanes in blocks of 256, or a block of whole warps to a row.
+dim3 norm_block(int64_t C, int channels) {
+  const int64_t lanes = ceil_div(C, channels);
+  if (lanes > 32) return dim3(unsigned(ceil_div(lanes, 32) * 32), 1);
   const int64_t l = pow2_ceil(lanes);
   return dim3(unsigned(l), unsigned(pba::kNormNarrowThreads / l));
 }
+int norm_channels(int dtype, bool backward) {
+  if (backward) return pba::kNormBwdChannels;
+  return dtype == PBA_BF16 ? pba::norm_fwd_channels<pba::Bf16>() : pba::norm_fwd_channels<pba::F32>();
+}
 
-int64_t norm_grad_blocks(int64_t rows, int64_t C) {
-  const dim3 b = norm_block(C);
-  // two blocks of 256 threads, or as many of a wide row's as make up 512 threads, on each SM
-  const int64_t per_sm = std::max<int64_t>(1, 512 / (int64_t(b.x) * b.y));
-  return std::max<int64_t>(1, std::min(ceil_div(rows, b.y), kPlanSms * per_sm));
+// Blocks of a launch: 512 threads to an SM, which is what the kernels'
+// registers leave room for, each walking over its share of the rows.
+int64_t norm_blocks(int64_t rows, dim3 block) {
+  const int64_t per_sm = std::max<int64_t>(1, 512 / (int64_t(block.x) * block.y));
+  return std::max<int64_t>(1, std::min(ceil_div(rows, block.y), kPlanSms * per_sm));
 }
 
 bool norm_vec(const pba_norm_desc *d, const void *const *rows, const int64_t *strides, int n_rows,
               const void *const *params, int n_params) {
   const int64_t m = 16 / dtype_size(d->dtype);
+  if (d->C % 8 != 0) return false;
   for (int i = 0; i < n_rows; ++i)
     if (rows[i] != nullptr && (!aligned16(rows[i]) || (d->rows > 1 && strides[i] % m != 0))) return false;
   for (int i = 0; i < n_params; ++i)
@@ -229,36 +237,45 @@ bool norm_vec(const pba_norm_desc *d, const void *const *rows, const int64_t *st
   return true;
 }
 
-template <typename T, bool kVec>
-cudaError_t launch_norm(const pba::NormParams &p, bool backward, unsigned grid, cudaStream_t st) {
-  const dim3 block = norm_block(p.C);
-  // the wider kinds leave each thread fewer registers
-  if (p.C <= pba::kNormNarrowC) {
-    if (backward)
-      pba::block_norm_bwd_kernel<T, kVec, pba::kNormNarrowThreads><<<grid, block, 0, st>>>(p);
-    else
-      pba::block_norm_fwd_kernel<T, kVec, pba::kNormNarrowThreads><<<grid, block, 0, st>>>(p);
-  } else if (block.x <= 512) {
-    if (backward)
-      pba::block_norm_bwd_kernel<T, kVec, 512><<<grid, block, 0, st>>>(p);
-    else
-      pba::block_norm_fwd_kernel<T, kVec, 512><<<grid, block, 0, st>>>(p);
-  } else {
-    if (backward)
-      pba::block_norm_bwd_kernel<T, kVec, 1024><<<grid, block, 0, st>>>(p);
-    else
-      pba::block_norm_fwd_kernel<T, kVec, 1024><<<grid, block, 0, st>>>(p);
-  }
+template <typename K>
+cudaError_t start_norm_kernel(K kern, PerDeviceOnce &once, int smem, const pba::NormParams &p, unsigned grid,
+                              dim3 block, cudaStream_t st) {
+  const cudaError_t e = once_per_device(
+      once, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem); });
+  if (e != cudaSuccess) return e;
+  kern<<<grid, block, smem, st>>>(p);
   return cudaGetLastError();
 }
+template <typename T, bool kVec, int kThreads>
+cudaError_t start_norm(const pba::NormParams &p, bool backward, unsigned grid, dim3 block, cudaStream_t st) {
+  static PerDeviceOnce once[2];
+  const int threads = int(block.x * block.y);
+  using Fwd = pba::NormFwdStream<T, kVec, kThreads>;
+  using Bwd = pba::NormBwdStream<T, kVec, kThreads>;
+  static_assert(kThreads * Fwd::kThreadBytes <= kNormSmem && kThreads * Bwd::kThreadBytes <= kNormSmem, "ring");
+  return backward ? start_norm_kernel(pba::block_norm_bwd_kernel<T, kVec, kThreads>, once[1],
+                                      threads * Bwd::kThreadBytes, p, grid, block, st)
+                  : start_norm_kernel(pba::block_norm_fwd_kernel<T, kVec, kThreads>, once[0],
+                                      threads * Fwd::kThreadBytes, p, grid, block, st);
+}
 
-cudaError_t dispatch_norm(const pba::NormParams &p, int dtype, bool vec, bool backward, unsigned grid,
-                          cudaStream_t st) {
+template <typename T, bool kVec>
+cudaError_t launch_norm(const pba::NormParams &p, bool backward, unsigned grid, dim3 block, cudaStream_t st) {
+  // rows that share a block, rows of a block, and rows of a block so large
+  // that each thread has half the registers
+  if (block.x <= 32) return start_norm<T, kVec, pba::kNormNarrowThreads>(p, backward, grid, block, st);
+  if (block.x <= 512) return start_norm<T, kVec, 512>(p, backward, grid, block, st);
+  return start_norm<T, kVec, 1024>(p, backward, grid, block, st);
+}
+
+cudaError_t dispatch_norm(const pba::NormParams &p, int dtype, bool vec, bool backward, cudaStream_t st) {
+  const dim3 block = norm_block(p.C, norm_channels(dtype, backward));
+  const unsigned grid = unsigned(norm_blocks(p.rows, block));
   if (dtype == PBA_BF16)
-    return vec ? launch_norm<pba::Bf16, true>(p, backward, grid, st)
-               : launch_norm<pba::Bf16, false>(p, backward, grid, st);
-  return vec ? launch_norm<pba::F32, true>(p, backward, grid, st)
-             : launch_norm<pba::F32, false>(p, backward, grid, st);
+    return vec ? launch_norm<pba::Bf16, true>(p, backward, grid, block, st)
+               : launch_norm<pba::Bf16, false>(p, backward, grid, block, st);
+  return vec ? launch_norm<pba::F32, true>(p, backward, grid, block, st)
+             : launch_norm<pba::F32, false>(p, backward, grid, block, st);
 }
 
 void fill_norm(pba::NormParams &p, const pba_norm_desc *d, const void *f, const void *gate, const void *scale,
@@ -306,7 +323,8 @@ pba_status pba_relpos_bias_forward(const pba_relpos_desc *desc, const int32_t *q
   // them all), fewer when that would leave SMs without a block.
   const int per_word = d.dtype == PBA_BF16 ? 2 : 1;
   const int lookup = pba::relpos_lookup_words(p.rule);
-  const int64_t fit = (kRelposSmem / 4 - lookup) / d.rows * per_word;
+  const int ring = base != nullptr && vec ? pba::kRelposBaseStages * pba::kRelposThreads * 8 * size : 0;
+  const int64_t fit = ((kRelposSmem - ring) / 4 - lookup - 4) / d.rows * per_word;
   const int64_t blocks = vec ? ceil_div(d.B * d.Nq * ceil_div(d.Nk, 8), pba::kRelposThreads)
                              : ceil_div(d.B * d.Nq * ceil_div(d.Nk, 256), pba::kRelposThreads / 32);
   int64_t heads = std::min<int64_t>(d.H, fit);
@@ -314,7 +332,8 @@ pba_status pba_relpos_bias_forward(const pba_relpos_desc *desc, const int32_t *q
     heads = std::min(heads, std::max<int64_t>(per_word, d.H * blocks / (2 * kPlanSms) / per_word * per_word));
   if (heads < d.H) heads = std::max<int64_t>(per_word, heads / per_word * per_word);
   p.heads_per_block = int(heads);
-  const int smem = int((lookup + ceil_div(heads, per_word) * d.rows) * 4);
+  p.ring_offset = int(ceil_div((lookup + ceil_div(heads, per_word) * d.rows) * 4, 16) * 16);
+  const int smem = p.ring_offset + ring;
   // a block stages its table once and then walks over its share of the rows
   const dim3 grid(unsigned(std::min<int64_t>(blocks, 8 * kPlanSms)), unsigned(ceil_div(d.H, heads)));
   cudaStream_t st = static_cast<cudaStream_t>(stream_ptr);
@@ -396,9 +415,7 @@ pba_status pba_block_norm_forward(const pba_norm_desc *desc, const void *x, cons
   pba::NormParams p;
   fill_norm(p, desc, f, gate, scale, post_w, post_b, pre_w, pre_b);
   p.x = x, p.h = h, p.y = y;
-  const dim3 block = norm_block(d.C);
-  const unsigned grid = unsigned(std::min<int64_t>(ceil_div(d.rows, block.y), kPlanSms * (2048 / (block.x * block.y))));
-  const cudaError_t e = dispatch_norm(p, d.dtype, norm_vec(desc, rows, strides, 5, params, 5), false, grid,
+  const cudaError_t e = dispatch_norm(p, d.dtype, norm_vec(desc, rows, strides, 5, params, 5), false,
                                       static_cast<cudaStream_t>(stream_ptr));
   return e == cudaSuccess ? PBA_OK : PBA_ERR_CUDA;
 }
@@ -406,7 +423,7 @@ pba_status pba_block_norm_forward(const pba_norm_desc *desc, const void *x, cons
 pba_status pba_block_norm_backward_workspace(const pba_norm_desc *desc, int64_t *bytes) {
   if (desc == nullptr || bytes == nullptr || desc->rows < 0 || desc->C < 1) return PBA_ERR_INVALID_ARG;
   if (desc->C > pba::kNormMaxC) return PBA_ERR_UNSUPPORTED;
-  *bytes = desc->rows == 0 ? 0 : norm_grad_blocks(desc->rows, desc->C) * pba::kNormParams * desc->C * 4;
+  *bytes = desc->rows == 0 ? 0 : norm_blocks(desc->rows, norm_block(desc->C, norm_channels(desc->dtype, true))) * pba::kNormParams * desc->C * 4;
   return PBA_OK;
 }
 
@@ -447,7 +464,7 @@ pba_status pba_block_norm_backward(const pba_norm_desc *desc, const void *h, con
     if (!aligned_to(o, 4)) return PBA_ERR_INVALID_ARG;
     any = any || o != nullptr;
   }
-  const int64_t blocks = d.rows == 0 ? 0 : norm_grad_blocks(d.rows, d.C);
+  const int64_t blocks = d.rows == 0 ? 0 : norm_blocks(d.rows, norm_block(d.C, norm_channels(d.dtype, true)));
   if (!aligned_to(workspace, 4) || workspace_bytes < blocks * pba::kNormParams * d.C * 4) return PBA_ERR_INVALID_ARG;
   s = check_device();
   if (s != PBA_OK) return s;
@@ -458,7 +475,7 @@ pba_status pba_block_norm_backward(const pba_norm_desc *desc, const void *h, con
     p.h = const_cast<void *>(h);  // read
     p.dh = dh, p.dy = dy, p.dx = dx, p.df = df, p.dgate = dgate;
     p.part = static_cast<float *>(workspace);
-    if (dispatch_norm(p, d.dtype, norm_vec(desc, rows, strides, 8, params, 5), true, unsigned(blocks), st) !=
+    if (dispatch_norm(p, d.dtype, norm_vec(desc, rows, strides, 8, params, 5), true, st) !=
         cudaSuccess)
       return PBA_ERR_CUDA;
   }

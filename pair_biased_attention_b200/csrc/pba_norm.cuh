@@ -10,11 +10,13 @@
 // attention sit between two such steps: f is what the block's output
 // projection returns, y what the next block's projections read.
 //
-// A row of C channels is held by blockDim.x threads of eight channels each,
-// all of it in registers: one pass over the data, the mean first and then the
-// squares around it.  Up to 256 channels (32 threads) several rows share a
-// block and sums go by shuffles; beyond, a block takes one row at a time and
-// sums go through shared memory.  Bound by the bytes read and written.
+// A row of C channels is held by blockDim.x threads, all of it in registers: one
+// pass over the data, the mean first and then the squares around it, while the
+// thread's next rows are on their way.  Rows of up to 32 threads share a block and
+// their sums go by shuffles; beyond, a block takes one row at a time and sums
+// go through shared memory.  Bound by the bytes read and written, and close
+// behind by the instructions per element: channels are worked on in packed
+// pairs, and a thread takes 32 bytes of every tensor where its registers allow.
 #pragma once
 
 #include "pba_vec8.cuh"
@@ -22,7 +24,6 @@
 namespace pba {
 
 constexpr int kNormMaxC = 8192;
-constexpr int kNormNarrowC = 256;  // widest row that shares its block with others
 constexpr int kNormNarrowThreads = 256;
 constexpr int kNormParams = 5;  // dscale, dpost_w, dpost_b, dpre_w, dpre_b
 
@@ -41,41 +42,173 @@ struct NormParams {
   float *part;               // backward: [blocks][kNormParams][C]
 };
 
-// A thread's channels of a per-channel parameter as fp32 (0 past the end), in
-// the order of load8.  Parameters stay in L1: they are read for every row.
-template <bool kVec>
-__device__ __forceinline__ void param8(const void *p, bool f32, int c, int n, int step, float (&x)[8]) {
-  if (f32) {
-    const float *q = static_cast<const float *>(p) + c;
-    if (kVec && n >= 8) {
-      const float4 a = __ldg(reinterpret_cast<const float4 *>(q)), b = __ldg(reinterpret_cast<const float4 *>(q) + 1);
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
+// Channels that a thread takes of each row: 32 bytes forward, eight backward,
+// where the sums over rows need registers too.
+template <typename T>
+__host__ __device__ constexpr int norm_fwd_channels() {
+  return 32 / int(sizeof(typename T::Word));
+}
+constexpr int kNormBwdChannels = 8;
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// E channels of a thread as packed pairs.
+template <int E>
+struct Channels {
+  float2 v[E / 2];
+  __device__ __forceinline__ float &at(int e) { return e & 1 ? v[e >> 1].y : v[e >> 1].x; }
+  __device__ __forceinline__ float total() const {
+    float2 s[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = e < n ? __ldg(q + (kVec ? e : e * step)) : 0.f;
+    for (int i = 4; i < E / 2; ++i) s[i & 3] = fadd2(s[i & 3], v[i]);
+    const float2 t = fadd2(fadd2(s[0], s[1]), fadd2(s[2], s[3]));
+    return t.x + t.y;
+  }
+};
+template <int E>
+__device__ __forceinline__ float dot(const Channels<E> &x, const Channels<E> &y) {
+  float2 s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] = fmul2(x.v[i], y.v[i]);
+#pragma unroll
+  for (int i = 4; i < E / 2; ++i) s[i & 3] = ffma2(x.v[i], y.v[i], s[i & 3]);
+  const float2 t = fadd2(fadd2(s[0], s[1]), fadd2(s[2], s[3]));
+  return t.x + t.y;
+}
+
+// Where a thread's channels lie.  kVec (16-byte aligned rows, C a multiple of
+// 8): eights number threadIdx.x, threadIdx.x + blockDim.x, each there or not
+// as a whole.  Otherwise every blockDim.x-th channel from threadIdx.x on, so
+// that neighbouring threads still touch neighbouring channels.
+template <bool kVec, int E>
+struct Place {
+  int lanes, t, C;
+  __device__ __forceinline__ explicit Place(int channels) : lanes(blockDim.x), t(threadIdx.x), C(channels) {}
+  __device__ __forceinline__ int channel(int e) const {
+    return kVec ? 8 * (t + (e >> 3) * lanes) + (e & 7) : t + e * lanes;
+  }
+  __device__ __forceinline__ bool has(int e) const { return channel(kVec ? e & ~7 : e) < C; }
+};
+
+// A thread's channels of `kArrays` tensors, row after row.  Aligned rows run
+// through a ring in shared memory, kStages rows deep, that the thread fills with
+// asynchronous copies and reads alone: about 100 KB on their way per SM, which
+// is what it takes to keep HBM busy (one row ahead in registers, 48 KB, reached
+// 0.69 of the rate).  Other rows are read element by element when they are
+// needed.
+template <typename T, bool kVec, int E, int kArrays, int kStages>
+struct RowStream {
+  using W = typename T::Word;
+  static constexpr int kWords = E * int(sizeof(W)) / 16;                 // 16-byte words of a row
+  static constexpr int kThreadBytes = kVec ? kArrays * kStages * kWords * 16 : 0;
+  uint8_t *slot;  // this thread's first word of the stage in turn
+  int threads, stage;
+
+  __device__ __forceinline__ explicit RowStream(uint8_t *smem) {
+    threads = blockDim.x * blockDim.y;
+    slot = smem + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
+    stage = 0;
+  }
+  __device__ __forceinline__ uint8_t *word(int array, int i) const {
+    return slot + ((stage * kArrays + array) * kWords + i) * threads * 16;
+  }
+  // starts copying a row of tensor `array` into the stage in turn; zeros for a
+  // row past the end and for channels past the last
+  __device__ __forceinline__ void fetch(int array, const void *base, int64_t row_offset, bool row,
+                                        const Place<kVec, E> &at) {
+    if (!kVec) return;
+    constexpr int kPer = kWords * 8 / E;  // words of an eight
+    const uint8_t *p = reinterpret_cast<const uint8_t *>(static_cast<const W *>(base) + (row ? row_offset : 0));
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const int first = 8 * (i / kPer);  // first channel of the word's eight, as an element of the thread's
+      const bool ok = row && at.has(first);
+      const int offset = at.channel(first) * int(sizeof(W)) + (i % kPer) * 16;
+      cp_async16_part(word(array, i), p + (ok ? offset : 0), ok ? 16 : 0);
     }
-  } else {
-    const uint16_t *q = static_cast<const uint16_t *>(p) + c;
-    if (kVec && n >= 8) {
-      unpack8(__ldg(reinterpret_cast<const uint4 *>(q)), x);
+  }
+  __device__ __forceinline__ void close() {  // the stage's last fetch has been started
+    if (kVec) cp_async_commit();
+  }
+  __device__ __forceinline__ void turn() { stage = stage + 1 == kStages ? 0 : stage + 1; }
+  __device__ __forceinline__ void wait() const {
+    if (kVec) cp_async_wait<kStages - 1>();
+  }
+  __device__ __forceinline__ Channels<E> get(int array, const void *base, int64_t row_offset, bool row,
+                                             const Place<kVec, E> &at) const {
+    Channels<E> r;
+    if (kVec) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(word(array, i));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if (sizeof(W) == 2) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r.v[(4 * i + k) % (E / 2)] = make_float2(bf16lo_to_f32(w[k]), bf16hi_to_f32(w[k]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            r.v[(2 * i + k) % (E / 2)] = make_float2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+        }
+      }
+    } else {
+      const W *p = static_cast<const W *>(base) + row_offset;
+#pragma unroll
+      for (int e = 0; e < E; ++e) r.at(e) = row && at.has(e) ? T::to_f32(p[at.channel(e)]) : 0.f;
+    }
+    return r;
+  }
+};
+
+template <typename T, bool kVec, int E>
+__device__ __forceinline__ void store_row(void *base, int64_t row_offset, bool row, const Place<kVec, E> &at,
+                                          Channels<E> &c) {
+  using W = typename T::Word;
+  if (!row) return;
+  W *p = static_cast<W *>(base) + row_offset;
+#pragma unroll
+  for (int j = 0; j < E / 8; ++j) {
+    if (kVec) {
+      const float2 *v = c.v + 4 * j;
+      const float x[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+      if (at.has(8 * j)) store8<T, true>(p + at.channel(8 * j), 8, 1, x);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = e < n ? Bf16::to_f32(__ldg(q + (kVec ? e : e * step))) : 0.f;
+      for (int e = 8 * j; e < 8 * j + 8; ++e)
+        if (at.has(e)) p[at.channel(e)] = T::from_f32(c.at(e));
     }
   }
 }
 
-// A thread's first channel, and how many of its eight exist (none for a thread
-// past the end, which still takes part in the sums): eight consecutive ones,
-// or every blockDim.x-th.
-template <bool kVec>
-__device__ __forceinline__ int norm_first() {
-  return kVec ? threadIdx.x * 8 : threadIdx.x;
-}
-template <bool kVec>
-__device__ __forceinline__ int norm_count(int C) {
-  const int left = C - norm_first<kVec>();
-  return max(0, kVec ? min(8, left) : (left + int(blockDim.x) - 1) / int(blockDim.x));
+// A thread's channels of a per-channel parameter as fp32 (0 past the end).
+// Parameters stay in L1: they are read for every row.
+template <bool kVec, int E>
+__device__ __forceinline__ Channels<E> param(const void *p, bool f32, const Place<kVec, E> &at) {
+  Channels<E> r;
+#pragma unroll
+  for (int j = 0; j < E / 8; ++j) {
+    float x[8] = {};
+    if (kVec) {
+      if (at.has(8 * j)) {
+        if (f32) {
+          const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at.channel(8 * j));
+          const float4 a = __ldg(q), b = __ldg(q + 1);
+          x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        } else {
+          unpack8(__ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at.channel(8 * j))), x);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (at.has(8 * j + e))
+          x[e] = f32 ? __ldg(static_cast<const float *>(p) + at.channel(8 * j + e))
+                     : Bf16::to_f32(__ldg(static_cast<const uint16_t *>(p) + at.channel(8 * j + e)));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[4 * j + i] = make_float2(x[2 * i], x[2 * i + 1]);
+  }
+  return r;
 }
 
 // Sums of N values over the threads of a row.  kWide: the row is the block
@@ -88,8 +221,8 @@ struct RowSum {
   int turn;
   __device__ __forceinline__ void operator()(float (&v)[N]) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      if (!kWide && o >= lanes) continue;
+    for (int o = 1; o < 32; o <<= 1) {
+      if (!kWide && o >= lanes) break;
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     }
@@ -115,85 +248,137 @@ struct RowSum {
   }
 };
 
-// Subtracts the mean (layer norm) and returns the reciprocal root of the mean
-// square of what is left; channels past the end stay 0.
-template <bool kWide, int N>
-__device__ __forceinline__ float centre(float (&x)[8], int n, const NormParams &p, RowSum<kWide, N> &sum) {
-  float v[N] = {};
-  if (p.layer) {
+// x - mean; channels past the end stay 0.
+template <bool kVec, int E>
+__device__ __forceinline__ void take_mean(Channels<E> &x, float mean, const Place<kVec, E> &at) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[0] += x[e];
-    sum(v);
-    const float mean = v[0] * p.inv_c;
+  for (int j = 0; j < E / 8; ++j) {
+    if (kVec) {
+      const float2 m = both(at.has(8 * j) ? -mean : 0.f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = e < n ? x[e] - mean : 0.f;
+      for (int i = 0; i < 4; ++i) x.v[4 * j + i] = fadd2(x.v[4 * j + i], m);
+    } else {
+#pragma unroll
+      for (int e = 8 * j; e < 8 * j + 8; ++e) x.at(e) = at.has(e) ? x.at(e) - mean : 0.f;
+    }
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[0] = fmaf(x[e], x[e], v[0]);
+}
+
+// Subtracts the mean (layer norm) and returns the reciprocal root of the mean
+// square of what is left.
+template <bool kWide, bool kVec, int E>
+__device__ __forceinline__ float centre(Channels<E> &x, const NormParams &p, const Place<kVec, E> &at,
+                                        RowSum<kWide, 1> &sum) {
+  float v[1];
+  if (p.layer) {
+    v[0] = x.total();
+    sum(v);
+    take_mean(x, v[0] * p.inv_c, at);
+  }
+  v[0] = dot(x, x);
   sum(v);
   return rsqrtf(fmaf(v[0], p.inv_c, p.eps));
 }
+// The same for two rows at once.
+template <bool kWide, bool kVec, int E>
+__device__ __forceinline__ float2 centre2(Channels<E> &x, Channels<E> &y, const NormParams &p,
+                                          const Place<kVec, E> &at, RowSum<kWide, 2> &sum) {
+  float v[2];
+  if (p.layer) {
+    v[0] = x.total(), v[1] = y.total();
+    sum(v);
+    take_mean(x, v[0] * p.inv_c, at);
+    take_mean(y, v[1] * p.inv_c, at);
+  }
+  v[0] = dot(x, x), v[1] = dot(y, y);
+  sum(v);
+  return make_float2(rsqrtf(fmaf(v[0], p.inv_c, p.eps)), rsqrtf(fmaf(v[1], p.inv_c, p.eps)));
+}
 
-__device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// 1 / (1 + 2^(-x log2 e)) on the exp2 and reciprocal units, each good to about
+// 2^-22: below the rounding of an fp32 product chain, and exact in the limits
+// (the exponential overflows to infinity, whose reciprocal is 0).
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+  const float2 a = fmul2(x, both(-1.4426950408889634f));
+  const float2 d = fadd2(make_float2(ex2_approx(a.x), ex2_approx(a.y)), both(1.f));
+  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
 
 template <typename T, bool kVec, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) block_norm_fwd_kernel(const __grid_constant__ NormParams p) {
-  using W = typename T::Word;
+using NormFwdStream = RowStream<T, kVec, norm_fwd_channels<T>(), 3, kThreads == 1024 ? 2 : 4>;
+
+template <typename T, bool kVec, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
+    block_norm_fwd_kernel(const __grid_constant__ NormParams p) {
   constexpr bool kWide = kThreads > kNormNarrowThreads;
+  constexpr int E = norm_fwd_channels<T>();
   __shared__ float buf[kWide ? 2 * 32 : 1];
-  const int lanes = blockDim.x;                        // threads of a row
-  const int c = norm_first<kVec>(), n = norm_count<kVec>(p.C);
-  RowSum<kWide, 1> sum{buf, lanes, 0};
+  extern __shared__ __align__(16) uint8_t norm_smem[];
+  const Place<kVec, E> at(p.C);
+  RowSum<kWide, 1> sum{buf, int(blockDim.x), 0};
   const int64_t step = int64_t(gridDim.x) * blockDim.y;
+  NormFwdStream<T, kVec, kThreads> in(norm_smem);
+  int64_t ahead = int64_t(blockIdx.x) * blockDim.y + threadIdx.y, r = ahead;
+  auto fetch = [&]() {
+    const bool row = ahead < p.rows;
+    in.fetch(0, p.x, ahead * p.x_s, row, at);
+    if (p.f != nullptr) in.fetch(1, p.f, ahead * p.f_s, row, at);
+    if (p.gate != nullptr) in.fetch(2, p.gate, ahead * p.gate_s, row, at);
+    in.close();
+    in.turn();
+    ahead += step;
+  };
+  for (int i = 0; i < (kThreads == 1024 ? 2 : 4); ++i) fetch();
   // every thread of a warp runs the same number of rounds: a row past the
-  // end is carried along without loads and stores
-  for (int64_t r0 = int64_t(blockIdx.x) * blockDim.y; r0 < p.rows; r0 += step) {
-    const int64_t r = r0 + threadIdx.y;
-    const int m = r < p.rows ? n : 0;
-    float h[8], u[8], g[8];
-    load8<T, kVec>(static_cast<const W *>(p.x) + r * p.x_s + c, m, lanes, h);
+  // end is carried along as zeros
+  for (int64_t r0 = int64_t(blockIdx.x) * blockDim.y; r0 < p.rows; r0 += step, r += step) {
+    const bool row = r < p.rows;
+    in.wait();
+    Channels<E> h = in.get(0, p.x, r * p.x_s, row, at), u, g;
+    if (p.f != nullptr) u = in.get(1, p.f, r * p.f_s, row, at);
+    if (p.gate != nullptr) g = in.get(2, p.gate, r * p.gate_s, row, at);
+    fetch();
     if (p.f != nullptr) {
-      load8<T, kVec>(static_cast<const W *>(p.f) + r * p.f_s + c, m, lanes, u);
-      if (p.gate != nullptr) load8<T, kVec>(static_cast<const W *>(p.gate) + r * p.gate_s + c, m, lanes, g);
       if (p.post_w != nullptr) {
-        const float rs = centre(u, m, p, sum);
-        float w[8];
-        param8<kVec>(p.post_w, p.param_f32, c, m, lanes, w);
+        const float rs = centre<kWide>(u, p, at, sum);
+        const Channels<E> w = param(p.post_w, p.param_f32, at);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] *= rs * w[e];
+        for (int i = 0; i < E / 2; ++i) u.v[i] = fmul2(u.v[i], fmul2(w.v[i], both(rs)));
         if (p.post_b != nullptr) {
-          param8<kVec>(p.post_b, p.param_f32, c, m, lanes, w);
+          const Channels<E> b = param(p.post_b, p.param_f32, at);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) u[e] += w[e];
+          for (int i = 0; i < E / 2; ++i) u.v[i] = fadd2(u.v[i], b.v[i]);
         }
       }
       if (p.gate != nullptr) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] *= sigmoid_f32(g[e]);
+        for (int i = 0; i < E / 2; ++i) u.v[i] = fmul2(u.v[i], sigmoid2(g.v[i]));
       }
       if (p.scale != nullptr) {
-        param8<kVec>(p.scale, p.param_f32, c, m, lanes, g);
+        const Channels<E> s = param(p.scale, p.param_f32, at);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] *= g[e];
+        for (int i = 0; i < E / 2; ++i) u.v[i] = fmul2(u.v[i], s.v[i]);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] += u[e];
-      store8<T, kVec>(static_cast<W *>(p.h) + r * p.h_s + c, m, lanes, h);
+      for (int i = 0; i < E / 2; ++i) h.v[i] = fadd2(h.v[i], u.v[i]);
+      store_row<T>(p.h, r * p.h_s, row, at, h);
     }
     if (p.pre_w != nullptr) {
-      const float rs = centre(h, m, p, sum);
-      float w[8];
-      param8<kVec>(p.pre_w, p.param_f32, c, m, lanes, w);
+      const float rs = centre<kWide>(h, p, at, sum);
+      const Channels<E> w = param(p.pre_w, p.param_f32, at);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] *= rs * w[e];
+      for (int i = 0; i < E / 2; ++i) h.v[i] = fmul2(h.v[i], fmul2(w.v[i], both(rs)));
       if (p.pre_b != nullptr) {
-        param8<kVec>(p.pre_b, p.param_f32, c, m, lanes, w);
+        const Channels<E> b = param(p.pre_b, p.param_f32, at);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] += w[e];
+        for (int i = 0; i < E / 2; ++i) h.v[i] = fadd2(h.v[i], b.v[i]);
       }
-      store8<T, kVec>(static_cast<W *>(p.y) + r * p.y_s + c, m, lanes, h);
+      store_row<T>(p.y, r * p.y_s, row, at, h);
     }
   }
 }
@@ -205,133 +390,154 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) block_norm_
 // The statistics are taken again from h and f, which the formulas need
 // anyway.  Sums over rows stay in each thread's registers for its channels,
 // then per block in shared memory, then in `part`, always in the same order.
+template <typename T, int kThreads>
+__host__ __device__ constexpr int norm_bwd_stages() {
+  return (kThreads == 1024 ? 4 : 8) / int(sizeof(typename T::Word));
+}
 template <typename T, bool kVec, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) block_norm_bwd_kernel(const __grid_constant__ NormParams p) {
-  using W = typename T::Word;
+using NormBwdStream = RowStream<T, kVec, kNormBwdChannels, 5, norm_bwd_stages<T, kThreads>()>;
+
+template <typename T, bool kVec, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
+    block_norm_bwd_kernel(const __grid_constant__ NormParams p) {
   constexpr bool kWide = kThreads > kNormNarrowThreads;
-  __shared__ float buf[kWide ? 2 * 2 * 32 : kNormNarrowThreads * 8];
-  const int lanes = blockDim.x;
-  const int c = norm_first<kVec>(), n = norm_count<kVec>(p.C);
-  RowSum<kWide, 2> sum{buf, lanes, 0};
+  constexpr int E = kNormBwdChannels;
+  using Ch = Channels<E>;
+  __shared__ float buf[kWide ? 2 * 2 * 32 : kNormNarrowThreads * E];
+  const Place<kVec, E> at(p.C);
+  RowSum<kWide, 2> sum{buf, int(blockDim.x), 0};
   const int64_t step = int64_t(gridDim.x) * blockDim.y;
-  float acc[kNormParams][8] = {};
-  for (int64_t r0 = int64_t(blockIdx.x) * blockDim.y; r0 < p.rows; r0 += step) {
-    const int64_t r = r0 + threadIdx.y;
-    const int m = r < p.rows ? n : 0;
-    float t[8], h[8], dy[8], f[8], g[8], w[8];
-    if (p.dh != nullptr) {
-      load8<T, kVec>(static_cast<const W *>(p.dh) + r * p.dh_s + c, m, lanes, t);
-    } else {
+  Ch acc[kNormParams] = {};
+  const bool pre = p.pre_w != nullptr, post = p.post_w != nullptr;
+  extern __shared__ __align__(16) uint8_t norm_smem[];
+  NormBwdStream<T, kVec, kThreads> in(norm_smem);
+  int64_t ahead = int64_t(blockIdx.x) * blockDim.y + threadIdx.y, r = ahead;
+  auto fetch = [&]() {
+    const bool row = ahead < p.rows;
+    if (p.dh != nullptr) in.fetch(0, p.dh, ahead * p.dh_s, row, at);
+    if (pre) {
+      in.fetch(1, p.h, ahead * p.h_s, row, at);
+      in.fetch(2, p.dy, ahead * p.dy_s, row, at);
+    }
+    if (p.f != nullptr) in.fetch(3, p.f, ahead * p.f_s, row, at);
+    if (p.gate != nullptr) in.fetch(4, p.gate, ahead * p.gate_s, row, at);
+    in.close();
+    in.turn();
+    ahead += step;
+  };
+  for (int i = 0; i < norm_bwd_stages<T, kThreads>(); ++i) fetch();
+  for (int64_t r0 = int64_t(blockIdx.x) * blockDim.y; r0 < p.rows; r0 += step, r += step) {
+    const bool row = r < p.rows;
+    in.wait();
+    Ch t = {}, h = {}, dy = {}, f = {}, g = {};
+    if (p.dh != nullptr) t = in.get(0, p.dh, r * p.dh_s, row, at);
+    if (pre) {
+      h = in.get(1, p.h, r * p.h_s, row, at);
+      dy = in.get(2, p.dy, r * p.dy_s, row, at);
+    }
+    if (p.f != nullptr) f = in.get(3, p.f, r * p.f_s, row, at);
+    if (p.gate != nullptr) g = in.get(4, p.gate, r * p.gate_s, row, at);
+    fetch();
+    float2 rs = both(1.f);  // of h and of f
+    Ch u = f;               // the block's output after its norm
+    if (post) {
+      rs = centre2<kWide>(h, f, p, at, sum);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = 0.f;
+      for (int i = 0; i < E / 2; ++i) f.v[i] = fmul2(f.v[i], both(rs.y));
+    } else if (pre) {
+      Ch none = {};
+      rs = centre2<kWide>(h, none, p, at, sum);
     }
-    if (p.pre_w != nullptr) {
-      load8<T, kVec>(static_cast<const W *>(p.h) + r * p.h_s + c, m, lanes, h);
-      load8<T, kVec>(static_cast<const W *>(p.dy) + r * p.dy_s + c, m, lanes, dy);
-    }
-    if (p.f != nullptr) {
-      load8<T, kVec>(static_cast<const W *>(p.f) + r * p.f_s + c, m, lanes, f);
-      if (p.gate != nullptr) load8<T, kVec>(static_cast<const W *>(p.gate) + r * p.gate_s + c, m, lanes, g);
-    }
-    if (p.pre_w != nullptr) {
-      const float rs = centre(h, m, p, sum);
-      param8<kVec>(p.pre_w, p.param_f32, c, m, lanes, w);
-      float v[2] = {0.f, 0.f};
+    if (pre) {
+      const Ch w = param(p.pre_w, p.param_f32, at);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[e] *= rs;
-        acc[3][e] = fmaf(dy[e], h[e], acc[3][e]);
-        acc[4][e] += dy[e];
-        dy[e] *= w[e];
-        v[0] += dy[e];
-        v[1] = fmaf(dy[e], h[e], v[1]);
+      for (int i = 0; i < E / 2; ++i) {
+        h.v[i] = fmul2(h.v[i], both(rs.x));
+        acc[3].v[i] = ffma2(dy.v[i], h.v[i], acc[3].v[i]);
+        acc[4].v[i] = fadd2(dy.v[i], acc[4].v[i]);
+        dy.v[i] = fmul2(dy.v[i], w.v[i]);
       }
+      float v[2] = {dy.total(), dot(dy, h)};
       sum(v);
-      const float a = p.layer ? v[0] * p.inv_c : 0.f, b = v[1] * p.inv_c;
+      const float a = p.layer ? -v[0] * p.inv_c : 0.f, b = -v[1] * p.inv_c;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = fmaf(rs, dy[e] - a - h[e] * b, t[e]);
+      for (int i = 0; i < E / 2; ++i)
+        t.v[i] = ffma2(both(rs.x), ffma2(h.v[i], both(b), fadd2(dy.v[i], both(a))), t.v[i]);
     }
-    store8<T, kVec>(static_cast<W *>(p.dx) + r * p.dx_s + c, m, lanes, t);
+    store_row<T>(p.dx, r * p.dx_s, row, at, t);
     if (p.f != nullptr) {
-      float rs = 1.f;
-      float u[8];
-      if (p.post_w != nullptr) {
-        rs = centre(f, m, p, sum);
-        param8<kVec>(p.post_w, p.param_f32, c, m, lanes, w);
+      Ch w;
+      if (post) {
+        w = param(p.post_w, p.param_f32, at);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          f[e] *= rs;
-          u[e] = f[e] * w[e];
-        }
+        for (int i = 0; i < E / 2; ++i) u.v[i] = fmul2(f.v[i], w.v[i]);
         if (p.post_b != nullptr) {
-          float pb[8];
-          param8<kVec>(p.post_b, p.param_f32, c, m, lanes, pb);
+          const Ch b = param(p.post_b, p.param_f32, at);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) u[e] += pb[e];
+          for (int i = 0; i < E / 2; ++i) u.v[i] = fadd2(u.v[i], b.v[i]);
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = f[e];
       }
-      float sc[8];
+      Ch s;  // sigmoid(gate)
+      // A row past the end is all zeros here: its t, dy and h are.  Channels
+      // past the end of a row may hold the mean's share in t; u is 0 there,
+      // and so is the weight that t is multiplied with below.
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        s.v[i] = p.gate != nullptr ? sigmoid2(g.v[i]) : both(1.f);
+        t.v[i] = fmul2(t.v[i], s.v[i]);
+        acc[0].v[i] = ffma2(t.v[i], u.v[i], acc[0].v[i]);
+      }
       if (p.scale != nullptr) {
-        param8<kVec>(p.scale, p.param_f32, c, m, lanes, sc);
-      } else {
+        const Ch sc = param(p.scale, p.param_f32, at);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sc[e] = 1.f;
+        for (int i = 0; i < E / 2; ++i) t.v[i] = fmul2(t.v[i], sc.v[i]);
       }
+      if (p.gate != nullptr) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float s = p.gate != nullptr ? sigmoid_f32(g[e]) : 1.f;
-        if (m <= 0) t[e] = 0.f;  // t holds no row here
-        acc[0][e] = fmaf(t[e] * s, u[e], acc[0][e]);
-        t[e] *= sc[e];
-        g[e] = t[e] * u[e] * s * (1.f - s);
-        t[e] *= s;
+        for (int i = 0; i < E / 2; ++i)
+          g.v[i] = fmul2(fmul2(t.v[i], u.v[i]), fadd2(both(1.f), make_float2(-s.v[i].x, -s.v[i].y)));
+        store_row<T>(p.dgate, r * p.dgate_s, row, at, g);
       }
-      if (p.gate != nullptr) store8<T, kVec>(static_cast<W *>(p.dgate) + r * p.dgate_s + c, m, lanes, g);
-      if (p.post_w != nullptr) {
-        float v[2] = {0.f, 0.f};
+      if (post) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          acc[1][e] = fmaf(t[e], f[e], acc[1][e]);
-          acc[2][e] += t[e];
-          t[e] *= w[e];
-          v[0] += t[e];
-          v[1] = fmaf(t[e], f[e], v[1]);
+        for (int i = 0; i < E / 2; ++i) {
+          acc[1].v[i] = ffma2(t.v[i], f.v[i], acc[1].v[i]);
+          acc[2].v[i] = fadd2(t.v[i], acc[2].v[i]);
+          t.v[i] = fmul2(t.v[i], w.v[i]);
         }
+        float v[2] = {t.total(), dot(t, f)};
         sum(v);
-        const float a = p.layer ? v[0] * p.inv_c : 0.f, b = v[1] * p.inv_c;
+        const float a = p.layer ? -v[0] * p.inv_c : 0.f, b = -v[1] * p.inv_c;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] = rs * (t[e] - a - f[e] * b);
+        for (int i = 0; i < E / 2; ++i)
+          t.v[i] = fmul2(both(rs.y), ffma2(f.v[i], both(b), fadd2(t.v[i], both(a))));
       }
-      store8<T, kVec>(static_cast<W *>(p.df) + r * p.df_s + c, m, lanes, t);
+      store_row<T>(p.df, r * p.df_s, row, at, t);
     }
   }
   // the block's sums: its rows' threads of a channel added in order
 #pragma unroll
   for (int k = 0; k < kNormParams; ++k) {
-    float *dst = p.part + (int64_t(blockIdx.x) * kNormParams + k) * p.C + c;
+    float *dst = p.part + (int64_t(blockIdx.x) * kNormParams + k) * p.C;
     if (!kWide) {
       __syncthreads();
-      float *mine = buf + (threadIdx.y * blockDim.x + threadIdx.x) * 8;
+      float *mine = buf + (threadIdx.y * blockDim.x + threadIdx.x) * E;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mine[e] = acc[k][e];
+      for (int e = 0; e < E; ++e) mine[e] = acc[k].at(e);
       __syncthreads();
       if (threadIdx.y == 0) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
+        acc[k] = Ch{};
         for (int y = 0; y < int(blockDim.y); ++y) {
-          const float *o = buf + (y * blockDim.x + threadIdx.x) * 8;
+          const float *o = buf + (y * blockDim.x + threadIdx.x) * E;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[k][e] += o[e];
+          for (int e = 0; e < E; ++e) acc[k].at(e) += o[e];
         }
       }
     }
     if (kWide || threadIdx.y == 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n) dst[kVec ? e : e * lanes] = acc[k][e];
+      for (int e = 0; e < E; ++e)
+        if (at.has(e)) dst[at.channel(e)] = acc[k].at(e);
     }
   }
 }

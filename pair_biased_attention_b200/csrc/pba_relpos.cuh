@@ -23,6 +23,7 @@ constexpr int kRelposMaxRows = 1025;     // rows of the table
 constexpr int kRelposLutFar = 2048;      // farthest last border that is looked up by distance
 constexpr int kRelposMaxBorders = 512;   // borders of the logarithmic rows of one side
 constexpr int kRelposThreads = 256;
+constexpr int kRelposBaseStages = 8;     // heads of the base on their way, per thread
 constexpr int kRelposGradThreads = 128;
 
 struct RelposRule {
@@ -40,6 +41,7 @@ struct RelposParams {
   int32_t B, H, Nq, Nk;
   int32_t rows;              // rows of the table
   int32_t heads_per_block;   // forward: even for bf16, heads a block writes
+  int32_t ring_offset;       // forward with an aligned base: where its ring lies in shared memory
   int32_t pos_vec;           // k_pos and k_group chunks readable as 16-byte words
   const int32_t *q_pos, *k_pos, *q_group, *k_group;
   int64_t q_sb, k_sb, qg_sb, kg_sb;  // batch strides (0: shared by the batch)
@@ -163,6 +165,35 @@ __global__ void __launch_bounds__(kRelposThreads) relpos_fwd_kernel(const __grid
   // (batch, query) row and key chunk, advanced without a division
   int row = int(first / chunks), col = int(first - int64_t(row) * chunks);
   const int drow = int(step / chunks), dcol = int(step - int64_t(drow) * chunks);
+  // Aligned rows of the base run ahead of their use through the thread's own
+  // ring in shared memory, one head after the other and on into the thread's
+  // next eights.
+  constexpr int slot_bytes = Ring8<T, true>::kSlotWords * kRelposThreads * 16;
+  uint8_t *ring = reinterpret_cast<uint8_t *>(relpos_smem) + p.ring_offset + threadIdx.x * 16;
+  int stage = 0, a_row = row, a_col = col, a_h = 0;
+  int64_t a_at = first;
+  auto fetch = [&]() {
+    if (a_at < total) {
+      const int b = a_row / p.Nq, i = a_row - b * p.Nq, c = a_col * 8;
+      const typename T::Word *src = static_cast<const typename T::Word *>(p.base) + b * p.base_s[0] +
+                                    (h0 + a_h) * p.base_s[1] + int64_t(i) * p.base_s[2] + c;
+      Ring8<T, true>::fetch(ring + stage * slot_bytes, kRelposThreads * 16, src, min(8, p.Nk - c), true);
+      if (++a_h == nh) {
+        a_h = 0;
+        a_at += step;
+        a_row += drow;
+        a_col += dcol;
+        if (a_col >= chunks) {
+          a_col -= chunks;
+          ++a_row;
+        }
+      }
+    }
+    cp_async_commit();
+    stage = stage + 1 == kRelposBaseStages ? 0 : stage + 1;
+  };
+  if (kBase && kVec)
+    for (int i = 0; i < kRelposBaseStages; ++i) fetch();
   for (int64_t at = first; at < total; at += step) {
     const int b = row / p.Nq, i = row - b * p.Nq;
     const int c = kVec ? col * 8 : col * 256 + lane;
@@ -188,7 +219,6 @@ __global__ void __launch_bounds__(kRelposThreads) relpos_fwd_kernel(const __grid
     const W *base = kBase ? static_cast<const W *>(p.base) + b * p.base_s[0] + h0 * p.base_s[1] +
                                 int64_t(i) * p.base_s[2] + c
                           : nullptr;
-#pragma unroll 2
     for (int w = 0; w < words; ++w) {
       const uint32_t *t = tab + w * p.rows;
       uint32_t v[8];
@@ -199,11 +229,22 @@ __global__ void __launch_bounds__(kRelposThreads) relpos_fwd_kernel(const __grid
         const int h = w * kHeadsPerWord + s;
         if (h >= nh) break;
         float x[8];
-        if (kBase) load8<T, kVec>(base + h * p.base_s[1], n, 32, x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float tv = !kBf ? __uint_as_float(v[e]) : (s == 0 ? bf16lo_to_f32(v[e]) : bf16hi_to_f32(v[e]));
-          x[e] = kBase ? x[e] + tv : tv;
+        for (int e = 0; e < 8; ++e)
+          x[e] = !kBf ? __uint_as_float(v[e]) : (s == 0 ? bf16lo_to_f32(v[e]) : bf16hi_to_f32(v[e]));
+        if (kBase) {
+          float y[8];
+          if (kVec) {
+            cp_async_wait<kRelposBaseStages - 1>();
+            const Raw8<T> raw = Ring8<T, true>::take(ring + stage * slot_bytes, kRelposThreads * 16, nullptr, true);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[2 * i] = raw.pair(i).x, y[2 * i + 1] = raw.pair(i).y;
+            fetch();
+          } else {
+            load8<T, false>(base + h * p.base_s[1], n, 32, y);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] += y[e];
         }
         store8<T, kVec>(out + h * p.out_s[1], n, 32, x);
       }
