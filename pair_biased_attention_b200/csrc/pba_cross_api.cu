@@ -121,13 +121,11 @@ pba_status run_tiles(const pba_cross_desc &d, const void *q, const void *k, cons
   return e == cudaSuccess ? PBA_OK : PBA_ERR_CUDA;
 }
 
-// Blocks that share 16 query rows: enough to fill the card, each with at
-// least one step per warp.
-int split_count(const pba_cross_desc &d, int64_t units) {
-  const int64_t want = ceil_div(148 * 4, units), most = ceil_div(d.Nk, pba::kXsWarps * pba::kXsKeys);
-  int s = 1;
-  while (s < pba::kXsMaxSplits && s < want && s < most) s *= 2;
-  return s;
+// Blocks that share 16 query rows: as many as the card holds at once, each
+// with at least one step per warp.
+int split_count(const pba_cross_desc &d, int64_t units, int blocks_per_sm) {
+  const int64_t fit = 148 * blocks_per_sm / units, most = ceil_div(d.Nk, pba::kXsWarps * pba::kXsKeys);
+  return int(std::max<int64_t>(1, std::min<int64_t>({pba::kXsMaxSplits, fit, most})));
 }
 
 template <int D>
@@ -148,8 +146,15 @@ pba_status run_split(const pba_cross_desc &d, const void *q, const void *k, cons
   p.lse = lse;
   p.lse_sb = d.lse_stride[0], p.lse_sh = d.lse_stride[1], p.lse_sn = d.lse_stride[2];
   const int64_t units = d.B * d.Hkv * p.row_tiles;
-  const int splits = split_count(d, units);
+  const int splits = split_count(d, units, pba::CrossSplitShape<D>::kBlocksPerSm);
   if (units * splits > kMaxI32) return PBA_ERR_INVALID_ARG;
+  auto kern = pba::pba_cross_split_kernel<D>;
+  constexpr int smem = pba::cross_split_smem<D>();
+  static PerDeviceOnce once;
+  if (once_per_device(once, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      }) != cudaSuccess)
+    return PBA_ERR_CUDA;
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
   cluster.val.clusterDim.x = unsigned(splits), cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
@@ -157,10 +162,11 @@ pba_status run_split(const pba_cross_desc &d, const void *q, const void *k, cons
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(unsigned(units * splits));
   cfg.blockDim = dim3(pba::kXsThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = &cluster;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pba::pba_cross_split_kernel<D>, p) == cudaSuccess ? PBA_OK : PBA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? PBA_OK : PBA_ERR_CUDA;
 }
 
 // Few rows per key head are bound by reading keys and values, and the split

@@ -4,11 +4,12 @@
 //
 // The query rows of the heads that share a key head (H / Hkv x Nq of them) are
 // one matrix; a block takes 16 of its rows and a share of the keys, and each
-// warp works on keys of its own, 32 at a time.  16 rows are one warp-level
-// matrix instruction high, which suits: the products are a small part of the
-// time, and the instruction takes its operands from registers, so keys and
-// values go from global memory to the registers that use them and never
-// through shared memory.  Two orders are chosen freely to make that so:
+// warp works on keys of its own, 16 at a time, which it copies ahead into its
+// own ring in shared memory (about 190 KB on their way per SM; loads straight
+// into registers, 8 KB a warp, left HBM at 0.42 of its rate).  16 rows are one
+// warp-level matrix instruction high, which suits: the products are a small
+// part of the time.  Two orders are chosen freely so that every operand is read
+// from shared memory in 16-byte words:
 //   - scores: the feature axis is summed over, so lane (g, t) of eight rows
 //     by four takes the 16-byte chunks t, t + 4, ... of key row g whole, and
 //     the query operand is loaded in the same order;
@@ -31,8 +32,15 @@ namespace pba {
 constexpr int kXsWarps = 4;
 constexpr int kXsThreads = 32 * kXsWarps;
 constexpr int kXsRows = 16;        // query rows of a block
-constexpr int kXsKeys = 32;        // keys of a warp's step
+constexpr int kXsKeys = 16;        // keys of a warp's step
 constexpr int kXsMaxSplits = 8;    // blocks of a cluster (the portable limit)
+// Blocks on an SM and steps under way per warp, by what registers and shared
+// memory allow.
+template <int D>
+struct CrossSplitShape {
+  static constexpr int kBlocksPerSm = D == 128 ? 2 : 4;
+  static constexpr int kStages = D == 32 ? 6 : 3;
+};
 
 struct CrossSplitParams {
   int32_t B, H, Hkv, group, Nq, Nk;
@@ -58,34 +66,44 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 ld_keep16(const void *p) {  // read once by this SM
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint2 ld_keep8(const void *p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
+// A ring of steps per warp: [stage][K, V][16 keys][D] bf16, the 16-byte chunks
+// of a row in an order that lets both kinds of reads touch all banks.
+template <int D>
+struct CrossRing {
+  static constexpr int kRowChunks = D / 8;
+  static constexpr int kTileBytes = kXsKeys * D * 2;
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStages = CrossSplitShape<D>::kStages;
+  static __device__ __forceinline__ int chunk_at(int row, int chunk) {
+    return row * D * 2 + ((D == 32 ? chunk ^ ((row >> 1) & 3) : chunk ^ ((row >> 1) & 3) * 2 ^ (row & 1) * 4) << 4);
+  }
+};
 
+// What the block's warps leave for the join; it takes the ring's place.
 template <int D>
 struct CrossSplitSmem {
-  // partial sums of the warps, then (in warp 0's place) of the block
   float o[kXsWarps][kXsRows][D + 4];
   float m[kXsWarps][kXsRows];
   float l[kXsWarps][kXsRows];
 };
 
 template <int D>
-__global__ void __launch_bounds__(kXsThreads) pba_cross_split_kernel(const __grid_constant__ CrossSplitParams p) {
+constexpr int cross_split_smem() {
+  constexpr int ring = kXsWarps * CrossRing<D>::kStages * CrossRing<D>::kStageBytes;
+  constexpr int join = int(sizeof(CrossSplitSmem<D>));
+  return ring > join ? ring : join;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kXsThreads, CrossSplitShape<D>::kBlocksPerSm)
+    pba_cross_split_kernel(const __grid_constant__ CrossSplitParams p) {
+  using Ring = CrossRing<D>;
   constexpr int kChunks = D / 32;            // 16-byte chunks of a key row per lane
   constexpr int kSteps = D / 16;             // matrix instructions along the features
   constexpr int kCols = D / 8;               // output accumulators: feature = kCols * column + accumulator, column 0..7
   constexpr int kWords = kCols / 2;          // 4-byte words of a value row per lane
-  __shared__ CrossSplitSmem<D> sm;
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  CrossSplitSmem<D> &sm = *reinterpret_cast<CrossSplitSmem<D> *>(ring_smem);
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int splits = int(cluster.num_blocks()), split = int(cluster.block_rank());
@@ -96,6 +114,37 @@ __global__ void __launch_bounds__(kXsThreads) pba_cross_split_kernel(const __gri
   const int hk = bh % p.Hkv, b = bh / p.Hkv;
   const int rows = p.group * p.Nq;
   const int keys = cross_keys(p.k_len, b, p.Nk);
+
+  // this block's keys, and within them every kXsWarps-th step for the warp
+  const int steps = (keys + kXsKeys - 1) / kXsKeys;
+  const int per = (steps + splits - 1) / splits;
+  const int s_begin = split * per + warp, s_end = min(steps, (split + 1) * per);
+  const uint16_t *kb = p.k + b * p.k_sb + hk * p.k_sh, *vb = p.v + b * p.v_sb + hk * p.v_sh;
+  const uint8_t *mrow = p.mask == nullptr ? nullptr : p.mask + b * p.mask_sb;
+  uint8_t *ring = ring_smem + warp * Ring::kStages * Ring::kStageBytes;
+  // copies the 16 keys of a step; keys past the end are not read and become zeros
+  auto fetch = [&](int s, int stage) {
+    if (s < s_end) {
+      uint8_t *kt = ring + stage * Ring::kStageBytes, *vt = kt + Ring::kTileBytes;
+#pragma unroll
+      for (int i = 0; i < kXsKeys * Ring::kRowChunks / 32; ++i) {
+        const int at = i * 32 + lane, row = at / Ring::kRowChunks, c = at % Ring::kRowChunks;
+        const int key = s * kXsKeys + row, bytes = key < keys ? 16 : 0;
+        const int64_t from = bytes ? key : 0;
+        cp_async16_part(kt + Ring::chunk_at(row, c), kb + from * p.k_sn + c * 8, bytes);
+        cp_async16_part(vt + Ring::chunk_at(row, c), vb + from * p.v_sn + c * 8, bytes);
+      }
+    }
+    cp_async_commit();
+  };
+  auto mask_byte = [&](int s) -> uint32_t {  // lane i: key i of the step
+    const int key = s * kXsKeys + (lane & 15);
+    if (mrow == nullptr || key >= keys) return key < keys ? 1u : 0u;
+    return __ldg(mrow + key);
+  };
+#pragma unroll
+  for (int i = 0; i < Ring::kStages; ++i) fetch(s_begin + i * kXsWarps, i);
+  uint32_t next_mask = mask_byte(s_begin);
 
   // query rows g and g + 8 of the tile as the first operand of every step
   uint32_t qa[kSteps][4];
@@ -115,113 +164,103 @@ __global__ void __launch_bounds__(kXsThreads) pba_cross_split_kernel(const __gri
     }
   }
 
-  // this block's keys, and within them every kXsWarps-th step for the warp
-  const int steps = (keys + kXsKeys - 1) / kXsKeys;
-  const int per = (steps + splits - 1) / splits;
-  const int s_end = min(steps, (split + 1) * per);
-  const uint16_t *kb = p.k + b * p.k_sb + hk * p.k_sh, *vb = p.v + b * p.v_sb + hk * p.v_sh;
-  const uint8_t *mrow = p.mask == nullptr ? nullptr : p.mask + b * p.mask_sb;
   const float c_s = p.tau * kXLog2e;
   float o[kCols][4] = {};
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  for (int s = split * per + warp; s < s_end; s += kXsWarps) {
-    const int key0 = s * kXsKeys;
-    // bit i: key key0 + i takes part; the others are neither read nor used
-    uint32_t keep = keys - key0 >= 32 ? 0xFFFFFFFFu : (1u << (keys - key0)) - 1u;
-    if (mrow != nullptr) {
-      const bool on = key0 + lane < keys && __ldg(mrow + key0 + lane) != 0;
-      keep &= __ballot_sync(0xffffffffu, on);
-    }
-    uint4 kr[4][kChunks];
-    uint32_t vr[4][4][kWords];  // [16-key half and pair][row of the pair ...]: rows 2t, 2t+1, 2t+8, 2t+9 of each 16
+  int stage = 0;
+  for (int s = s_begin; s < s_end; s += kXsWarps) {
+    // bit i: key i of the step takes part
+    const uint32_t keep = __ballot_sync(0xffffffffu, next_mask != 0) & 0xFFFFu;
+    next_mask = mask_byte(s + kXsWarps);
+    cp_async_wait<Ring::kStages - 1>();
+    __syncwarp();
+    const uint8_t *kt = ring + stage * Ring::kStageBytes, *vt = kt + Ring::kTileBytes;
+    // scores of 16 rows by 16 keys
+    float sc[2][4] = {};
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const int key = 8 * n + g;
+    for (int n = 0; n < 2; ++n) {
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
-        kr[n][i] = make_uint4(0, 0, 0, 0);
-        if ((keep >> key) & 1u) kr[n][i] = ld_keep16(kb + int64_t(key0 + key) * p.k_sn + 8 * (t + 4 * i));
+        const uint4 kr = *reinterpret_cast<const uint4 *>(kt + Ring::chunk_at(8 * n + g, t + 4 * i));
+        mma_16816(sc[n], qa[2 * i], kr.x, kr.y);
+        mma_16816(sc[n], qa[2 * i + 1], kr.z, kr.w);
       }
     }
+    // value rows 2t, 2t + 1 (then + 8), features kCols g ... of each
+    uint32_t vr[2][2][kWords];
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
+    for (int n = 0; n < 2; ++n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int key = 8 * n + 2 * t + e;
-        uint32_t *w = vr[n][e];
+        const int row = 8 * n + 2 * t + e;
+        if (kWords == 2) {
+          const uint2 x = *reinterpret_cast<const uint2 *>(vt + Ring::chunk_at(row, g >> 1) + (g & 1) * 8);
+          vr[n][e][0] = x.x, vr[n][e][1] = x.y;
+        } else {
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) w[i] = 0;
-        if ((keep >> key) & 1u) {
-          const uint16_t *src = vb + int64_t(key0 + key) * p.v_sn + kCols * g;
-          if (kWords == 2) {
-            const uint2 x = ld_keep8(src);
-            w[0] = x.x, w[1] = x.y;
-          } else {
-#pragma unroll
-            for (int i = 0; i < kWords; i += 4) {
-              const uint4 x = ld_keep16(src + 2 * i);
-              w[i] = x.x, w[i + 1 < kWords ? i + 1 : 0] = x.y, w[i + 2 < kWords ? i + 2 : 0] = x.z,
-              w[i + 3 < kWords ? i + 3 : 0] = x.w;
-            }
+          for (int i = 0; i < kWords; i += 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(vt + Ring::chunk_at(row, g * (kWords / 4) + i / 4));
+            vr[n][e][i] = x.x, vr[n][e][(i + 1) % kWords] = x.y, vr[n][e][(i + 2) % kWords] = x.z,
+            vr[n][e][(i + 3) % kWords] = x.w;
           }
         }
       }
     }
-    // scores of 16 rows by 32 keys
-    float sc[4][4] = {};
+    if (keep != 0xFFFFu) {
+      // whatever the others hold: their scores are -inf, their values 0
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        mma_16816(sc[n], qa[2 * i], kr[n][i].x, kr[n][i].y);
-        mma_16816(sc[n], qa[2 * i + 1], kr[n][i].z, kr[n][i].w);
-      }
-    }
-    if (keep != 0xFFFFFFFFu) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int n = 0; n < 2; ++n) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (!((keep >> (8 * n + 2 * t + (e & 1))) & 1u)) sc[n][e] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (!((keep >> (8 * n + 2 * t + e)) & 1u)) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) vr[n][e][i] = 0;
+          }
+      }
     }
-    uint32_t pa[2][4];
+    __syncwarp();  // the stage has been read
+    fetch(s + Ring::kStages * kXsWarps, stage);
+    stage = stage + 1 == Ring::kStages ? 0 : stage + 1;
+    uint32_t pa[4];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      float mx = fmaxf(sc[0][2 * half], sc[0][2 * half + 1]);
-#pragma unroll
-      for (int n = 1; n < 4; ++n) mx = max3f(mx, sc[n][2 * half], sc[n][2 * half + 1]);
+      float mx = fmaxf(fmaxf(sc[0][2 * half], sc[0][2 * half + 1]), fmaxf(sc[1][2 * half], sc[1][2 * half + 1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const float m_new = fmaxf(m[half], mx);
       const float neg = m_new == -INFINITY ? 0.f : -m_new * c_s;
-      const float alpha = m[half] == -INFINITY ? 0.f : ex2_approx(fmaf(m[half], c_s, neg));
-      m[half] = m_new;
-      l[half] *= alpha;
+      if (m_new != m[half]) {  // the maximum has risen
+        const float alpha = m[half] == -INFINITY ? 0.f : ex2_approx(fmaf(m[half], c_s, neg));
+        m[half] = m_new;
+        l[half] *= alpha;
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        o[c][2 * half] *= alpha;
-        o[c][2 * half + 1] *= alpha;
+        for (int c = 0; c < kCols; ++c) {
+          o[c][2 * half] *= alpha;
+          o[c][2 * half + 1] *= alpha;
+        }
       }
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
+      for (int n = 0; n < 2; ++n) {
         const float a = ex2_approx(fmaf(sc[n][2 * half], c_s, neg));
         const float d = ex2_approx(fmaf(sc[n][2 * half + 1], c_s, neg));
         l[half] += a + d;
-        pa[n >> 1][(n & 1) * 2 + half] = pack_bf16x2(a, d);
+        pa[n * 2 + half] = pack_bf16x2(a, d);
       }
     }
-    // output: 16 keys at a time, rows 2t and 2t+1 of each eight interleaved
+    // output: rows 2t and 2t+1 of each eight interleaved
 #pragma unroll
-    for (int h16 = 0; h16 < 2; ++h16) {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        const uint32_t a0 = vr[2 * h16][0][i], a1 = vr[2 * h16][1][i];
-        const uint32_t b0 = vr[2 * h16 + 1][0][i], b1 = vr[2 * h16 + 1][1][i];
-        mma_16816(o[2 * i], pa[h16], __byte_perm(a0, a1, 0x5410), __byte_perm(b0, b1, 0x5410));
-        mma_16816(o[2 * i + 1], pa[h16], __byte_perm(a0, a1, 0x7632), __byte_perm(b0, b1, 0x7632));
-      }
+    for (int i = 0; i < kWords; ++i) {
+      mma_16816(o[2 * i], pa, __byte_perm(vr[0][0][i], vr[0][1][i], 0x5410),
+                __byte_perm(vr[1][0][i], vr[1][1][i], 0x5410));
+      mma_16816(o[2 * i + 1], pa, __byte_perm(vr[0][0][i], vr[0][1][i], 0x7632),
+                __byte_perm(vr[1][0][i], vr[1][1][i], 0x7632));
     }
   }
+  cp_async_wait<0>();
+  __syncthreads();  // the ring's memory now takes the partial sums
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
