@@ -85,6 +85,7 @@ struct CrossSplitSmem {
   float o[kXsWarps][kXsRows][D + 4];
   float m[kXsWarps][kXsRows];
   float l[kXsWarps][kXsRows];
+  float2 joined[kXsRows];  // maximum and sum of the block
 };
 
 template <int D>
@@ -122,18 +123,35 @@ __global__ void __launch_bounds__(kXsThreads, CrossSplitShape<D>::kBlocksPerSm)
   const uint16_t *kb = p.k + b * p.k_sb + hk * p.k_sh, *vb = p.v + b * p.v_sb + hk * p.v_sh;
   const uint8_t *mrow = p.mask == nullptr ? nullptr : p.mask + b * p.mask_sb;
   uint8_t *ring = ring_smem + warp * Ring::kStages * Ring::kStageBytes;
-  // copies the 16 keys of a step; keys past the end are not read and become zeros
-  auto fetch = [&](int s, int stage) {
-    if (s < s_end) {
+  // Copies the 16 keys of the next step: a lane takes the same chunk of every
+  // kLaneRows-th row.  Keys past the end are not read and become zeros.
+  constexpr int kLaneRows = 32 / Ring::kRowChunks, kCopies = kXsKeys / kLaneRows;
+  const int lane_row = lane / Ring::kRowChunks, lane_chunk = lane % Ring::kRowChunks;
+  const uint16_t *k_at = kb + (int64_t(s_begin) * kXsKeys + lane_row) * p.k_sn + lane_chunk * 8;
+  const uint16_t *v_at = vb + (int64_t(s_begin) * kXsKeys + lane_row) * p.v_sn + lane_chunk * 8;
+  int s_next = s_begin;
+  auto fetch = [&](int stage) {
+    if (s_next < s_end) {
       uint8_t *kt = ring + stage * Ring::kStageBytes, *vt = kt + Ring::kTileBytes;
+      if ((s_next + 1) * kXsKeys <= keys) {
 #pragma unroll
-      for (int i = 0; i < kXsKeys * Ring::kRowChunks / 32; ++i) {
-        const int at = i * 32 + lane, row = at / Ring::kRowChunks, c = at % Ring::kRowChunks;
-        const int key = s * kXsKeys + row, bytes = key < keys ? 16 : 0;
-        const int64_t from = bytes ? key : 0;
-        cp_async16_part(kt + Ring::chunk_at(row, c), kb + from * p.k_sn + c * 8, bytes);
-        cp_async16_part(vt + Ring::chunk_at(row, c), vb + from * p.v_sn + c * 8, bytes);
+        for (int i = 0; i < kCopies; ++i) {
+          const int to = Ring::chunk_at(i * kLaneRows + lane_row, lane_chunk);
+          cp_async16(kt + to, k_at + i * kLaneRows * p.k_sn);
+          cp_async16(vt + to, v_at + i * kLaneRows * p.v_sn);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          const int row = i * kLaneRows + lane_row, to = Ring::chunk_at(row, lane_chunk);
+          const bool ok = s_next * kXsKeys + row < keys;
+          cp_async16_part(kt + to, ok ? k_at + i * kLaneRows * p.k_sn : kb, ok ? 16 : 0);
+          cp_async16_part(vt + to, ok ? v_at + i * kLaneRows * p.v_sn : vb, ok ? 16 : 0);
+        }
       }
+      s_next += kXsWarps;
+      k_at += kXsWarps * kXsKeys * p.k_sn;
+      v_at += kXsWarps * kXsKeys * p.v_sn;
     }
     cp_async_commit();
   };
@@ -143,7 +161,7 @@ __global__ void __launch_bounds__(kXsThreads, CrossSplitShape<D>::kBlocksPerSm)
     return __ldg(mrow + key);
   };
 #pragma unroll
-  for (int i = 0; i < Ring::kStages; ++i) fetch(s_begin + i * kXsWarps, i);
+  for (int i = 0; i < Ring::kStages; ++i) fetch(i);
   uint32_t next_mask = mask_byte(s_begin);
 
   // query rows g and g + 8 of the tile as the first operand of every step
@@ -222,7 +240,7 @@ __global__ void __launch_bounds__(kXsThreads, CrossSplitShape<D>::kBlocksPerSm)
       }
     }
     __syncwarp();  // the stage has been read
-    fetch(s + Ring::kStages * kXsWarps, stage);
+    fetch(stage);
     stage = stage + 1 == Ring::kStages ? 0 : stage + 1;
     uint32_t pa[4];
 #pragma unroll
@@ -277,45 +295,67 @@ __global__ void __launch_bounds__(kXsThreads, CrossSplitShape<D>::kBlocksPerSm)
       sm.o[warp][r][kCols * (2 * t + 1) + c] = o[c][2 * half + 1];
     }
   }
-  cluster.sync();
-  // join: the cluster's blocks share out the rows, each row's partials taken
-  // in the order of block and warp
-  for (int at = split * kXsThreads + threadIdx.x; at < kXsRows * (D / 4); at += splits * kXsThreads) {
+  // join over the block's warps, into warp 0's place
+  const int live = min(kXsRows, rows - tile * kXsRows);  // rows of the tile that exist
+  __syncthreads();
+  for (int at = threadIdx.x; at < live * (D / 4); at += kXsThreads) {
     const int r = at / (D / 4), c = (at - r * (D / 4)) * 4;
-    float mm = -INFINITY;
-    for (int s = 0; s < splits; ++s) {
-      const CrossSplitSmem<D> *o_sm = cluster.map_shared_rank(&sm, s);
+    float mm = sm.m[0][r];
 #pragma unroll
-      for (int w = 0; w < kXsWarps; ++w) mm = fmaxf(mm, o_sm->m[w][r]);
-    }
+    for (int w = 1; w < kXsWarps; ++w) mm = fmaxf(mm, sm.m[w][r]);
     float ll = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (mm != -INFINITY) {
-      for (int s = 0; s < splits; ++s) {
-        const CrossSplitSmem<D> *o_sm = cluster.map_shared_rank(&sm, s);
 #pragma unroll
-        for (int w = 0; w < kXsWarps; ++w) {
-          const float mw = o_sm->m[w][r];
-          const float a = mw == -INFINITY ? 0.f : ex2_approx((mw - mm) * c_s);
-          const float4 x = *reinterpret_cast<const float4 *>(&o_sm->o[w][r][c]);
-          ll = fmaf(a, o_sm->l[w][r], ll);
-          acc.x = fmaf(a, x.x, acc.x);
-          acc.y = fmaf(a, x.y, acc.y);
-          acc.z = fmaf(a, x.z, acc.z);
-          acc.w = fmaf(a, x.w, acc.w);
-        }
+    for (int w = 0; w < kXsWarps; ++w) {
+      const float mw = sm.m[w][r], a = mw == -INFINITY ? 0.f : ex2_approx((mw - mm) * c_s);
+      const float4 x = *reinterpret_cast<const float4 *>(&sm.o[w][r][c]);
+      ll = fmaf(a, sm.l[w][r], ll);
+      acc.x = fmaf(a, x.x, acc.x);
+      acc.y = fmaf(a, x.y, acc.y);
+      acc.z = fmaf(a, x.z, acc.z);
+      acc.w = fmaf(a, x.w, acc.w);
+    }
+    *reinterpret_cast<float4 *>(&sm.o[0][r][c]) = acc;
+    if (c == 0) sm.joined[r] = make_float2(mm, ll);
+  }
+  cluster.sync();
+  // join over the cluster's blocks, which share out the rows: every partial is
+  // asked for before the first is used
+  for (int at = split * kXsThreads + threadIdx.x; at < live * (D / 4); at += splits * kXsThreads) {
+    const int r = at / (D / 4), c = (at - r * (D / 4)) * 4;
+    float2 ml[kXsMaxSplits];
+    float4 x[kXsMaxSplits];
+#pragma unroll
+    for (int s = 0; s < kXsMaxSplits; ++s) {
+      ml[s] = make_float2(-INFINITY, 0.f);
+      x[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < splits) {
+        const CrossSplitSmem<D> *o_sm = cluster.map_shared_rank(&sm, s);
+        ml[s] = o_sm->joined[r];
+        x[s] = *reinterpret_cast<const float4 *>(&o_sm->o[0][r][c]);
       }
+    }
+    float mm = ml[0].x;
+#pragma unroll
+    for (int s = 1; s < kXsMaxSplits; ++s) mm = fmaxf(mm, ml[s].x);
+    float ll = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < kXsMaxSplits; ++s) {
+      const float a = ml[s].x == -INFINITY ? 0.f : ex2_approx((ml[s].x - mm) * c_s);
+      ll = fmaf(a, ml[s].y, ll);
+      acc.x = fmaf(a, x[s].x, acc.x);
+      acc.y = fmaf(a, x[s].y, acc.y);
+      acc.z = fmaf(a, x[s].z, acc.z);
+      acc.w = fmaf(a, x[s].w, acc.w);
     }
     const float inv = ll > 0.f ? 1.f / ll : 0.f;
     const int row = tile * kXsRows + r;
-    if (row < rows) {
-      const int hr = row / p.Nq, h = hk * p.group + hr, i = row - hr * p.Nq;
-      uint2 w = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-      *reinterpret_cast<uint2 *>(p.out + b * p.out_sb + h * p.out_sh + int64_t(i) * p.out_sn + c) = w;
-      if (c == 0 && p.lse != nullptr)
-        p.lse[b * p.lse_sb + h * p.lse_sh + int64_t(i) * p.lse_sn] =
-            ll > 0.f ? fmaf(mm, p.tau, logf(ll)) : -INFINITY;
-    }
+    const int hr = row / p.Nq, h = hk * p.group + hr, i = row - hr * p.Nq;
+    const uint2 w = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    *reinterpret_cast<uint2 *>(p.out + b * p.out_sb + h * p.out_sh + int64_t(i) * p.out_sn + c) = w;
+    if (c == 0 && p.lse != nullptr)
+      p.lse[b * p.lse_sb + h * p.lse_sh + int64_t(i) * p.lse_sn] = ll > 0.f ? fmaf(mm, p.tau, logf(ll)) : -INFINITY;
   }
   cluster.sync();  // no block leaves while another reads its shared memory
 }
