@@ -168,58 +168,70 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
       }
     } else if (warp == kXWarpMma) {
       // ================================================================ MMA issuer
-      if (lane == 0 && nsteps > 0) {
+      // The whole warp walks through the loop and one lane issues: the operand
+      // descriptors then stay in uniform registers.
+      if (nsteps > 0) {
         constexpr uint32_t idesc_s = idesc_bf16_f32(kXTile, kXTile, false);  // both operands K-major
         constexpr uint32_t idesc_g = idesc_bf16_f32(kXTile, D, true);        // B MN-major
-        const uint32_t sF0 = smem_u32(smem + L::kOffFix0), sF1 = smem_u32(smem + L::kOffFix1);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t smem0 = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+        const uint32_t a0 = smem_desc_lo(smem0 + L::kOffFix0, 16), a1 = smem_desc_lo(smem0 + L::kOffFix1, 16);
+        // a warp's waits end as one
+        auto wait = [&](int bar, int parity) -> bool {
+          return __all_sync(0xffffffffu, mbar_wait<false>(&bars[bar], parity & 1, wc));
+        };
         // S, dP of step `it` (A: Q K^T, dO V^T; B: K Q^T, V dO^T) once its
         // tiles have landed and the previous step's S and dP have been read
         // (at D = 128: and the products over them are done)
         auto issue_s = [&](int it) -> bool {
           const int s = it % L::kStages;
-          if (!mbar_wait(&bars[L::kBarStepFull + s], (it / L::kStages) & 1, wc)) return false;
-          if (fix && !mbar_wait(&bars[L::kBarStepReady + s], (it / L::kStages) & 1, wc)) return false;
-          if (it > 0 && !mbar_wait(&bars[L::kAlias ? L::kBarGDone : L::kBarSFree], (it - 1) & 1, wc)) return false;
+          if (!wait(fix ? L::kBarStepReady + s : L::kBarStepFull + s, it / L::kStages)) return false;
+          if (it > 0 && !wait(L::kAlias ? L::kBarGDone : L::kBarSFree, it - 1)) return false;
           tc_fence_after_sync();
-          const uint32_t a0 = smem_desc_lo(sF0, 16), a1 = smem_desc_lo(sF1, 16);
-          const uint32_t b0 = smem_desc_lo(smem_u32(smem + L::kOffStep0 + s * T::kBytes), 16);
-          const uint32_t b1 = smem_desc_lo(smem_u32(smem + L::kOffStep1 + s * T::kBytes), 16);
+          const uint32_t b0 = smem_desc_lo(smem0 + L::kOffStep0 + s * T::kBytes, 16);
+          const uint32_t b1 = smem_desc_lo(smem0 + L::kOffStep1 + s * T::kBytes, 16);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16_ss(tmem + L::kColS, desc_at(a0, T::k_step(kk), T::kDescHi), desc_at(b0, T::k_step(kk), T::kDescHi),
-                        idesc_s, kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_bf16_ss(tm + L::kColS, desc_join(a0 + T::k_step(kk), T::kDescHi),
+                          desc_join(b0 + T::k_step(kk), T::kDescHi), idesc_s, kk > 0);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16_ss(tmem + L::kColDP, desc_at(a1, T::k_step(kk), T::kDescHi),
-                        desc_at(b1, T::k_step(kk), T::kDescHi), idesc_s, kk > 0);
-          tc_commit(&bars[L::kBarSFull]);
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_bf16_ss(tm + L::kColDP, desc_join(a1 + T::k_step(kk), T::kDescHi),
+                          desc_join(b1 + T::k_step(kk), T::kDescHi), idesc_s, kk > 0);
+            tc_commit(&bars[L::kBarSFull]);
+          }
+          __syncwarp();
           return true;
         };
-        // acc += G X with G (bf16, in Tensor Memory) and X an MN-major tile
+        // acc += G X with G (bf16, in Tensor Memory) and X an MN-major tile; by one lane
         auto issue_g = [&](uint32_t acc, bool ds, uint32_t x_lo, bool more) {
 #pragma unroll
           for (int kk = 0; kk < kXTile / 16; ++kk)
-            mma_bf16_ts(tmem + acc, tmem + (ds ? L::col_ds(kk >> 2) : L::col_p(kk >> 2)) + (kk & 3) * 8,
-                        desc_at(x_lo, T::mn_step(kk), T::kDescHi), idesc_g, (more || kk > 0) ? 1u : 0u);
+            mma_bf16_ts(tm + acc, tm + (ds ? L::col_ds(kk >> 2) : L::col_p(kk >> 2)) + (kk & 3) * 8,
+                        desc_join(x_lo + T::mn_step(kk), T::kDescHi), idesc_g, (more || kk > 0) ? 1u : 0u);
         };
-        bool ok = mbar_wait(&bars[L::kBarFixFull], 0, wc);
-        if (ok) ok = issue_s(0);
+        bool ok = wait(L::kBarFixFull, 0) && issue_s(0);
         for (int it = 0; it < nsteps && ok; ++it) {
           const int s = it % L::kStages;
           if (!L::kAlias && it + 1 < nsteps && !(ok = issue_s(it + 1))) break;
-          ok = mbar_wait(&bars[L::kBarGFull], it & 1, wc);
+          ok = wait(L::kBarGFull, it);
           if (!ok) break;
           tc_fence_after_sync();
-          const uint32_t x0 = smem_desc_lo(smem_u32(smem + L::kOffStep0 + s * T::kBytes), T::kSlabBytes);
-          const uint32_t x1 = smem_desc_lo(smem_u32(smem + L::kOffStep1 + s * T::kBytes), T::kSlabBytes);
-          if (kB) issue_g(L::kColAcc1, false, x1, it > 0);  // dV += P^T dO
-          issue_g(L::kColAcc0, true, x0, it > 0);           // A: dQ += dS K; B: dK += dS^T Q
-          tc_commit(&bars[L::kBarGDone]);
-          tc_commit(&bars[L::kBarStepEmpty + s]);
+          const uint32_t x0 = smem_desc_lo(smem0 + L::kOffStep0 + s * T::kBytes, T::kSlabBytes);
+          const uint32_t x1 = smem_desc_lo(smem0 + L::kOffStep1 + s * T::kBytes, T::kSlabBytes);
+          if (elect_one()) {
+            if (kB) issue_g(L::kColAcc1, false, x1, it > 0);  // dV += P^T dO
+            issue_g(L::kColAcc0, true, x0, it > 0);           // A: dQ += dS K; B: dK += dS^T Q
+            tc_commit(&bars[L::kBarGDone]);
+            tc_commit(&bars[L::kBarStepEmpty + s]);
+          }
+          __syncwarp();
           if (L::kAlias && it + 1 < nsteps && !(ok = issue_s(it + 1))) break;
         }
-        tc_commit(&bars[L::kBarDrain]);
-        mbar_wait(&bars[L::kBarDrain], 0, wc_drain);
+        if (elect_one()) tc_commit(&bars[L::kBarDrain]);
+        __syncwarp();
+        mbar_wait<false>(&bars[L::kBarDrain], 0, wc_drain);
       }
     } else if (warp == kXWarpFix && fix) {
       // ================================================================ A: K rows that do not count

@@ -14,7 +14,8 @@
 //   warps 0-3   softmax warpgroup of query tile 0 (thread t owns row t)
 //   warps 4-7   softmax warpgroup of query tile 1
 //   warp 8      TMA producer of Q (per unit) and of K and V
-//   warp 9      allocates Tensor Memory and issues every tcgen05.mma
+//   warps 9, 11 issue the tcgen05.mma of query tile 0 and 1 (9 allocates
+//               Tensor Memory)
 //   warp 10     zeroes the V rows of keys that do not take part
 // Without a bias nothing streams from HBM while a unit runs (K and V of a head
 // stay in L2), so what bounds the kernel is the exponentials: per key tile and
@@ -43,6 +44,7 @@ constexpr int kXThreads = 384;
 constexpr int kXWarpProducer = 8;
 constexpr int kXWarpMma = 9;
 constexpr int kXWarpFix = 10;
+constexpr int kXWarpMma1 = 11;
 constexpr int kXRegsSoftmax = 224;
 constexpr int kXRegsOther = 56;
 constexpr int kXRegSplitTotal = 256 * kXRegsSoftmax + 128 * kXRegsOther;
@@ -150,8 +152,9 @@ struct CrossLayout {
   static constexpr int kBarPFull = kBarSFree + kXQTiles;
   static constexpr int kBarODone = kBarPFull + kXQTiles;
   static constexpr int kBarOFree = kBarODone + kXQTiles;
-  static constexpr int kBarDrain = kBarOFree + kXQTiles;
-  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kBarTurn = kBarOFree + kXQTiles;  // [w][warp of the warpgroup]
+  static constexpr int kBarDrain = kBarTurn + kXQTiles * 4;
+  static constexpr int kNumBars = kBarDrain + kXQTiles;
   static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
   static constexpr int kOffAbort = kOffTmemSlot + 4;
   static constexpr int kBytes = kOffAbort + 4;
@@ -197,12 +200,12 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
 
   if (threadIdx.x == 0) {
     mbar_init(&bars[L::kBarQFull], 1);
-    mbar_init(&bars[L::kBarQEmpty], 1);
+    mbar_init(&bars[L::kBarQEmpty], kXQTiles);  // a commit of each issuer, as for the tiles
     for (int s = 0; s < L::kKVStages; ++s) {
       mbar_init(&bars[L::kBarKFull + s], 1);
       mbar_init(&bars[L::kBarVFull + s], 1);
-      mbar_init(&bars[L::kBarKEmpty + s], 1);
-      mbar_init(&bars[L::kBarVEmpty + s], 1);
+      mbar_init(&bars[L::kBarKEmpty + s], kXQTiles);
+      mbar_init(&bars[L::kBarVEmpty + s], kXQTiles);
       mbar_init(&bars[L::kBarVReady + s], 32);
     }
     for (int w = 0; w < kXQTiles; ++w) {
@@ -211,8 +214,9 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
       mbar_init(&bars[L::kBarPFull + w], kXTile);
       mbar_init(&bars[L::kBarODone + w], 1);
       mbar_init(&bars[L::kBarOFree + w], kXTile);
+      mbar_init(&bars[L::kBarDrain + w], 1);
+      for (int i = 0; i < 4; ++i) mbar_init(&bars[L::kBarTurn + w * 4 + i], 1);
     }
-    mbar_init(&bars[L::kBarDrain], 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -291,99 +295,102 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
           }
         }
       }
-    } else if (warp == kXWarpMma) {
-      // ============================================================== MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = idesc_bf16_f32(kXTile, kXTile, false);
-        constexpr uint32_t idesc_o = idesc_bf16_f32(kXTile, D, true);
-        const uint32_t sQ = smem_u32(smem + L::kOffQ);
-        const uint32_t sK = smem_u32(smem + L::kOffK);
-        const uint32_t sV = smem_u32(smem + L::kOffV);
-        bool ok = true;
-        int kc = 0, vc = 0;  // K and V tiles consumed
-        int gs = 0, gp = 0;  // score tiles and P V tiles issued per warpgroup
-        int uc = 0;
-        auto issue_s = [&](int w, int s) {
-          const uint32_t a_lo = smem_desc_lo(sQ + w * T::kBytes, 16);
-          const uint32_t b_lo = smem_desc_lo(sK + s * T::kBytes, 16);
+    } else if (warp == kXWarpMma || warp == kXWarpMma1) {
+      // ============================================================== MMA issuers
+      // One warp per query tile: a single one that served both in turn made
+      // each tile's products wait for the other's softmax.  The whole warp
+      // walks through the loop and one lane issues, which keeps the operand
+      // descriptors in uniform registers; under a branch for one lane every
+      // instruction took some 85 cycles to issue.
+      const int w = __shfl_sync(0xffffffffu, int(warp == kXWarpMma1), 0);
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kXTile, kXTile, false);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(kXTile, D, true);
+      const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t tS = tbase + L::col_s(w), tP = tbase + L::col_p(w), tO = tbase + L::col_o(w);
+      const uint32_t smem0 = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+      const uint32_t q_lo = smem_desc_lo(smem0 + L::kOffQ + w * T::kBytes, 16);
+      bool ok = true;
+      int kc = 0, vc = 0;  // K and V tiles consumed (= score and P V tiles issued)
+      int uc = 0;
+      // a warp's waits end as one
+      auto wait = [&](int bar, int parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait<false>(&bars[bar], parity & 1, wc));
+      };
+      auto issue_s = [&](int s) {
+        const uint32_t k_lo = smem_desc_lo(smem0 + L::kOffK + s * T::kBytes, 16);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16_ss(tmem + L::col_s(w), desc_at(a_lo, T::k_step(kk), T::kDescHi),
-                        desc_at(b_lo, T::k_step(kk), T::kDescHi), idesc_s, kk > 0 ? 1u : 0u);
+            mma_bf16_ss(tS, desc_join(q_lo + T::k_step(kk), T::kDescHi), desc_join(k_lo + T::k_step(kk), T::kDescHi),
+                        idesc_s, kk > 0 ? 1u : 0u);
           tc_commit(&bars[L::kBarSFull + w]);
-        };
-        auto issue_pv = [&](int w, int s, bool first) {
-          const uint32_t v_lo = smem_desc_lo(sV + s * T::kBytes, T::kSlabBytes);
+          tc_commit(&bars[L::kBarKEmpty + s]);
+        }
+        __syncwarp();
+      };
+      auto issue_pv = [&](int s, bool first) {
+        const uint32_t v_lo = smem_desc_lo(smem0 + L::kOffV + s * T::kBytes, T::kSlabBytes);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kXTile / 16; ++kk)
-            mma_bf16_ts(tmem + L::col_o(w), tmem + L::col_p(w) + kk * 8, desc_at(v_lo, T::mn_step(kk), T::kDescHi),
-                        idesc_o, (!first || kk > 0) ? 1u : 0u);
+            mma_bf16_ts(tO, tP + kk * 8, desc_join(v_lo + T::mn_step(kk), T::kDescHi), idesc_o,
+                        (!first || kk > 0) ? 1u : 0u);
           tc_commit(&bars[L::kBarODone + w]);
-        };
-        // D <= 64, per key tile j: S0(j+1), P0 V(j), S1(j+1), P1 V(j), so that a
-        // warpgroup's next scores are there when it has written P(j).
-        // D = 128 (P over S): P0 V(j), S0(j+1), P1 V(j), S1(j+1), each score
-        // tile once the product that reads P from its columns is done.
-        for (int u = u_begin; u < p.n_units && ok; u += u_step) {
-          const int nt = cross_unit(p, u).nt;
-          if (nt == 0) continue;
-          ok = mbar_wait(&bars[L::kBarQFull], uc & 1, wc);
-          if (ok) ok = mbar_wait(&bars[L::kBarKFull + kc % L::kKVStages], (kc / L::kKVStages) & 1, wc);
-          for (int w = 0; w < kXQTiles && ok; ++w) {
-            if (gs > 0 && !(ok = mbar_wait(&bars[L::kBarSFree + w], (gs - 1) & 1, wc))) break;
-            // P over S: the last P V of the previous unit has read its P
-            if (L::kAlias && gp > 0 && !(ok = mbar_wait(&bars[L::kBarODone + w], (gp - 1) & 1, wc))) break;
-            tc_fence_after_sync();
-            issue_s(w, kc % L::kKVStages);
-          }
-          if (!ok) break;
-          tc_commit(&bars[L::kBarKEmpty + kc % L::kKVStages]);
-          if (nt == 1) tc_commit(&bars[L::kBarQEmpty]);
-          ++kc;
-          ++gs;
-          for (int j = 0; j < nt && ok; ++j) {
-            const bool has_next = j + 1 < nt;
-            const int sk = kc % L::kKVStages;
-            const int sv = vc % L::kKVStages;
-            if (has_next) ok = mbar_wait(&bars[L::kBarKFull + sk], (kc / L::kKVStages) & 1, wc);
-            if (ok) ok = mbar_wait(&bars[L::kBarVFull + sv], (vc / L::kKVStages) & 1, wc);
-            if (ok && fix) ok = mbar_wait(&bars[L::kBarVReady + sv], (vc / L::kKVStages) & 1, wc);
-            for (int w = 0; w < kXQTiles && ok; ++w) {
-              if (!L::kAlias && has_next) {
-                if (!(ok = mbar_wait(&bars[L::kBarSFree + w], (gs - 1) & 1, wc))) break;
-                tc_fence_after_sync();
-                issue_s(w, sk);
-              }
-              if (!(ok = mbar_wait(&bars[L::kBarPFull + w], gp & 1, wc))) break;
-              // the first P V of a unit overwrites O: the epilogue of the
-              // previous unit must have read it
-              if (j == 0 && uc > 0 && !(ok = mbar_wait(&bars[L::kBarOFree + w], (uc - 1) & 1, wc))) break;
-              tc_fence_after_sync();
-              issue_pv(w, sv, j == 0);
-              if (L::kAlias && has_next) {
-                if (!(ok = mbar_wait(&bars[L::kBarODone + w], gp & 1, wc))) break;
-                tc_fence_after_sync();
-                issue_s(w, sk);
-              }
-            }
-            if (!ok) break;
-            if (has_next) {
-              tc_commit(&bars[L::kBarKEmpty + sk]);
-              // after the unit's last score MMAs the Q slot can be refilled
-              if (j + 2 == nt) tc_commit(&bars[L::kBarQEmpty]);
-              ++kc;
-              ++gs;
-            }
-            tc_commit(&bars[L::kBarVEmpty + sv]);
-            ++vc;
-            ++gp;
-          }
-          ++uc;
+          tc_commit(&bars[L::kBarVEmpty + s]);
         }
-        // every MMA issued above completes before Tensor Memory is released
-        tc_commit(&bars[L::kBarDrain]);
-        mbar_wait(&bars[L::kBarDrain], 0, wc_drain);
+        __syncwarp();
+      };
+      // the next score tile, once its keys are there and S (at D = 128: P
+      // over it) has been read
+      auto next_s = [&]() -> bool {
+        const int s = kc % L::kKVStages;
+        if (!wait(L::kBarKFull + s, kc / L::kKVStages)) return false;
+        if (kc > 0 && !wait(L::kBarSFree + w, kc - 1)) return false;
+        if (L::kAlias && vc > 0 && !wait(L::kBarODone + w, vc - 1)) return false;
+        tc_fence_after_sync();
+        issue_s(s);
+        ++kc;
+        return true;
+      };
+      auto q_done = [&]() {
+        if (elect_one()) tc_commit(&bars[L::kBarQEmpty]);
+        __syncwarp();
+      };
+      // D <= 64: S(j+1) before P V(j), so that the next scores are there when
+      // the softmax has written P(j).  D = 128 (P over S): after it.
+      for (int u = u_begin; u < p.n_units && ok; u += u_step) {
+        const int nt = cross_unit(p, u).nt;
+        if (nt == 0) continue;
+        ok = wait(L::kBarQFull, uc) && next_s();
+        if (!ok) break;
+        if (nt == 1) q_done();
+        for (int j = 0; j < nt && ok; ++j) {
+          const bool has_next = j + 1 < nt;
+          const int sv = vc % L::kKVStages;
+          if (!L::kAlias && has_next) {
+            if (!(ok = next_s())) break;
+            // after the unit's last score MMAs the Q slot can be refilled
+            if (j + 2 == nt) q_done();
+          }
+          if (!(ok = wait(fix ? L::kBarVReady + sv : L::kBarVFull + sv, vc / L::kKVStages))) break;
+          if (!(ok = wait(L::kBarPFull + w, vc))) break;
+          // the first P V of a unit overwrites O: the epilogue of the
+          // previous unit must have read it
+          if (j == 0 && uc > 0 && !(ok = wait(L::kBarOFree + w, uc - 1))) break;
+          tc_fence_after_sync();
+          issue_pv(sv, j == 0);
+          ++vc;
+          if (L::kAlias && has_next) {
+            if (!(ok = next_s())) break;
+            if (j + 2 == nt) q_done();
+          }
+        }
+        ++uc;
       }
+      // every MMA issued above completes before Tensor Memory is released
+      if (elect_one()) tc_commit(&bars[L::kBarDrain + w]);
+      __syncwarp();
+      mbar_wait<false>(&bars[L::kBarDrain + w], 0, wc_drain);
     } else if (warp == kXWarpFix && fix) {
       // ============================================================== V rows that do not count
       bool ok = true;
@@ -430,6 +437,8 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
     // in log2 units, so most tiles skip the rescale of O; the kept maximum is
     // used for P and l alike, so the result is unchanged.
     const float slack = fminf(8.f / c_s, 1e30f);
+    uint64_t *my_turn = &bars[L::kBarTurn + w * 4 + (warp & 3)];
+    uint64_t *other_turn = &bars[L::kBarTurn + (1 - w) * 4 + (warp & 3)];
     bool ok = true;
     int gt = 0;  // key tiles processed (all units)
     for (int u = u_begin; u < p.n_units && ok; u += u_step) {
@@ -484,6 +493,14 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
           m_cur = mx;
           neg_m = -mx * c_s;
         }
+        // The exponentials' turn.  Warps w and w + 4 share a scheduler and its
+        // exp2 unit; left alone they fall into step, both in their exponentials
+        // and then both out of them.  Taking turns, one loads, masks and finds
+        // maxima while the other keeps the unit busy.
+        if (w == 1 || gt > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait<false>(my_turn, w == 1 ? (gt & 1) : ((gt - 1) & 1), wc));
+          if (!ok) break;
+        }
         const float2 cs2 = make_float2(c_s, c_s), negm2 = make_float2(neg_m, neg_m);
         uint32_t pk[kXTile / 2];
         float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -495,6 +512,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
           ls[i & 3] = fadd2(ls[i & 3], pv);
           pk[i] = pack_bf16x2(pv.x, pv.y);
         }
+        if (lane == 0) mbar_arrive(other_turn);
         const float2 lsum2 = fadd2(fadd2(ls[0], ls[1]), fadd2(ls[2], ls[3]));
         l += lsum2.x + lsum2.y;
 
