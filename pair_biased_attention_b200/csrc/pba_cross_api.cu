@@ -79,9 +79,9 @@ cudaError_t set_up(K kern, int smem) {
   return e;
 }
 
-template <int D, bool kMasked>
+template <int D>
 cudaError_t launch_cross(const pba::CrossParams &p, int grid, cudaStream_t stream) {
-  auto kern = pba::pba_cross_sm100_kernel<D, kMasked>;
+  auto kern = pba::pba_cross_sm100_kernel<D>;
   constexpr int smem = pba::CrossLayout<D>::kSmemAlloc;
   static PerDeviceOnce once;
   const cudaError_t err = once_per_device(once, [&] { return set_up(kern, smem); });
@@ -117,7 +117,7 @@ pba_status run_tiles(const pba_cross_desc &d, const void *q, const void *k, cons
   if (p.err == nullptr || sms < 1) return PBA_ERR_CUDA;
   p.timeout_ns = wait_timeout_ns();
   const int grid = int(std::min<int64_t>(n_units, sms));  // persistent: one CTA per SM
-  const cudaError_t e = mask != nullptr ? launch_cross<D, true>(p, grid, stream) : launch_cross<D, false>(p, grid, stream);
+  const cudaError_t e = launch_cross<D>(p, grid, stream);
   return e == cudaSuccess ? PBA_OK : PBA_ERR_CUDA;
 }
 
@@ -173,9 +173,9 @@ pba_status run_split(const pba_cross_desc &d, const void *q, const void *k, cons
 // kernel reads them once over the whole card.
 bool few_rows(const pba_cross_desc &d) { return d.H / d.Hkv * d.Nq <= 64; }
 
-template <int D, bool kB, bool kMasked>
+template <int D, bool kB>
 cudaError_t launch_cross_bwd(const pba::CrossBwdParams &p, int64_t grid, cudaStream_t stream) {
-  auto kern = pba::pba_cross_bwd_sm100_kernel<D, kB, kMasked>;
+  auto kern = pba::pba_cross_bwd_sm100_kernel<D, kB>;
   constexpr int smem = pba::CrossBwdLayout<D>::kSmemAlloc;
   static PerDeviceOnce once;
   const cudaError_t err = once_per_device(once, [&] { return set_up(kern, smem); });
@@ -223,15 +223,11 @@ pba_status run_cross_bwd(const pba_cross_desc &d, const void *q, const void *k, 
     pba::pba_cross_delta_kernel<D><<<unsigned(blocks), 256, 0, stream>>>(dp);
     if (cudaGetLastError() != cudaSuccess) return PBA_ERR_CUDA;
     p.n_tiles = int(q_tiles);
-    const cudaError_t e = mask != nullptr ? launch_cross_bwd<D, false, true>(p, grid_a, stream)
-                                          : launch_cross_bwd<D, false, false>(p, grid_a, stream);
-    if (e != cudaSuccess) return PBA_ERR_CUDA;
+    if (launch_cross_bwd<D, false>(p, grid_a, stream) != cudaSuccess) return PBA_ERR_CUDA;
   }
   if (d.Nk > 0) {
     p.n_tiles = int(k_tiles);
-    const cudaError_t e = mask != nullptr ? launch_cross_bwd<D, true, true>(p, grid_b, stream)
-                                          : launch_cross_bwd<D, true, false>(p, grid_b, stream);
-    if (e != cudaSuccess) return PBA_ERR_CUDA;
+    if (launch_cross_bwd<D, true>(p, grid_b, stream) != cudaSuccess) return PBA_ERR_CUDA;
   }
   return PBA_OK;
 }

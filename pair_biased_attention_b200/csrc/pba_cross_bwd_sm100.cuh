@@ -17,7 +17,8 @@
 // One CTA per unit, 384 threads: warps 0-7 two compute warpgroups (row =
 // thread = Tensor Memory lane; warpgroup g takes columns 64g .. 64g+63 of
 // every step), warp 8 the TMA producer, warp 9 Tensor Memory and the MMAs,
-// warp 10 in kernel A zeroes the K rows of keys that do not take part.  For
+// warp 10 in kernel A takes out the keys that do not take part, as in the forward
+// (their rows of K and V are zeros, their scores -inf).  For
 // D <= 64 the next step's S and dP are issued as soon as this step's have been
 // read; at D = 128 P and dS lie over S and dP, so they wait for the products
 // that read them.
@@ -57,11 +58,14 @@ struct CrossBwdLayout {
   // double-buffered by step parity
   static constexpr int kRowvFloats = kXTile;
   static constexpr int kOffRowv = kOffStep1 + kStages * T::kBytes;
-  static constexpr int kOffBar = kOffRowv + 2 * 8 * kRowvFloats * 4;
+  static constexpr int kOffOnes = kOffRowv + 2 * 8 * kRowvFloats * 4;
+  static constexpr int kOffMask = kOffOnes + XMaskTile::kBytes;              // [stage]
+  static constexpr int kOffPartial = kOffMask + kStages * XMaskTile::kBytes;  // [stage]: the tile needs its column
+  static constexpr int kOffBar = kOffPartial + 16;
   static constexpr int kBarFixFull = 0;
   static constexpr int kBarStepFull = 1;
   static constexpr int kBarStepEmpty = kBarStepFull + kStages;
-  static constexpr int kBarStepReady = kBarStepEmpty + kStages;  // A: masked K rows zeroed
+  static constexpr int kBarStepReady = kBarStepEmpty + kStages;  // A: keys that do not take part are out
   static constexpr int kBarSFull = kBarStepReady + kStages;
   static constexpr int kBarSFree = kBarSFull + 1;
   static constexpr int kBarGFull = kBarSFree + 1;  // P / dS written to Tensor Memory
@@ -84,7 +88,7 @@ struct CrossBwdLayout {
 };
 
 // kB = false: kernel A (dq); kB = true: kernel B (dk, dv).
-template <int D, bool kB, bool kMasked>
+template <int D, bool kB>
 __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const __grid_constant__ CrossBwdParams p) {
   using L = CrossBwdLayout<D>;
   using T = typename L::T;
@@ -105,7 +109,8 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
   const int q_tiles = (p.Nq + kXTile - 1) / kXTile;
   // B: a key tile with no key that counts has no steps (its gradients are 0)
   const int nsteps = kB ? (row0 < keys ? p.group * q_tiles : 0) : (keys + kXTile - 1) / kXTile;
-  const bool fix = !kB && (kMasked || p.k_len != nullptr);
+  const bool fix = !kB && (p.mask != nullptr || p.k_len != nullptr || p.Nk % kXTile != 0);
+  volatile int *partial = reinterpret_cast<volatile int *>(smem + L::kOffPartial);
 
   if (threadIdx.x == 0) {
     mbar_init(&bars[L::kBarFixFull], 1);
@@ -121,6 +126,13 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
     mbar_init(&bars[L::kBarDrain], 1);
     *abort_flag = 0;
     fence_barrier_init();
+  }
+  if (!kB) {  // zeros but for the ones
+    for (int i = threadIdx.x; i < (1 + L::kStages) * XMaskTile::kBytes / 16; i += kXThreads)
+      reinterpret_cast<uint4 *>(smem + L::kOffOnes)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    if (threadIdx.x < kXTile) *XMaskTile::at(smem + L::kOffOnes, threadIdx.x) = 0x3F80u;
+    fence_proxy_async_smem();
   }
   if (warp == kXWarpMma) {
     tmem_alloc(tmem_slot, 512);
@@ -190,11 +202,17 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
           tc_fence_after_sync();
           const uint32_t b0 = smem_desc_lo(smem0 + L::kOffStep0 + s * T::kBytes, 16);
           const uint32_t b1 = smem_desc_lo(smem0 + L::kOffStep1 + s * T::kBytes, 16);
+          const uint32_t ones_lo = smem_desc_lo(smem0 + L::kOffOnes, 16);
+          const uint32_t mask_lo = smem_desc_lo(smem0 + L::kOffMask + s * XMaskTile::kBytes, 16);
+          const bool masked = fix && partial[s] != 0;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               mma_bf16_ss(tm + L::kColS, desc_join(a0 + T::k_step(kk), T::kDescHi),
                           desc_join(b0 + T::k_step(kk), T::kDescHi), idesc_s, kk > 0);
+            if (masked)
+              mma_bf16_ss(tm + L::kColS, desc_join(ones_lo, XMaskTile::kDescHi),
+                          desc_join(mask_lo, XMaskTile::kDescHi), idesc_s, 1u);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               mma_bf16_ss(tm + L::kColDP, desc_join(a1 + T::k_step(kk), T::kDescHi),
@@ -234,21 +252,25 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
         mbar_wait<false>(&bars[L::kBarDrain], 0, wc_drain);
       }
     } else if (warp == kXWarpFix && fix) {
-      // ================================================================ A: K rows that do not count
-      const uint8_t *mrow = kMasked ? p.mask + int64_t(b) * p.mask_sb : nullptr;
+      // ================================================================ A: keys that do not take part
+      const uint8_t *mrow = p.mask != nullptr ? p.mask + int64_t(b) * p.mask_sb : nullptr;
       bool ok = true;
+      uint32_t next = nsteps > 0 ? cross_mask_bytes(mrow, p.mask_vec4, 0, keys, lane) : 0u;
       for (int it = 0; it < nsteps && ok; ++it) {
         const int s = it % L::kStages;
-        KeepWords keep;
-        if (kMasked) keep = cross_keep(cross_mask_bytes(mrow, p.mask_vec4, it * kXTile, keys, lane));
+        const KeepWords keep = cross_keep(next);
+        if (it + 1 < nsteps) next = cross_mask_bytes(mrow, p.mask_vec4, (it + 1) * kXTile, keys, lane);
         ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarStepFull + s], (it / L::kStages) & 1, wc));
         if (!ok) break;
-        const int n = min(kXTile, keys - it * kXTile);
-        if (kMasked ? !keep.all() : n < kXTile) {
-          for (int r = 0; r < kXTile; ++r)
-            if (!(kMasked ? keep.has(r) : r < n)) T::zero_row(smem + L::kOffStep0 + s * T::kBytes, r, lane);
+        const bool any = !keep.all();
+        if (any) {
+          cross_zero_rows<D>(smem + L::kOffStep0 + s * T::kBytes, keep, lane);
+          cross_zero_rows<D>(smem + L::kOffStep1 + s * T::kBytes, keep, lane);
+          cross_mask_column(smem + L::kOffMask + s * XMaskTile::kBytes, keep, lane);
           fence_proxy_async_smem();
         }
+        if (lane == 0) partial[s] = any;
+        __syncwarp();
         mbar_arrive(&bars[L::kBarStepReady + s]);
       }
     }
@@ -260,28 +282,26 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const int r = row0 + t;            // A: query row; B: key row
     const float c_s = p.tau * kXLog2e;
-    const uint8_t *mrow = kMasked ? p.mask + int64_t(b) * p.mask_sb : nullptr;
     float lse2 = 0.f, delta = 0.f;     // A: this row's
-    uint32_t key_keep = 0xFFFFFFFFu;   // B: all bits if this row's key takes part
+    bool key_ok = true;                // B: this row's key takes part
     if (!kB) {
       if (r < p.Nq) {
-        // a row without a key (lse = -inf) gets a finite stand-in; none of its
-        // keys counts, so nothing of it is used
+        // a row without a key (lse = -inf) gets a finite stand-in: its scores
+        // are all -inf already
         const float lse = p.lse[b * p.lse_sb + h * p.lse_sh + int64_t(r) * p.lse_sn];
         lse2 = (lse == -INFINITY) ? 0.f : lse * kXLog2e;
         delta = p.delta[(int64_t(b) * p.H + h) * p.Nq + r];
       }
-    } else if (r >= keys || (kMasked && mrow[r] == 0)) {
-      key_keep = 0u;
+    } else {
+      // a key that does not take part keeps its row to itself: what the row
+      // sums up to, NaN included, is dropped at the end
+      key_ok = r < keys && (p.mask == nullptr || p.mask[int64_t(b) * p.mask_sb + r] != 0);
     }
-    // Column data of a step, loaded a step ahead.  A: mask bytes of four keys;
-    // B: lse and Delta of query columns `lane` and `lane + 32`.
-    uint32_t nmask = 0;
+    // B: lse and Delta of a step's query columns `lane` and `lane + 32`, loaded
+    // a step ahead
     float nlse[2] = {0.f, 0.f}, ndelta[2] = {0.f, 0.f};
     auto load_cols = [&](int step) {
-      if (!kB) {
-        if (kMasked) nmask = cross_mask_bytes(mrow, p.mask_vec4, step * kXTile, keys, lane);
-      } else {
+      if (kB) {
         const int qh = h * p.group + step / q_tiles;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -296,20 +316,10 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
     if (nsteps > 0) load_cols(0);
     bool ok = true;
     for (int it = 0; it < nsteps && ok; ++it) {
-      const uint32_t cmask = nmask;
       const float clse[2] = {nlse[0], nlse[1]}, cdelta[2] = {ndelta[0], ndelta[1]};
       if (it + 1 < nsteps) load_cols(it + 1);
       float *rv = reinterpret_cast<float *>(smem + L::kOffRowv) + ((it & 1) * 8 + warp) * L::kRowvFloats;
-      KeepWords keep;
-      bool partial = false;  // A: some of the tile's keys do not count
-      if (!kB) {
-        if (kMasked) {
-          keep = cross_keep(cmask);
-          partial = !keep.all();
-        } else {
-          partial = keys - it * kXTile < kXTile;
-        }
-      } else {
+      if (kB) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int col = lane + 32 * e;
@@ -355,19 +365,8 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
             const float2 a = ffma2(make_float2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])), cs2, nl[e]);
             const float2 pe = make_float2(ex2_approx(a.x), ex2_approx(a.y));
             const float2 ds = fmul2(pe, fadd2(make_float2(__uint_as_float(dpv[i]), __uint_as_float(dpv[i + 1])), nd[e]));
-            if (kB) pk[j4 * 2 + e] = pack_bf16x2(pe.x, pe.y) & key_keep;
+            if (kB) pk[j4 * 2 + e] = pack_bf16x2(pe.x, pe.y);
             dk[j4 * 2 + e] = pack_bf16x2(ds.x, ds.y);
-            if (kB) dk[j4 * 2 + e] &= key_keep;
-          }
-        }
-        if (!kB && partial) {
-          // pairs of keys that do not count become zeros, whatever was there
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int c = g * 64 + qt * 32 + 2 * j;
-            const int n = keys - it * kXTile;
-            const bool k0 = kMasked ? keep.has(c) : c < n, k1 = kMasked ? keep.has(c + 1) : c + 1 < n;
-            dk[j] &= (k0 ? 0x0000FFFFu : 0u) | (k1 ? 0xFFFF0000u : 0u);
           }
         }
         if (!L::kAlias && qt == 0 && it > 0) {
@@ -411,8 +410,9 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16x2(__uint_as_float(v[8 * q + 2 * e]) * scale,
-                                 __uint_as_float(v[8 * q + 2 * e + 1]) * scale);
+              w[e] = key_ok ? pack_bf16x2(__uint_as_float(v[8 * q + 2 * e]) * scale,
+                                          __uint_as_float(v[8 * q + 2 * e + 1]) * scale)
+                            : 0u;
             o[q] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }

@@ -16,7 +16,7 @@
 //   warp 8      TMA producer of Q (per unit) and of K and V
 //   warps 9, 11 issue the tcgen05.mma of query tile 0 and 1 (9 allocates
 //               Tensor Memory)
-//   warp 10     zeroes the V rows of keys that do not take part
+//   warp 10     takes out the keys that do not take part
 // Without a bias nothing streams from HBM while a unit runs (K and V of a head
 // stay in L2), so what bounds the kernel is the exponentials: per key tile and
 // SM 2 x 128 x 128 of them, 2048 cycles of the exp2 unit, against 1050 cycles
@@ -28,8 +28,12 @@
 // one.  D = 128: O0 and O1 take [256,512) and P lies over its own S, whose next
 // tile then waits for the product with V; the two query tiles alternate.
 //
-// A masked key's score is replaced by -inf and its V row by zeros, so that
-// what lies there, NaN included, does not matter.
+// Keys that do not take part cost the softmax nothing: warp 10 zeroes their
+// rows of K and V in shared memory, so that what lies there, NaN included, does
+// not matter, and in a tile that has any it fills one more column of K, 0 or
+// -inf per key, which meets a column of ones beside Q in one more MMA of the
+// score tile (K = 16).  Selecting among the 128 scores of a row in registers
+// instead took 35 of 93 us at 2048 x 2048 keys, 32 heads, one key in ten masked.
 #pragma once
 
 #include <cuda.h>
@@ -70,11 +74,11 @@ struct XTileLayout {
   }
   // and of an MN-major one (16 rows down)
   static constexpr __host__ __device__ uint32_t mn_step(int kk) { return uint32_t(kk * 16 * kRowBytes) / 16; }
-  // zeroes row r of a tile at `tile`; `lane` of 32 threads takes a share
-  static __device__ __forceinline__ void zero_row(uint8_t *tile, int r, int lane) {
+  static __device__ __forceinline__ void zero_row(uint8_t *tile, int r) {
     // a row is the same 16-byte chunks whatever their swizzled order
-    if (lane < kSlabs * (kRowBytes / 16)) {
-      const int slab = lane / (kRowBytes / 16), chunk = lane % (kRowBytes / 16);
+#pragma unroll
+    for (int i = 0; i < kSlabs * (kRowBytes / 16); ++i) {
+      const int slab = i / (kRowBytes / 16), chunk = i % (kRowBytes / 16);
       *reinterpret_cast<uint4 *>(tile + slab * kSlabBytes + r * kRowBytes + chunk * 16) = make_uint4(0, 0, 0, 0);
     }
   }
@@ -112,6 +116,10 @@ __device__ __forceinline__ int cross_keys(const int32_t *k_len, int b, int Nk) {
 // bit l of word e is key 4 l + e.  `bytes` is what cross_mask_bytes read.
 __device__ __forceinline__ uint32_t cross_mask_bytes(const uint8_t *row, bool vec4, int key0, int keys, int lane) {
   const int k = key0 + 4 * lane;
+  if (row == nullptr) {  // no mask: all keys before the end
+    const int n = min(max(keys - k, 0), 4);
+    return n == 0 ? 0u : 0x01010101u >> (32 - 8 * n);
+  }
   if (vec4 && k + 3 < keys) return __ldg(reinterpret_cast<const uint32_t *>(row + k));
   uint32_t v = 0;
 #pragma unroll
@@ -122,13 +130,36 @@ __device__ __forceinline__ uint32_t cross_mask_bytes(const uint8_t *row, bool ve
 struct KeepWords {
   uint32_t w[4];
   __device__ __forceinline__ bool all() const { return (w[0] & w[1] & w[2] & w[3]) == 0xFFFFFFFFu; }
-  __device__ __forceinline__ bool has(int key) const { return (w[key & 3] >> (key >> 2)) & 1u; }
 };
 __device__ __forceinline__ KeepWords cross_keep(uint32_t bytes) {
   KeepWords k;
 #pragma unroll
   for (int e = 0; e < 4; ++e) k.w[e] = __ballot_sync(0xffffffffu, ((bytes >> (8 * e)) & 0xFFu) != 0);
   return k;
+}
+
+// The column of ones beside Q and the columns of 0 and -inf beside K: [128][16]
+// bf16 tiles, K-major, 32-byte swizzle, of which only feature 0 is not 0.
+struct XMaskTile {
+  static constexpr int kBytes = kXTile * 32;
+  static constexpr uint32_t kDescHi = smem_desc_hi(256, 6);
+  // feature 0 of row r: the 16-byte chunk's place in the row follows bit 2 of r
+  static __device__ __forceinline__ uint16_t *at(uint8_t *tile, int r) {
+    return reinterpret_cast<uint16_t *>(tile + r * 32 + ((r >> 2) & 1) * 16);
+  }
+};
+// By one warp: zeroes the rows of `tile` (of D features) whose keys do not take
+// part, each lane its own four.
+template <int D>
+__device__ __forceinline__ void cross_zero_rows(uint8_t *tile, const KeepWords &keep, int lane) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (!((keep.w[e] >> lane) & 1u)) XTileLayout<D>::zero_row(tile, 4 * lane + e);
+}
+// By one warp: the column of a tile's keys.
+__device__ __forceinline__ void cross_mask_column(uint8_t *tile, const KeepWords &keep, int lane) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) *XMaskTile::at(tile, 4 * lane + e) = (keep.w[e] >> lane) & 1u ? 0x0000u : 0xFF80u;
 }
 
 template <int D>
@@ -139,14 +170,19 @@ struct CrossLayout {
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + kXQTiles * T::kBytes;
   static constexpr int kOffV = kOffK + kKVStages * T::kBytes;
-  static constexpr int kOffBar = kOffV + kKVStages * T::kBytes;
+  static constexpr int kOffOnes = kOffV + kKVStages * T::kBytes;
+  static constexpr int kOffMask = kOffOnes + XMaskTile::kBytes;                // [K stage]
+  static constexpr int kOffPartial = kOffMask + kKVStages * XMaskTile::kBytes;  // [K stage]: the tile needs its column
+  static constexpr int kOffBar = kOffPartial + 16;
+  static_assert(kKVStages * 4 <= 16, "flags");
   static constexpr int kBarQFull = 0;
   static constexpr int kBarQEmpty = 1;
   static constexpr int kBarKFull = 2;
   static constexpr int kBarVFull = kBarKFull + kKVStages;
   static constexpr int kBarKEmpty = kBarVFull + kKVStages;
   static constexpr int kBarVEmpty = kBarKEmpty + kKVStages;
-  static constexpr int kBarVReady = kBarVEmpty + kKVStages;  // masked rows zeroed
+  static constexpr int kBarKReady = kBarVEmpty + kKVStages;  // keys that do not take part are out
+  static constexpr int kBarVReady = kBarKReady + kKVStages;
   static constexpr int kBarSFull = kBarVReady + kKVStages;   // [w]
   static constexpr int kBarSFree = kBarSFull + kXQTiles;
   static constexpr int kBarPFull = kBarSFree + kXQTiles;
@@ -179,9 +215,7 @@ __device__ __forceinline__ CrossUnit cross_unit(const CrossParams &p, int u) {
   return x;
 }
 
-// kMasked: a key mask is given.  Key lengths need no variant: they end the
-// loop over the tiles, and the last tile's tail is cut off by its length.
-template <int D, bool kMasked>
+template <int D>
 __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __grid_constant__ CrossParams p) {
   using L = CrossLayout<D>;
   using T = typename L::T;
@@ -194,9 +228,9 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int u_begin = blockIdx.x, u_step = gridDim.x;
-  // V rows past the keys' end are zeros by the tile load itself when the
-  // tensor ends there; otherwise warp 10 looks at every tile
-  const bool fix = kMasked || p.k_len != nullptr;
+  // whole tiles of keys that all take part: nothing for warp 10 to do
+  const bool fix = p.mask != nullptr || p.k_len != nullptr || p.Nk % kXTile != 0;
+  volatile int *partial = reinterpret_cast<volatile int *>(smem + L::kOffPartial);
 
   if (threadIdx.x == 0) {
     mbar_init(&bars[L::kBarQFull], 1);
@@ -206,6 +240,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
       mbar_init(&bars[L::kBarVFull + s], 1);
       mbar_init(&bars[L::kBarKEmpty + s], kXQTiles);
       mbar_init(&bars[L::kBarVEmpty + s], kXQTiles);
+      mbar_init(&bars[L::kBarKReady + s], 32);
       mbar_init(&bars[L::kBarVReady + s], 32);
     }
     for (int w = 0; w < kXQTiles; ++w) {
@@ -220,6 +255,12 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
     *abort_flag = 0;
     fence_barrier_init();
   }
+  // zeros but for the ones
+  for (int i = threadIdx.x; i < (1 + L::kKVStages) * XMaskTile::kBytes / 16; i += kXThreads)
+    reinterpret_cast<uint4 *>(smem + L::kOffOnes)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  if (threadIdx.x < kXTile) *XMaskTile::at(smem + L::kOffOnes, threadIdx.x) = 0x3F80u;
+  fence_proxy_async_smem();
   if (warp == kXWarpMma) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -318,11 +359,16 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
       };
       auto issue_s = [&](int s) {
         const uint32_t k_lo = smem_desc_lo(smem0 + L::kOffK + s * T::kBytes, 16);
+        const uint32_t ones_lo = smem_desc_lo(smem0 + L::kOffOnes, 16);
+        const uint32_t mask_lo = smem_desc_lo(smem0 + L::kOffMask + s * XMaskTile::kBytes, 16);
+        const bool masked = fix && partial[s] != 0;
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             mma_bf16_ss(tS, desc_join(q_lo + T::k_step(kk), T::kDescHi), desc_join(k_lo + T::k_step(kk), T::kDescHi),
                         idesc_s, kk > 0 ? 1u : 0u);
+          if (masked)
+            mma_bf16_ss(tS, desc_join(ones_lo, XMaskTile::kDescHi), desc_join(mask_lo, XMaskTile::kDescHi), idesc_s, 1u);
           tc_commit(&bars[L::kBarSFull + w]);
           tc_commit(&bars[L::kBarKEmpty + s]);
         }
@@ -344,7 +390,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
       // over it) has been read
       auto next_s = [&]() -> bool {
         const int s = kc % L::kKVStages;
-        if (!wait(L::kBarKFull + s, kc / L::kKVStages)) return false;
+        if (!wait((fix ? L::kBarKReady : L::kBarKFull) + s, kc / L::kKVStages)) return false;
         if (kc > 0 && !wait(L::kBarSFree + w, kc - 1)) return false;
         if (L::kAlias && vc > 0 && !wait(L::kBarODone + w, vc - 1)) return false;
         tc_fence_after_sync();
@@ -392,34 +438,55 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
       __syncwarp();
       mbar_wait<false>(&bars[L::kBarDrain + w], 0, wc_drain);
     } else if (warp == kXWarpFix && fix) {
-      // ============================================================== V rows that do not count
+      // ============================================================== keys that do not take part
       bool ok = true;
-      int vc = 0;
+      int kc = 0, vc = 0;
+      auto wait = [&](int bar, int parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait<false>(&bars[bar], parity & 1, wc));
+      };
+      auto fix_k = [&](const KeepWords &keep) -> bool {
+        const int s = kc % L::kKVStages;
+        if (!wait(L::kBarKFull + s, kc / L::kKVStages)) return false;
+        const bool any = !keep.all();
+        if (any) {
+          cross_zero_rows<D>(smem + L::kOffK + s * T::kBytes, keep, lane);
+          cross_mask_column(smem + L::kOffMask + s * XMaskTile::kBytes, keep, lane);
+          fence_proxy_async_smem();
+        }
+        if (lane == 0) partial[s] = any;
+        __syncwarp();
+        mbar_arrive(&bars[L::kBarKReady + s]);
+        ++kc;
+        return true;
+      };
+      auto fix_v = [&](const KeepWords &keep) -> bool {
+        const int s = vc % L::kKVStages;
+        if (!wait(L::kBarVFull + s, vc / L::kKVStages)) return false;
+        if (!keep.all()) {
+          cross_zero_rows<D>(smem + L::kOffV + s * T::kBytes, keep, lane);
+          fence_proxy_async_smem();
+        }
+        mbar_arrive(&bars[L::kBarVReady + s]);
+        ++vc;
+        return true;
+      };
+      // in the order of the loads: K runs one tile ahead of V
       for (int u = u_begin; u < p.n_units && ok; u += u_step) {
         const CrossUnit un = cross_unit(p, u);
-        const uint8_t *mrow = kMasked ? p.mask + int64_t(un.b) * p.mask_sb : nullptr;
-        uint32_t next = kMasked && un.nt > 0 ? cross_mask_bytes(mrow, p.mask_vec4, 0, un.keys, lane) : 0u;
-        for (int j = 0; j < un.nt && ok; ++j, ++vc) {
-          const int s = vc % L::kKVStages;
-          KeepWords keep;
-          if (kMasked) {
+        if (un.nt == 0) continue;
+        const uint8_t *mrow = p.mask != nullptr ? p.mask + int64_t(un.b) * p.mask_sb : nullptr;
+        auto bytes = [&](int j) { return cross_mask_bytes(mrow, p.mask_vec4, j * kXTile, un.keys, lane); };
+        KeepWords keep = cross_keep(bytes(0));
+        uint32_t next = un.nt > 1 ? bytes(1) : 0u;
+        ok = fix_k(keep);
+        for (int j = 0; j < un.nt && ok; ++j) {
+          const KeepWords v_keep = keep;
+          if (j + 1 < un.nt) {
             keep = cross_keep(next);
-            if (j + 1 < un.nt) next = cross_mask_bytes(mrow, p.mask_vec4, (j + 1) * kXTile, un.keys, lane);
+            if (j + 2 < un.nt) next = bytes(j + 2);
+            ok = fix_k(keep);
           }
-          ok = mbar_wait<false>(&bars[L::kBarVFull + s], (vc / L::kKVStages) & 1, wc);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          uint8_t *tile = smem + L::kOffV + s * T::kBytes;
-          const int n = min(kXTile, un.keys - j * kXTile);
-          const bool any = kMasked ? !keep.all() : n < kXTile;
-          if (any) {
-            for (int r = 0; r < kXTile; ++r) {
-              const bool has = kMasked ? keep.has(r) : r < n;
-              if (!has) T::zero_row(tile, r, lane);
-            }
-            fence_proxy_async_smem();
-          }
-          mbar_arrive(&bars[L::kBarVReady + s]);
+          if (ok) ok = fix_v(v_keep);
         }
       }
     }
@@ -443,17 +510,10 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
     int gt = 0;  // key tiles processed (all units)
     for (int u = u_begin; u < p.n_units && ok; u += u_step) {
       const CrossUnit un = cross_unit(p, u);
-      const uint8_t *mrow = kMasked ? p.mask + int64_t(un.b) * p.mask_sb : nullptr;
-      uint32_t next = kMasked && un.nt > 0 ? cross_mask_bytes(mrow, p.mask_vec4, 0, un.keys, lane) : 0u;
       float m_cur = -INFINITY;  // maximum used for P and l (raw scores)
       float neg_m = 0.f;        // -m_cur in log2 units (0 while there is none)
       float l = 0.f;
       for (int j = 0; j < un.nt && ok; ++j, ++gt) {
-        KeepWords keep;
-        if (kMasked) {
-          keep = cross_keep(next);
-          if (j + 1 < un.nt) next = cross_mask_bytes(mrow, p.mask_vec4, (j + 1) * kXTile, un.keys, lane);
-        }
         // the loads below are warp-collective: a warp leaves its waits as one
         ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarSFull + w], gt & 1, wc));
         if (!ok) break;
@@ -467,16 +527,6 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
         tc_fence_before_sync();
         mbar_arrive(&bars[L::kBarSFree + w]);
 
-        if (kMasked) {
-          if (!keep.all()) {
-#pragma unroll
-            for (int c = 0; c < kXTile; ++c) sreg[c] = keep.has(c) ? sreg[c] : 0xFF800000u;
-          }
-        } else if (un.keys - j * kXTile < kXTile) {
-          const int n = un.keys - j * kXTile;
-#pragma unroll
-          for (int c = 0; c < kXTile; ++c) sreg[c] = c < n ? sreg[c] : 0xFF800000u;
-        }
         // tile maximum: eight independent chains
         float m8[8];
 #pragma unroll
