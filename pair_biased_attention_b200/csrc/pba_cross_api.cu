@@ -42,11 +42,12 @@ bool rows_ok(const int64_t s[3], int64_t B, int64_t H, int64_t N) {
   return (B <= 1 || s[0] % 8 == 0) && (H <= 1 || s[1] % 8 == 0) && (N <= 1 || s[2] % 8 == 0);
 }
 
-// [B][heads][n][D] as (D, n, heads, B): boxes of 128 rows of at most 64 features.
-bool cross_map(CUtensorMap *m, const void *base, int64_t D, int64_t n, int64_t heads, int64_t B, const int64_t s[3]) {
+// [B][heads][n][D] as (D, n, heads, B): boxes of `rows` rows of at most 64 features.
+bool cross_map(CUtensorMap *m, const void *base, int64_t D, int64_t n, int64_t heads, int64_t B, const int64_t s[3],
+               int rows = pba::kXTile) {
   const uint64_t dims[4] = {uint64_t(D), uint64_t(n), uint64_t(heads), uint64_t(B)};
   const int64_t st[3] = {s[2] * 2, s[1] * 2, s[0] * 2};
-  const uint32_t box[4] = {uint32_t(std::min<int64_t>(D, 64)), uint32_t(pba::kXTile), 1, 1};
+  const uint32_t box[4] = {uint32_t(std::min<int64_t>(D, 64)), uint32_t(rows), 1, 1};
   return make_map(m, base, dims, st, box, D == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
@@ -190,16 +191,10 @@ pba_status run_cross_bwd(const pba_cross_desc &d, const void *q, const void *k, 
                          void *dk, void *dv, float *delta, cudaStream_t stream) {
   pba::CrossBwdParams p;
   std::memset(&p, 0, sizeof(p));
-  if (d.Nq > 0 && (!cross_map(&p.tm_q, q, D, d.Nq, d.H, d.B, d.q_stride) ||
-                   !cross_map(&p.tm_do, dout, D, d.Nq, d.H, d.B, d.dout_stride)))
-    return PBA_ERR_INVALID_ARG;
-  if (d.Nk > 0 && (!cross_map(&p.tm_k, k, D, d.Nk, d.Hkv, d.B, d.k_stride) ||
-                   !cross_map(&p.tm_v, v, D, d.Nk, d.Hkv, d.B, d.v_stride)))
-    return PBA_ERR_INVALID_ARG;
   p.B = int(d.B), p.H = int(d.H), p.Hkv = int(d.Hkv), p.group = int(d.H / d.Hkv), p.Nq = int(d.Nq), p.Nk = int(d.Nk);
   p.tau = cross_tau(&d);
   p.k_len = k_len;
-  p.mask = mask, p.mask_sb = d.mask_stride_b, p.mask_vec4 = mask_words(d, mask);
+  p.mask = mask, p.mask_sb = d.mask_stride_b;
   p.lse = lse;
   p.lse_sb = d.lse_stride[0], p.lse_sh = d.lse_stride[1], p.lse_sn = d.lse_stride[2];
   p.delta = delta;
@@ -209,7 +204,7 @@ pba_status run_cross_bwd(const pba_cross_desc &d, const void *q, const void *k, 
   p.timeout_ns = wait_timeout_ns();
   const int64_t q_tiles = ceil_div(d.Nq, pba::kXTile), k_tiles = ceil_div(d.Nk, pba::kXTile);
   const int64_t grid_a = d.B * d.H * q_tiles, grid_b = d.B * d.Hkv * k_tiles;
-  if (grid_a > kMaxI32 || grid_b > kMaxI32 || d.H / d.Hkv * q_tiles > kMaxI32) return PBA_ERR_INVALID_ARG;
+  if (grid_a > kMaxI32 || grid_b > kMaxI32 || d.H / d.Hkv * q_tiles * 2 > kMaxI32) return PBA_ERR_INVALID_ARG;
   if (d.Nq > 0) {
     pba::CrossDeltaParams dp;
     dp.dout = static_cast<const uint16_t *>(dout), dp.out = static_cast<const uint16_t *>(out);
@@ -223,10 +218,23 @@ pba_status run_cross_bwd(const pba_cross_desc &d, const void *q, const void *k, 
     pba::pba_cross_delta_kernel<D><<<unsigned(blocks), 256, 0, stream>>>(dp);
     if (cudaGetLastError() != cudaSuccess) return PBA_ERR_CUDA;
     p.n_tiles = int(q_tiles);
+    if (!cross_map(&p.tm_fix0, q, D, d.Nq, d.H, d.B, d.q_stride) ||
+        !cross_map(&p.tm_fix1, dout, D, d.Nq, d.H, d.B, d.dout_stride))
+      return PBA_ERR_INVALID_ARG;
+    // without a key no unit has a step
+    if (d.Nk > 0 && (!cross_map(&p.tm_step0, k, D, d.Nk, d.Hkv, d.B, d.k_stride, pba::kXStep) ||
+                     !cross_map(&p.tm_step1, v, D, d.Nk, d.Hkv, d.B, d.v_stride, pba::kXStep)))
+      return PBA_ERR_INVALID_ARG;
     if (launch_cross_bwd<D, false>(p, grid_a, stream) != cudaSuccess) return PBA_ERR_CUDA;
   }
   if (d.Nk > 0) {
     p.n_tiles = int(k_tiles);
+    if (!cross_map(&p.tm_fix0, k, D, d.Nk, d.Hkv, d.B, d.k_stride) ||
+        !cross_map(&p.tm_fix1, v, D, d.Nk, d.Hkv, d.B, d.v_stride))
+      return PBA_ERR_INVALID_ARG;
+    if (d.Nq > 0 && (!cross_map(&p.tm_step0, q, D, d.Nq, d.H, d.B, d.q_stride, pba::kXStep) ||
+                     !cross_map(&p.tm_step1, dout, D, d.Nq, d.H, d.B, d.dout_stride, pba::kXStep)))
+      return PBA_ERR_INVALID_ARG;
     if (launch_cross_bwd<D, true>(p, grid_b, stream) != cudaSuccess) return PBA_ERR_CUDA;
   }
   return PBA_OK;

@@ -7,36 +7,39 @@
 //     dk_j = tau sum dS_ij q_i,  dv_j = sum P_ij dO_i     (kernel B, over the
 //                                 queries of every head that shares key head)
 //
-// Kernel A walks the key tiles of one 128-row query tile: S = Q K^T and dP =
-// dO V^T into Tensor Memory, dS in registers and back to Tensor Memory as
-// bf16, dQ += dS K.  Kernel B walks the query tiles, head by head of the group,
-// of one 128-row key tile: S^T = K Q^T, dP^T = V dO^T, then dV += P^T dO and
+// Kernel A walks the keys of one 128-row query tile, 64 at a step: S = Q K^T and
+// dP = dO V^T into Tensor Memory, dS in registers and back to Tensor Memory as
+// bf16, dQ += dS K.  Kernel B walks the queries, head by head of the group, of
+// one 128-row key tile: S^T = K Q^T, dP^T = V dO^T, then dV += P^T dO and
 // dK += dS^T Q.  No atomics and nothing of size Nq Nk in memory: each gradient
 // is summed in one accumulator in one order.
 //
 // One CTA per unit, 384 threads: warps 0-7 two compute warpgroups (row =
-// thread = Tensor Memory lane; warpgroup g takes columns 64g .. 64g+63 of
-// every step), warp 8 the TMA producer, warp 9 Tensor Memory and the MMAs,
-// warp 10 in kernel A takes out the keys that do not take part, as in the forward
-// (their rows of K and V are zeros, their scores -inf).  For
-// D <= 64 the next step's S and dP are issued as soon as this step's have been
-// read; at D = 128 P and dS lie over S and dP, so they wait for the products
-// that read them.
+// thread = Tensor Memory lane), which take the steps in turn, each with its own
+// S and dP, so that one's exponentials run while the other waits for its scores
+// or stores; warp 8 the TMA producer, warps 9 and 11 the MMAs, warp 10
+// in kernel A takes out the keys that do not take part, as in the forward (their
+// rows of K and V are zeros, their scores -inf).  For D <= 64 a warpgroup's next
+// S and dP are issued as soon as these have been read; at D = 128 P and dS lie
+// over S and dP, so they wait for the products that read them.
 #pragma once
 
 #include "pba_cross_sm100.cuh"
 
 namespace pba {
 
+constexpr int kXStep = 64;  // keys (A) or queries (B) of a step
+
 struct CrossBwdParams {
-  CUtensorMap tm_q, tm_k, tm_v, tm_do;  // (D, n, heads, B) bf16, box {min(D, 64), 128, 1, 1}
+  // (D, n, heads, B) bf16.  The unit's own rows (A: Q, dO; B: K, V): box
+  // {min(D, 64), 128, 1, 1}; the steps' (A: K, V; B: Q, dO): 64 rows
+  CUtensorMap tm_fix0, tm_fix1, tm_step0, tm_step1;
   int32_t B, H, Hkv, group, Nq, Nk;
   int32_t n_tiles;      // A: ceil(Nq / 128) per (b, h); B: ceil(Nk / 128) per (b, hkv)
   float tau;
   const int32_t *k_len;
   const uint8_t *mask;
   int64_t mask_sb;
-  int32_t mask_vec4;
   const float *lse;     // [B][H][Nq] with strides
   int64_t lse_sb, lse_sh, lse_sn;
   const float *delta;   // [B][H][Nq] contiguous
@@ -47,44 +50,47 @@ struct CrossBwdParams {
 
 template <int D>
 struct CrossBwdLayout {
-  using T = XTileLayout<D>;
+  using T = XTileLayout<D>;          // the unit's rows
+  using S = XTileLayout<D, kXStep>;  // a step's
   static constexpr bool kAlias = D == 128;
-  static constexpr int kStages = D == 128 ? 2 : 3;
+  static constexpr int kStages = D == 128 ? 4 : 6;
   static constexpr int kOffFix0 = 0;
   static constexpr int kOffFix1 = kOffFix0 + T::kBytes;
   static constexpr int kOffStep0 = kOffFix1 + T::kBytes;             // [stage]
-  static constexpr int kOffStep1 = kOffStep0 + kStages * T::kBytes;  // [stage]
-  // B: per compute warp -lse log2(e) and -Delta of its 64 query columns,
-  // double-buffered by step parity
-  static constexpr int kRowvFloats = kXTile;
-  static constexpr int kOffRowv = kOffStep1 + kStages * T::kBytes;
+  static constexpr int kOffStep1 = kOffStep0 + kStages * S::kBytes;  // [stage]
+  // B: per compute warp -lse log2(e) and -Delta of the step's 64 query columns,
+  // double-buffered by the parity of the warpgroup's steps
+  static constexpr int kRowvFloats = 2 * kXStep;
+  static constexpr int kOffRowv = kOffStep1 + kStages * S::kBytes;
+  static constexpr int kMaskBytes = kXStep * XMaskTile::kRowBytes;
   static constexpr int kOffOnes = kOffRowv + 2 * 8 * kRowvFloats * 4;
-  static constexpr int kOffMask = kOffOnes + XMaskTile::kBytes;              // [stage]
-  static constexpr int kOffPartial = kOffMask + kStages * XMaskTile::kBytes;  // [stage]: the tile needs its column
-  static constexpr int kOffBar = kOffPartial + 16;
+  static constexpr int kOffMask = kOffOnes + kXTile * XMaskTile::kRowBytes;  // [stage]
+  static constexpr int kOffPartial = kOffMask + kStages * kMaskBytes;        // [stage]: the tile needs its column
+  static constexpr int kOffBar = kOffPartial + 32;
+  static_assert(kStages * 4 <= 32, "flags");
   static constexpr int kBarFixFull = 0;
   static constexpr int kBarStepFull = 1;
   static constexpr int kBarStepEmpty = kBarStepFull + kStages;
   static constexpr int kBarStepReady = kBarStepEmpty + kStages;  // A: keys that do not take part are out
-  static constexpr int kBarSFull = kBarStepReady + kStages;
-  static constexpr int kBarSFree = kBarSFull + 1;
-  static constexpr int kBarGFull = kBarSFree + 1;  // P / dS written to Tensor Memory
-  static constexpr int kBarGDone = kBarGFull + 1;  // the accumulating MMAs of a step are done
-  static constexpr int kBarDrain = kBarGDone + 1;
-  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kBarSFull = kBarStepReady + kStages;  // [warpgroup], and so on
+  static constexpr int kBarSFree = kBarSFull + 2;
+  static constexpr int kBarGFull = kBarSFree + 2;  // P / dS written to Tensor Memory
+  static constexpr int kBarGDone = kBarGFull + 2;  // the accumulating MMAs of a step are done
+  static constexpr int kBarDrain = kBarGDone + 2;
+  static constexpr int kNumBars = kBarDrain + 2;
   static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
   static constexpr int kOffAbort = kOffTmemSlot + 4;
   static constexpr int kBytes = kOffAbort + 4;
   static constexpr int kSmemAlloc = kBytes + 1024;
   static_assert(kSmemAlloc <= 232448, "shared memory budget");
-  // Tensor Memory columns.  The 128 columns of P^T / dS as bf16 are two halves
-  // of 32 words, one per warpgroup; over S and dP each half lies in the columns
-  // that its own warpgroup has read.
-  static constexpr uint32_t kColS = 0, kColDP = 128;
+  // Tensor Memory columns, per warpgroup g: S and dP of 64 columns each, P and
+  // dS as bf16 of 32 each (at D = 128 over S and dP); then the accumulators
+  static constexpr __host__ __device__ uint32_t col_s(int g) { return 128u * g; }
+  static constexpr __host__ __device__ uint32_t col_dp(int g) { return 128u * g + 64; }
+  static constexpr __host__ __device__ uint32_t col_p(int g) { return kAlias ? col_s(g) : 256u + 64 * g; }
+  static constexpr __host__ __device__ uint32_t col_ds(int g) { return kAlias ? col_dp(g) : 288u + 64 * g; }
   static constexpr uint32_t kColAcc0 = kAlias ? 256 : 384, kColAcc1 = kColAcc0 + D;
   static_assert(kColAcc1 + D <= 512, "Tensor Memory budget");
-  static constexpr __host__ __device__ uint32_t col_p(int half) { return kAlias ? kColS + half * 64 : 256u + half * 32; }
-  static constexpr __host__ __device__ uint32_t col_ds(int half) { return kAlias ? kColDP + half * 64 : 320u + half * 32; }
 };
 
 // kB = false: kernel A (dq); kB = true: kernel B (dk, dv).
@@ -92,6 +98,7 @@ template <int D, bool kB>
 __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const __grid_constant__ CrossBwdParams p) {
   using L = CrossBwdLayout<D>;
   using T = typename L::T;
+  using S = typename L::S;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
@@ -106,10 +113,10 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
   const int h = bh % heads, b = bh / heads;  // A: query head; B: key head
   const int row0 = tile * kXTile;
   const int keys = cross_keys(p.k_len, b, p.Nk);
-  const int q_tiles = (p.Nq + kXTile - 1) / kXTile;
+  const int q_tiles = (p.Nq + kXStep - 1) / kXStep;
   // B: a key tile with no key that counts has no steps (its gradients are 0)
-  const int nsteps = kB ? (row0 < keys ? p.group * q_tiles : 0) : (keys + kXTile - 1) / kXTile;
-  const bool fix = !kB && (p.mask != nullptr || p.k_len != nullptr || p.Nk % kXTile != 0);
+  const int nsteps = kB ? (row0 < keys ? p.group * q_tiles : 0) : (keys + kXStep - 1) / kXStep;
+  const bool fix = !kB && (p.mask != nullptr || p.k_len != nullptr || p.Nk % kXStep != 0);
   volatile int *partial = reinterpret_cast<volatile int *>(smem + L::kOffPartial);
 
   if (threadIdx.x == 0) {
@@ -119,16 +126,19 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
       mbar_init(&bars[L::kBarStepEmpty + s], 1);  // the commit after the step's last MMAs
       mbar_init(&bars[L::kBarStepReady + s], 32);
     }
-    mbar_init(&bars[L::kBarSFull], 1);
-    mbar_init(&bars[L::kBarSFree], 2 * kXTile);
-    mbar_init(&bars[L::kBarGFull], 2 * kXTile);
-    mbar_init(&bars[L::kBarGDone], 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&bars[L::kBarSFull + g], 1);
+      mbar_init(&bars[L::kBarSFree + g], kXTile);
+      mbar_init(&bars[L::kBarGFull + g], kXTile);
+      mbar_init(&bars[L::kBarGDone + g], 1);
+    }
     mbar_init(&bars[L::kBarDrain], 1);
+    mbar_init(&bars[L::kBarDrain + 1], 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
   if (!kB) {  // zeros but for the ones
-    for (int i = threadIdx.x; i < (1 + L::kStages) * XMaskTile::kBytes / 16; i += kXThreads)
+    for (int i = threadIdx.x; i < (L::kOffPartial - L::kOffOnes) / 16; i += kXThreads)
       reinterpret_cast<uint4 *>(smem + L::kOffOnes)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     if (threadIdx.x < kXTile) *XMaskTile::at(smem + L::kOffOnes, threadIdx.x) = 0x3F80u;
@@ -155,20 +165,20 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
         const uint64_t pol = l2_policy_evict_last();
         // fixed tiles of the unit: A: Q, dO rows; B: K, V rows
         mbar_arrive_expect_tx(&bars[L::kBarFixFull], 2 * T::kBytes);
-        T::load(smem + L::kOffFix0, kB ? &p.tm_k : &p.tm_q, &bars[L::kBarFixFull], row0, h, b, pol);
-        T::load(smem + L::kOffFix1, kB ? &p.tm_v : &p.tm_do, &bars[L::kBarFixFull], row0, h, b, pol);
+        T::load(smem + L::kOffFix0, &p.tm_fix0, &bars[L::kBarFixFull], row0, h, b, pol);
+        T::load(smem + L::kOffFix1, &p.tm_fix1, &bars[L::kBarFixFull], row0, h, b, pol);
         bool ok = true;
         int it = 0;
         for (; it < nsteps && ok; ++it) {
           const int s = it % L::kStages;
           if (it >= L::kStages) ok = mbar_wait(&bars[L::kBarStepEmpty + s], ((it / L::kStages) - 1) & 1, wc);
           if (!ok) break;
-          const int o0 = (kB ? it % q_tiles : it) * kXTile;
+          const int o0 = (kB ? it % q_tiles : it) * kXStep;
           const int oh = kB ? h * p.group + it / q_tiles : h / p.group;
           uint64_t *full = &bars[L::kBarStepFull + s];
-          mbar_arrive_expect_tx(full, 2 * T::kBytes);
-          T::load(smem + L::kOffStep0 + s * T::kBytes, kB ? &p.tm_q : &p.tm_k, full, o0, oh, b, pol);
-          T::load(smem + L::kOffStep1 + s * T::kBytes, kB ? &p.tm_do : &p.tm_v, full, o0, oh, b, pol);
+          mbar_arrive_expect_tx(full, 2 * S::kBytes);
+          S::load(smem + L::kOffStep0 + s * S::kBytes, &p.tm_step0, full, o0, oh, b, pol);
+          S::load(smem + L::kOffStep1 + s * S::kBytes, &p.tm_step1, full, o0, oh, b, pol);
         }
         // every copy issued lands before the CTA exits
         mbar_wait(&bars[L::kBarFixFull], 0, wc_drain);
@@ -178,95 +188,100 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
             if (a > 0) mbar_wait(&bars[L::kBarStepFull + s], (a - 1) & 1, wc_drain);
           }
       }
-    } else if (warp == kXWarpMma) {
-      // ================================================================ MMA issuer
-      // The whole warp walks through the loop and one lane issues: the operand
+    } else if (warp == kXWarpMma || warp == kXWarpMma1) {
+      // ================================================================ MMA issuers
+      // One warp for the scores, one for the products over them: neither's
+      // waits hold up the other, and the accumulators see one order.  The whole
+      // warp walks through the loop and one lane issues: the operand
       // descriptors then stay in uniform registers.
-      if (nsteps > 0) {
-        constexpr uint32_t idesc_s = idesc_bf16_f32(kXTile, kXTile, false);  // both operands K-major
-        constexpr uint32_t idesc_g = idesc_bf16_f32(kXTile, D, true);        // B MN-major
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint32_t smem0 = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kXTile, kXStep, false);  // both operands K-major
+      constexpr uint32_t idesc_g = idesc_bf16_f32(kXTile, D, true);        // B MN-major
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t smem0 = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+      auto wait = [&](int bar, int parity) -> bool { return warp_wait(&bars[bar], parity, wc); };
+      bool ok = nsteps > 0;
+      if (warp == kXWarpMma) {
+        // S, dP (A: Q K^T, dO V^T; B: K Q^T, V dO^T) once the tiles have landed
+        // and the warpgroup has read those of its last step (at D = 128: and
+        // the products over them are done)
         const uint32_t a0 = smem_desc_lo(smem0 + L::kOffFix0, 16), a1 = smem_desc_lo(smem0 + L::kOffFix1, 16);
-        // a warp's waits end as one
-        auto wait = [&](int bar, int parity) -> bool {
-          return __all_sync(0xffffffffu, mbar_wait<false>(&bars[bar], parity & 1, wc));
-        };
-        // S, dP of step `it` (A: Q K^T, dO V^T; B: K Q^T, V dO^T) once its
-        // tiles have landed and the previous step's S and dP have been read
-        // (at D = 128: and the products over them are done)
-        auto issue_s = [&](int it) -> bool {
-          const int s = it % L::kStages;
-          if (!wait(fix ? L::kBarStepReady + s : L::kBarStepFull + s, it / L::kStages)) return false;
-          if (it > 0 && !wait(L::kAlias ? L::kBarGDone : L::kBarSFree, it - 1)) return false;
+        const uint32_t ones_lo = smem_desc_lo(smem0 + L::kOffOnes, 16);
+        if (ok) ok = wait(L::kBarFixFull, 0);
+        for (int it = 0; it < nsteps && ok; ++it) {
+          const int s = it % L::kStages, g = it & 1, n = it >> 1;
+          const int full = (fix ? L::kBarStepReady : L::kBarStepFull) + s;
+          const int read = (L::kAlias ? L::kBarGDone : L::kBarSFree) + g;
+          ok = n > 0 ? warp_wait2(&bars[full], it / L::kStages, &bars[read], n - 1, wc) : wait(full, it / L::kStages);
+          if (!ok) break;
           tc_fence_after_sync();
-          const uint32_t b0 = smem_desc_lo(smem0 + L::kOffStep0 + s * T::kBytes, 16);
-          const uint32_t b1 = smem_desc_lo(smem0 + L::kOffStep1 + s * T::kBytes, 16);
-          const uint32_t ones_lo = smem_desc_lo(smem0 + L::kOffOnes, 16);
-          const uint32_t mask_lo = smem_desc_lo(smem0 + L::kOffMask + s * XMaskTile::kBytes, 16);
+          const uint32_t b0 = smem_desc_lo(smem0 + L::kOffStep0 + s * S::kBytes, 16);
+          const uint32_t b1 = smem_desc_lo(smem0 + L::kOffStep1 + s * S::kBytes, 16);
+          const uint32_t mask_lo = smem_desc_lo(smem0 + L::kOffMask + s * L::kMaskBytes, 16);
+          const uint32_t ts = tm + L::col_s(g), tdp = tm + L::col_dp(g);
           const bool masked = fix && partial[s] != 0;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16_ss(tm + L::kColS, desc_join(a0 + T::k_step(kk), T::kDescHi),
-                          desc_join(b0 + T::k_step(kk), T::kDescHi), idesc_s, kk > 0);
+              mma_bf16_ss(ts, desc_join(a0 + T::k_step(kk), T::kDescHi), desc_join(b0 + S::k_step(kk), S::kDescHi),
+                          idesc_s, kk > 0);
             if (masked)
-              mma_bf16_ss(tm + L::kColS, desc_join(ones_lo, XMaskTile::kDescHi),
-                          desc_join(mask_lo, XMaskTile::kDescHi), idesc_s, 1u);
+              mma_bf16_ss(ts, desc_join(ones_lo, XMaskTile::kDescHi), desc_join(mask_lo, XMaskTile::kDescHi), idesc_s,
+                          1u);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16_ss(tm + L::kColDP, desc_join(a1 + T::k_step(kk), T::kDescHi),
-                          desc_join(b1 + T::k_step(kk), T::kDescHi), idesc_s, kk > 0);
-            tc_commit(&bars[L::kBarSFull]);
+              mma_bf16_ss(tdp, desc_join(a1 + T::k_step(kk), T::kDescHi), desc_join(b1 + S::k_step(kk), S::kDescHi),
+                          idesc_s, kk > 0);
+            tc_commit(&bars[L::kBarSFull + g]);
           }
           __syncwarp();
-          return true;
-        };
-        // acc += G X with G (bf16, in Tensor Memory) and X an MN-major tile; by one lane
-        auto issue_g = [&](uint32_t acc, bool ds, uint32_t x_lo, bool more) {
+        }
+      } else {
+        // acc += G X with G (bf16, in Tensor Memory) and X an MN-major tile
+        auto issue_g = [&](uint32_t acc, uint32_t gcol, uint32_t x_lo, bool more) {
 #pragma unroll
-          for (int kk = 0; kk < kXTile / 16; ++kk)
-            mma_bf16_ts(tm + acc, tm + (ds ? L::col_ds(kk >> 2) : L::col_p(kk >> 2)) + (kk & 3) * 8,
-                        desc_join(x_lo + T::mn_step(kk), T::kDescHi), idesc_g, (more || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kXStep / 16; ++kk)
+            mma_bf16_ts(acc, gcol + kk * 8, desc_join(x_lo + S::mn_step(kk), S::kDescHi), idesc_g,
+                        (more || kk > 0) ? 1u : 0u);
         };
-        bool ok = wait(L::kBarFixFull, 0) && issue_s(0);
         for (int it = 0; it < nsteps && ok; ++it) {
-          const int s = it % L::kStages;
-          if (!L::kAlias && it + 1 < nsteps && !(ok = issue_s(it + 1))) break;
-          ok = wait(L::kBarGFull, it);
-          if (!ok) break;
+          const int s = it % L::kStages, g = it & 1, n = it >> 1;
+          // the step's tiles are there: its scores came from them
+          if (!(ok = wait(L::kBarGFull + g, n))) break;
           tc_fence_after_sync();
-          const uint32_t x0 = smem_desc_lo(smem0 + L::kOffStep0 + s * T::kBytes, T::kSlabBytes);
-          const uint32_t x1 = smem_desc_lo(smem0 + L::kOffStep1 + s * T::kBytes, T::kSlabBytes);
+          const uint32_t x0 = smem_desc_lo(smem0 + L::kOffStep0 + s * S::kBytes, S::kSlabBytes);
+          const uint32_t x1 = smem_desc_lo(smem0 + L::kOffStep1 + s * S::kBytes, S::kSlabBytes);
+          const uint32_t tp = tm + L::col_p(g), tds = tm + L::col_ds(g);
           if (elect_one()) {
-            if (kB) issue_g(L::kColAcc1, false, x1, it > 0);  // dV += P^T dO
-            issue_g(L::kColAcc0, true, x0, it > 0);           // A: dQ += dS K; B: dK += dS^T Q
-            tc_commit(&bars[L::kBarGDone]);
+            if (kB) issue_g(tm + L::kColAcc1, tp, x1, it > 0);  // dV += P^T dO
+            issue_g(tm + L::kColAcc0, tds, x0, it > 0);         // A: dQ += dS K; B: dK += dS^T Q
+            tc_commit(&bars[L::kBarGDone + g]);
             tc_commit(&bars[L::kBarStepEmpty + s]);
           }
           __syncwarp();
-          if (L::kAlias && it + 1 < nsteps && !(ok = issue_s(it + 1))) break;
         }
-        if (elect_one()) tc_commit(&bars[L::kBarDrain]);
-        __syncwarp();
-        mbar_wait<false>(&bars[L::kBarDrain], 0, wc_drain);
       }
+      // every MMA issued above completes before Tensor Memory is released; the
+      // second issuer's end is also the sums'
+      const int drain = L::kBarDrain + (warp == kXWarpMma1);
+      if (elect_one()) tc_commit(&bars[drain]);
+      __syncwarp();
+      mbar_wait<false>(&bars[drain], 0, wc_drain);
     } else if (warp == kXWarpFix && fix) {
       // ================================================================ A: keys that do not take part
       const uint8_t *mrow = p.mask != nullptr ? p.mask + int64_t(b) * p.mask_sb : nullptr;
       bool ok = true;
-      uint32_t next = nsteps > 0 ? cross_mask_bytes(mrow, p.mask_vec4, 0, keys, lane) : 0u;
+      uint32_t next = nsteps > 0 ? cross_mask_bytes<2>(mrow, false, 0, keys, lane) : 0u;
       for (int it = 0; it < nsteps && ok; ++it) {
         const int s = it % L::kStages;
-        const KeepWords keep = cross_keep(next);
-        if (it + 1 < nsteps) next = cross_mask_bytes(mrow, p.mask_vec4, (it + 1) * kXTile, keys, lane);
+        const KeepWords<2> keep = cross_keep<2>(next);
+        if (it + 1 < nsteps) next = cross_mask_bytes<2>(mrow, false, (it + 1) * kXStep, keys, lane);
         ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarStepFull + s], (it / L::kStages) & 1, wc));
         if (!ok) break;
         const bool any = !keep.all();
         if (any) {
-          cross_zero_rows<D>(smem + L::kOffStep0 + s * T::kBytes, keep, lane);
-          cross_zero_rows<D>(smem + L::kOffStep1 + s * T::kBytes, keep, lane);
-          cross_mask_column(smem + L::kOffMask + s * XMaskTile::kBytes, keep, lane);
+          cross_zero_rows<D>(smem + L::kOffStep0 + s * S::kBytes, keep, lane);
+          cross_zero_rows<D>(smem + L::kOffStep1 + s * S::kBytes, keep, lane);
+          cross_mask_column(smem + L::kOffMask + s * L::kMaskBytes, keep, lane);
           fence_proxy_async_smem();
         }
         if (lane == 0) partial[s] = any;
@@ -277,10 +292,11 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
   } else {
     // ================================================================ compute warpgroups
     setmaxnreg_inc<kXRegsSoftmax>();
-    const int g = warp >> 2;           // column half of each step
+    const int g = warp >> 2;           // takes the steps g, g + 2, ...
     const int t = threadIdx.x & 127;   // row of the unit's tile = Tensor Memory lane
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const int r = row0 + t;            // A: query row; B: key row
+    const uint32_t tS = tmem + lane_base + L::col_s(g), tDP = tmem + lane_base + L::col_dp(g);
     const float c_s = p.tau * kXLog2e;
     float lse2 = 0.f, delta = 0.f;     // A: this row's
     bool key_ok = true;                // B: this row's key takes part
@@ -305,7 +321,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
         const int qh = h * p.group + step / q_tiles;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int qi = (step % q_tiles) * kXTile + g * 64 + lane + 32 * e;
+          const int qi = (step % q_tiles) * kXStep + lane + 32 * e;
           if (qi < p.Nq) {
             nlse[e] = p.lse[b * p.lse_sb + qh * p.lse_sh + int64_t(qi) * p.lse_sn];
             ndelta[e] = p.delta[(int64_t(b) * p.H + qh) * p.Nq + qi];
@@ -313,38 +329,39 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
         }
       }
     };
-    if (nsteps > 0) load_cols(0);
+    if (g < nsteps) load_cols(g);
     bool ok = true;
-    for (int it = 0; it < nsteps && ok; ++it) {
+    int n = 0;  // steps of this warpgroup so far
+    for (int it = g; it < nsteps && ok; it += 2, ++n) {
       const float clse[2] = {nlse[0], nlse[1]}, cdelta[2] = {ndelta[0], ndelta[1]};
-      if (it + 1 < nsteps) load_cols(it + 1);
-      float *rv = reinterpret_cast<float *>(smem + L::kOffRowv) + ((it & 1) * 8 + warp) * L::kRowvFloats;
+      if (it + 2 < nsteps) load_cols(it + 2);
+      float *rv = reinterpret_cast<float *>(smem + L::kOffRowv) + ((n & 1) * 8 + warp) * L::kRowvFloats;
       if (kB) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int col = lane + 32 * e;
-          const int qi = (it % q_tiles) * kXTile + g * 64 + col;
+          const int qi = (it % q_tiles) * kXStep + col;
           rv[col] = qi >= p.Nq ? -INFINITY : (clse[e] == -INFINITY ? 0.f : -clse[e] * kXLog2e);
           rv[64 + col] = qi < p.Nq ? -cdelta[e] : 0.f;
         }
         __syncwarp();
       }
-      ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarSFull], it & 1, wc));
+      ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarSFull + g], n & 1, wc));
       if (!ok) break;
       tc_fence_after_sync();
       const float2 cs2 = make_float2(c_s, c_s);
       const float2 rowl2 = make_float2(-lse2, -lse2), rowd2 = make_float2(-delta, -delta);
       uint32_t sv[64], dpv[64];
-      tmem_ld32(tmem + lane_base + L::kColS + g * 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-      tmem_ld32(tmem + lane_base + L::kColS + g * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-      tmem_ld32(tmem + lane_base + L::kColDP + g * 64, *reinterpret_cast<uint32_t(*)[32]>(&dpv[0]));
-      tmem_ld32(tmem + lane_base + L::kColDP + g * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&dpv[32]));
+      tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+      tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+      tmem_ld32(tDP, *reinterpret_cast<uint32_t(*)[32]>(&dpv[0]));
+      tmem_ld32(tDP + 32, *reinterpret_cast<uint32_t(*)[32]>(&dpv[32]));
       tmem_wait_ld();
       reg_fence(sv);
       reg_fence(dpv);
-      // the next step's S and dP may overwrite these columns
+      // the warpgroup's next S and dP may overwrite these columns
       tc_fence_before_sync();
-      if (!L::kAlias) mbar_arrive(&bars[L::kBarSFree]);
+      if (!L::kAlias) mbar_arrive(&bars[L::kBarSFree + g]);
       // two quarters of 32 columns, each stored to Tensor Memory before the next is formed
 #pragma unroll
       for (int qt = 0; qt < 2; ++qt) {
@@ -369,9 +386,9 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
             dk[j4 * 2 + e] = pack_bf16x2(ds.x, ds.y);
           }
         }
-        if (!L::kAlias && qt == 0 && it > 0) {
-          // the previous step's accumulating MMAs read what the stores below overwrite
-          ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarGDone], (it - 1) & 1, wc));
+        if (!L::kAlias && qt == 0 && n > 0) {
+          // the accumulating MMAs of its last step read what the stores below overwrite
+          ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarGDone + g], (n - 1) & 1, wc));
           if (!ok) break;
           tc_fence_after_sync();
         }
@@ -381,10 +398,11 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
       if (!ok) break;
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(&bars[L::kBarGFull]);
+      mbar_arrive(&bars[L::kBarGFull + g]);
     }
     // -------------------------------------------------------------- epilogue
-    if (ok && nsteps > 0) ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarGDone], (nsteps - 1) & 1, wc));
+    // all steps, the other warpgroup's too, are in the accumulators
+    if (ok && nsteps > 0) ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarDrain + 1], 0, wc));
     if (ok) {
       tc_fence_after_sync();
       const int nrows = kB ? p.Nk : p.Nq;

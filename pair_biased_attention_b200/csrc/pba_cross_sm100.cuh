@@ -55,9 +55,9 @@ constexpr int kXRegSplitTotal = 256 * kXRegsSoftmax + 128 * kXRegsOther;
 constexpr float kXLog2e = 1.4426950408889634f;
 constexpr float kXLn2 = 0.6931471805599453f;
 
-// Shared-memory tile of [128][D] bf16 as TMA and the tensor core see it: one
+// Shared-memory tile of [kRows][D] bf16 as TMA and the tensor core see it: one
 // or two slabs of at most 64 features (128 bytes) per row.
-template <int D>
+template <int D, int kRows = kXTile>
 struct XTileLayout {
   static_assert(D == 32 || D == 64 || D == 128, "head dimension");
   static constexpr int kSlabs = D == 128 ? 2 : 1;
@@ -65,7 +65,7 @@ struct XTileLayout {
   static constexpr int kRowBytes = kSlabCols * 2;
   static constexpr int kSwizzleMode = kRowBytes == 128 ? 2 : 4;  // 128- / 64-byte swizzle
   static constexpr int kAtomBytes = 8 * kRowBytes;
-  static constexpr int kSlabBytes = kXTile * kRowBytes;
+  static constexpr int kSlabBytes = kRows * kRowBytes;
   static constexpr int kBytes = kSlabs * kSlabBytes;
   static constexpr uint32_t kDescHi = smem_desc_hi(kAtomBytes, kSwizzleMode);
   // address step (16-byte units) of the K = 16 slice kk of a K-major operand
@@ -107,59 +107,83 @@ struct CrossParams {
   uint64_t timeout_ns;
 };
 
+// Waits of a whole warp, which end as one: the phases of one barrier, or of two
+// at once (both are asked before the first answer is used, which is what it
+// takes when both are usually there).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, int parity, const WaitCtl &wc) {
+  return __all_sync(0xffffffffu, mbar_wait<false>(bar, parity & 1, wc));
+}
+__device__ __forceinline__ bool warp_wait2(uint64_t *a, int pa, uint64_t *b, int pb, const WaitCtl &wc) {
+  const bool ra = mbar_try_wait(a, pa & 1), rb = mbar_try_wait(b, pb & 1);
+  if (__all_sync(0xffffffffu, ra && rb)) return true;
+  return warp_wait(a, pa, wc) && warp_wait(b, pb, wc);
+}
+
 // Keys of batch b that may take part: k_len, kept inside [0, Nk].
 __device__ __forceinline__ int cross_keys(const int32_t *k_len, int b, int Nk) {
   return k_len == nullptr ? Nk : min(max(__ldg(k_len + b), 0), Nk);
 }
 
-// Which of the 128 keys of the tile at key0 take part, asked by a whole warp:
-// bit l of word e is key 4 l + e.  `bytes` is what cross_mask_bytes read.
+// Which of the 32 kPer keys of the tile at key0 take part, asked by a whole
+// warp: bit l of word e is key kPer l + e.  `bytes` is what cross_mask_bytes read
+// (without a mask all keys before the end take part).
+template <int kPer>
 __device__ __forceinline__ uint32_t cross_mask_bytes(const uint8_t *row, bool vec4, int key0, int keys, int lane) {
-  const int k = key0 + 4 * lane;
-  if (row == nullptr) {  // no mask: all keys before the end
-    const int n = min(max(keys - k, 0), 4);
-    return n == 0 ? 0u : 0x01010101u >> (32 - 8 * n);
-  }
-  if (vec4 && k + 3 < keys) return __ldg(reinterpret_cast<const uint32_t *>(row + k));
+  const int k = key0 + kPer * lane;
   uint32_t v = 0;
+  if (row == nullptr) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < kPer; ++e) v |= uint32_t(k + e < keys) << (8 * e);
+    return v;
+  }
+  if (kPer == 4 && vec4 && k + 3 < keys) return __ldg(reinterpret_cast<const uint32_t *>(row + k));
+#pragma unroll
+  for (int e = 0; e < kPer; ++e)
     if (k + e < keys) v |= uint32_t(__ldg(row + k + e)) << (8 * e);
   return v;
 }
+template <int kPer>
 struct KeepWords {
-  uint32_t w[4];
-  __device__ __forceinline__ bool all() const { return (w[0] & w[1] & w[2] & w[3]) == 0xFFFFFFFFu; }
-};
-__device__ __forceinline__ KeepWords cross_keep(uint32_t bytes) {
-  KeepWords k;
+  uint32_t w[kPer];
+  __device__ __forceinline__ bool all() const {
+    uint32_t a = w[0];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) k.w[e] = __ballot_sync(0xffffffffu, ((bytes >> (8 * e)) & 0xFFu) != 0);
+    for (int e = 1; e < kPer; ++e) a &= w[e];
+    return a == 0xFFFFFFFFu;
+  }
+};
+template <int kPer>
+__device__ __forceinline__ KeepWords<kPer> cross_keep(uint32_t bytes) {
+  KeepWords<kPer> k;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) k.w[e] = __ballot_sync(0xffffffffu, ((bytes >> (8 * e)) & 0xFFu) != 0);
   return k;
 }
 
-// The column of ones beside Q and the columns of 0 and -inf beside K: [128][16]
+// The column of ones beside Q and the columns of 0 and -inf beside K: [rows][16]
 // bf16 tiles, K-major, 32-byte swizzle, of which only feature 0 is not 0.
 struct XMaskTile {
-  static constexpr int kBytes = kXTile * 32;
+  static constexpr int kRowBytes = 32;
   static constexpr uint32_t kDescHi = smem_desc_hi(256, 6);
   // feature 0 of row r: the 16-byte chunk's place in the row follows bit 2 of r
   static __device__ __forceinline__ uint16_t *at(uint8_t *tile, int r) {
-    return reinterpret_cast<uint16_t *>(tile + r * 32 + ((r >> 2) & 1) * 16);
+    return reinterpret_cast<uint16_t *>(tile + r * kRowBytes + ((r >> 2) & 1) * 16);
   }
 };
 // By one warp: zeroes the rows of `tile` (of D features) whose keys do not take
-// part, each lane its own four.
-template <int D>
-__device__ __forceinline__ void cross_zero_rows(uint8_t *tile, const KeepWords &keep, int lane) {
+// part, each lane its own.
+template <int D, int kPer>
+__device__ __forceinline__ void cross_zero_rows(uint8_t *tile, const KeepWords<kPer> &keep, int lane) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (!((keep.w[e] >> lane) & 1u)) XTileLayout<D>::zero_row(tile, 4 * lane + e);
+  for (int e = 0; e < kPer; ++e)
+    if (!((keep.w[e] >> lane) & 1u)) XTileLayout<D, 32 * kPer>::zero_row(tile, kPer * lane + e);
 }
 // By one warp: the column of a tile's keys.
-__device__ __forceinline__ void cross_mask_column(uint8_t *tile, const KeepWords &keep, int lane) {
+template <int kPer>
+__device__ __forceinline__ void cross_mask_column(uint8_t *tile, const KeepWords<kPer> &keep, int lane) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) *XMaskTile::at(tile, 4 * lane + e) = (keep.w[e] >> lane) & 1u ? 0x0000u : 0xFF80u;
+  for (int e = 0; e < kPer; ++e)
+    *XMaskTile::at(tile, kPer * lane + e) = (keep.w[e] >> lane) & 1u ? 0x0000u : 0xFF80u;
 }
 
 template <int D>
@@ -171,8 +195,9 @@ struct CrossLayout {
   static constexpr int kOffK = kOffQ + kXQTiles * T::kBytes;
   static constexpr int kOffV = kOffK + kKVStages * T::kBytes;
   static constexpr int kOffOnes = kOffV + kKVStages * T::kBytes;
-  static constexpr int kOffMask = kOffOnes + XMaskTile::kBytes;                // [K stage]
-  static constexpr int kOffPartial = kOffMask + kKVStages * XMaskTile::kBytes;  // [K stage]: the tile needs its column
+  static constexpr int kMaskBytes = kXTile * XMaskTile::kRowBytes;
+  static constexpr int kOffMask = kOffOnes + kMaskBytes;                // [K stage]
+  static constexpr int kOffPartial = kOffMask + kKVStages * kMaskBytes;  // [K stage]: the tile needs its column
   static constexpr int kOffBar = kOffPartial + 16;
   static_assert(kKVStages * 4 <= 16, "flags");
   static constexpr int kBarQFull = 0;
@@ -256,7 +281,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
     fence_barrier_init();
   }
   // zeros but for the ones
-  for (int i = threadIdx.x; i < (1 + L::kKVStages) * XMaskTile::kBytes / 16; i += kXThreads)
+  for (int i = threadIdx.x; i < (1 + L::kKVStages) * L::kMaskBytes / 16; i += kXThreads)
     reinterpret_cast<uint4 *>(smem + L::kOffOnes)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   if (threadIdx.x < kXTile) *XMaskTile::at(smem + L::kOffOnes, threadIdx.x) = 0x3F80u;
@@ -353,14 +378,12 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
       bool ok = true;
       int kc = 0, vc = 0;  // K and V tiles consumed (= score and P V tiles issued)
       int uc = 0;
-      // a warp's waits end as one
-      auto wait = [&](int bar, int parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait<false>(&bars[bar], parity & 1, wc));
-      };
+      auto wait = [&](int bar, int parity) -> bool { return warp_wait(&bars[bar], parity, wc); };
+      auto wait2 = [&](int a, int pa, int b, int pb) -> bool { return warp_wait2(&bars[a], pa, &bars[b], pb, wc); };
       auto issue_s = [&](int s) {
         const uint32_t k_lo = smem_desc_lo(smem0 + L::kOffK + s * T::kBytes, 16);
         const uint32_t ones_lo = smem_desc_lo(smem0 + L::kOffOnes, 16);
-        const uint32_t mask_lo = smem_desc_lo(smem0 + L::kOffMask + s * XMaskTile::kBytes, 16);
+        const uint32_t mask_lo = smem_desc_lo(smem0 + L::kOffMask + s * L::kMaskBytes, 16);
         const bool masked = fix && partial[s] != 0;
         if (elect_one()) {
 #pragma unroll
@@ -390,8 +413,9 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
       // over it) has been read
       auto next_s = [&]() -> bool {
         const int s = kc % L::kKVStages;
-        if (!wait((fix ? L::kBarKReady : L::kBarKFull) + s, kc / L::kKVStages)) return false;
-        if (kc > 0 && !wait(L::kBarSFree + w, kc - 1)) return false;
+        const int full = (fix ? L::kBarKReady : L::kBarKFull) + s;
+        if (kc > 0 ? !wait2(full, kc / L::kKVStages, L::kBarSFree + w, kc - 1) : !wait(full, kc / L::kKVStages))
+          return false;
         if (L::kAlias && vc > 0 && !wait(L::kBarODone + w, vc - 1)) return false;
         tc_fence_after_sync();
         issue_s(s);
@@ -418,8 +442,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
             // after the unit's last score MMAs the Q slot can be refilled
             if (j + 2 == nt) q_done();
           }
-          if (!(ok = wait(fix ? L::kBarVReady + sv : L::kBarVFull + sv, vc / L::kKVStages))) break;
-          if (!(ok = wait(L::kBarPFull + w, vc))) break;
+          if (!(ok = wait2((fix ? L::kBarVReady : L::kBarVFull) + sv, vc / L::kKVStages, L::kBarPFull + w, vc))) break;
           // the first P V of a unit overwrites O: the epilogue of the
           // previous unit must have read it
           if (j == 0 && uc > 0 && !(ok = wait(L::kBarOFree + w, uc - 1))) break;
@@ -441,16 +464,14 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
       // ============================================================== keys that do not take part
       bool ok = true;
       int kc = 0, vc = 0;
-      auto wait = [&](int bar, int parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait<false>(&bars[bar], parity & 1, wc));
-      };
-      auto fix_k = [&](const KeepWords &keep) -> bool {
+      auto wait = [&](int bar, int parity) -> bool { return warp_wait(&bars[bar], parity, wc); };
+      auto fix_k = [&](const KeepWords<4> &keep) -> bool {
         const int s = kc % L::kKVStages;
         if (!wait(L::kBarKFull + s, kc / L::kKVStages)) return false;
         const bool any = !keep.all();
         if (any) {
           cross_zero_rows<D>(smem + L::kOffK + s * T::kBytes, keep, lane);
-          cross_mask_column(smem + L::kOffMask + s * XMaskTile::kBytes, keep, lane);
+          cross_mask_column(smem + L::kOffMask + s * L::kMaskBytes, keep, lane);
           fence_proxy_async_smem();
         }
         if (lane == 0) partial[s] = any;
@@ -459,7 +480,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
         ++kc;
         return true;
       };
-      auto fix_v = [&](const KeepWords &keep) -> bool {
+      auto fix_v = [&](const KeepWords<4> &keep) -> bool {
         const int s = vc % L::kKVStages;
         if (!wait(L::kBarVFull + s, vc / L::kKVStages)) return false;
         if (!keep.all()) {
@@ -475,14 +496,14 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
         const CrossUnit un = cross_unit(p, u);
         if (un.nt == 0) continue;
         const uint8_t *mrow = p.mask != nullptr ? p.mask + int64_t(un.b) * p.mask_sb : nullptr;
-        auto bytes = [&](int j) { return cross_mask_bytes(mrow, p.mask_vec4, j * kXTile, un.keys, lane); };
-        KeepWords keep = cross_keep(bytes(0));
+        auto bytes = [&](int j) { return cross_mask_bytes<4>(mrow, p.mask_vec4, j * kXTile, un.keys, lane); };
+        KeepWords<4> keep = cross_keep<4>(bytes(0));
         uint32_t next = un.nt > 1 ? bytes(1) : 0u;
         ok = fix_k(keep);
         for (int j = 0; j < un.nt && ok; ++j) {
-          const KeepWords v_keep = keep;
+          const KeepWords<4> v_keep = keep;
           if (j + 1 < un.nt) {
-            keep = cross_keep(next);
+            keep = cross_keep<4>(next);
             if (j + 2 < un.nt) next = bytes(j + 2);
             ok = fix_k(keep);
           }
