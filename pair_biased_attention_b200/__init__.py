@@ -621,50 +621,55 @@ def pba_relpos_bias_backward(dbias, q_pos, k_pos, rows, rule="clip", max_distanc
 _NORM_KINDS = {"layer": PBA_NORM_LAYER, "rms": PBA_NORM_RMS}
 
 
-def _row_stride(name, t, shape, dtype):
-    """Row stride of t [..., C] read as rows of C channels (0 for None)."""
-    if t is None:
-        return 0
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor")
-    if t.is_contiguous():
-        return shape[-1]
-    stride, rows = None, 1
+def _row_strides(ref, tensors, names):
+    """Row strides of the tensors [..., C] of ref's shape and dtype, read as rows
+    of C channels (0 for None)."""
+    strides, C, dtype = [], ref.shape[-1], ref.dtype
+    for i, t in enumerate(tensors):
+        if t is None:
+            strides.append(0)
+        elif t.dtype == dtype and t.is_same_size(ref):
+            strides.append(C if t.is_contiguous() else _row_stride(names.split()[i], t))
+        else:
+            raise ValueError(f"{names.split()[i]} must be a {tuple(ref.shape)} {dtype} tensor")
+    return strides
+
+
+def _row_stride(name, t):
+    shape, stride, rows = t.shape, None, 1
     if t.stride(-1) == 1 or shape[-1] == 1:
         for i in range(t.dim() - 2, -1, -1):
-            if t.shape[i] == 1:
+            if shape[i] == 1:
                 continue
             if stride is None:
                 stride = t.stride(i)
             elif t.stride(i) != stride * rows:
                 break
-            rows *= t.shape[i]
+            rows *= shape[i]
         else:
             return shape[-1] if stride is None else stride
     raise ValueError(f"{name} must be rows of contiguous channels a fixed stride apart")
 
 
-def _norm_desc(ref, kind, eps, post, pre, scale):
-    """The descriptor without its strides, and (post_w, post_b, pre_w, pre_b)."""
+def _norm_params(ref, kind, post, pre, scale):
+    """The kind's code, the parameters' dtype and (post_w, post_b, pre_w, pre_b)."""
     code = _NORM_KINDS.get(kind)
     if code is None:
         raise ValueError(f"kind must be one of {sorted(_NORM_KINDS)}")
     if ref.dim() < 1:
         raise ValueError("x must have a channel axis")
-    C = ref.shape[-1]
     post_w, post_b = (None, None) if post is None else post
     pre_w, pre_b = (None, None) if pre is None else pre
     if (post is not None and post_w is None) or (pre is not None and pre_w is None):
         raise ValueError("a norm needs its weight")
-    dtype = None
+    C, dtype = ref.shape[-1], None
     for t in (scale, post_w, post_b, pre_w, pre_b):
         if t is not None:
-            dtype = dtype or t.dtype
-            if t.dim() != 1 or t.shape[0] != C or t.dtype != dtype or not t.is_contiguous():
+            if dtype is None:
+                dtype = t.dtype
+            if t.dim() != 1 or t.numel() != C or t.dtype != dtype or not t.is_contiguous():
                 raise ValueError(f"scale, weights and biases must be contiguous [{C}] tensors of one dtype")
-    d = PbaNormDesc(ref.numel() // C if C else 0, C, _dtype_code(ref.dtype), _dtype_code(dtype or ref.dtype), code,
-                    eps)
-    return d, (post_w, post_b, pre_w, pre_b)
+    return code, _dtype_code(dtype or ref.dtype), (post_w, post_b, pre_w, pre_b)
 
 
 def pba_block_norm_forward(x, f=None, gate=None, scale=None, post=None, pre=None, kind="layer", eps=1e-5, h=None, y=None,
@@ -676,22 +681,20 @@ def pba_block_norm_forward(x, f=None, gate=None, scale=None, post=None, pre=None
     (weight, bias or None) pairs of [C] tensors or None (no norm there); scale
     [C] or None; the parameters are all bf16 or all fp32.  kind "layer" or
     "rms".  ``h`` may be x itself.  Returns h and y (None without pre)."""
-    d, params = _norm_desc(x, kind, eps, post, pre, scale)
+    code, param_code, params = _norm_params(x, kind, post, pre, scale)
     _here((x, f, gate, scale, *params, h, y), "x f gate scale post_w post_b pre_w pre_b h y")
     with _alloc_on(stream):
         if h is None and f is not None:
             h = _empty_as(x)
         if y is None and pre is not None:
             y = _empty_as(x)
-    shape, dtype = x.shape, x.dtype
-    d.x_stride = _row_stride("x", x, shape, dtype)
-    d.f_stride = _row_stride("f", f, shape, dtype)
-    d.gate_stride = _row_stride("gate", gate, shape, dtype)
-    d.h_stride = _row_stride("h", h, shape, dtype)
-    d.y_stride = _row_stride("y", y, shape, dtype)
-    _check("pba_block_norm_forward", load_library().pba_block_norm_forward(
-        ctypes.byref(d), _ptr(x), _ptr(f), _ptr(gate), _ptr(scale), *map(_ptr, params), _ptr(h), _ptr(y),
-        _stream(stream)))
+    C = x.shape[-1]
+    d = PbaNormDesc(x.numel() // C if C else 0, C, _dtype_code(x.dtype), param_code, code, eps,
+                    *_row_strides(x, (x, f, gate, h, y), "x f gate h y"))
+    status = load_library().pba_block_norm_forward(
+        ctypes.byref(d), _ptr(x), _ptr(f), _ptr(gate), _ptr(scale), *[_ptr(t) for t in params], _ptr(h), _ptr(y),
+        _stream(stream))
+    _check("pba_block_norm_forward", status)
     return (x if f is None else h), (y if pre is not None else None)
 
 
@@ -702,25 +705,27 @@ def pba_block_norm_backward(h, dh, dy, f=None, gate=None, scale=None, post=None,
     Returns dx, df, dgate (the inputs' dtype) and dscale, dpost_w, dpost_b,
     dpre_w, dpre_b ([C], fp32); None for what was not given."""
     ref = h if h is not None else dh
-    d, params = _norm_desc(ref, kind, eps, post, pre, scale)
+    code, param_code, params = _norm_params(ref, kind, post, pre, scale)
     _here((h, dh, dy, f, gate, scale, *params), "h dh dy f gate scale post_w post_b pre_w pre_b")
-    shape, dtype, C = ref.shape, ref.dtype, ref.shape[-1]
-    d.h_stride = _row_stride("h", h, shape, dtype)
-    d.f_stride = _row_stride("f", f, shape, dtype)
-    d.gate_stride = _row_stride("gate", gate, shape, dtype)
-    d.dh_stride = _row_stride("dh", dh, shape, dtype)
-    d.dy_stride = _row_stride("dy", dy, shape, dtype)
-    d.dx_stride = d.df_stride = d.dgate_stride = C
+    C = ref.shape[-1]
+    h_s, f_s, gate_s, dh_s, dy_s = _row_strides(ref, (h, f, gate, dh, dy), "h f gate dh dy")
+    d = PbaNormDesc(ref.numel() // C if C else 0, C, _dtype_code(ref.dtype), param_code, code, eps, 0, f_s, gate_s,
+                    h_s, 0, dh_s, dy_s, C, C, C)
     lib = load_library()
     need = ctypes.c_int64()
-    _check("pba_block_norm_backward_workspace", lib.pba_block_norm_backward_workspace(ctypes.byref(d), ctypes.byref(need)))
+    _check("pba_block_norm_backward_workspace",
+           lib.pba_block_norm_backward_workspace(ctypes.byref(d), ctypes.byref(need)))
+    wanted = [t is not None for t in (scale, *params)]
     with _alloc_on(stream):
         dx, df, dgate = (None if t is None else _empty_as(ref) for t in (ref, f, gate))
-        sums = [None if t is None else _empty_as(t, torch.float32) for t in (scale, *params)]
+        # the parameters' gradients are rows of one tensor
+        rows = iter(ref.new_empty((sum(wanted), C), dtype=torch.float32).unbind())
         work = ref.new_empty(need.value, dtype=torch.uint8)
-    _check("pba_block_norm_backward", lib.pba_block_norm_backward(
-        ctypes.byref(d), _ptr(h), _ptr(f), _ptr(gate), _ptr(scale), *map(_ptr, params), _ptr(dh), _ptr(dy), _ptr(dx),
-        _ptr(df), _ptr(dgate), *map(_ptr, sums), _ptr(work), need.value, _stream(stream)))
+    sums = [next(rows) if w else None for w in wanted]
+    status = lib.pba_block_norm_backward(
+        ctypes.byref(d), _ptr(h), _ptr(f), _ptr(gate), _ptr(scale), *[_ptr(t) for t in params], _ptr(dh), _ptr(dy),
+        _ptr(dx), _ptr(df), _ptr(dgate), *[_ptr(t) for t in sums], _ptr(work), need.value, _stream(stream))
+    _check("pba_block_norm_backward", status)
     return (dx, df, dgate, *sums)
 
 

@@ -191,6 +191,13 @@ pba_status run_cross_bwd(const pba_cross_desc &d, const void *q, const void *k, 
                          void *dk, void *dv, float *delta, cudaStream_t stream) {
   pba::CrossBwdParams p;
   std::memset(&p, 0, sizeof(p));
+  // a side without rows is loaded by no unit
+  if (d.Nq > 0 && (!cross_map(&p.tm_q, q, D, d.Nq, d.H, d.B, d.q_stride, pba::kXStep) ||
+                   !cross_map(&p.tm_do, dout, D, d.Nq, d.H, d.B, d.dout_stride, pba::kXStep)))
+    return PBA_ERR_INVALID_ARG;
+  if (d.Nk > 0 && (!cross_map(&p.tm_k, k, D, d.Nk, d.Hkv, d.B, d.k_stride, pba::kXStep) ||
+                   !cross_map(&p.tm_v, v, D, d.Nk, d.Hkv, d.B, d.v_stride, pba::kXStep)))
+    return PBA_ERR_INVALID_ARG;
   p.B = int(d.B), p.H = int(d.H), p.Hkv = int(d.Hkv), p.group = int(d.H / d.Hkv), p.Nq = int(d.Nq), p.Nk = int(d.Nk);
   p.tau = cross_tau(&d);
   p.k_len = k_len;
@@ -218,23 +225,10 @@ pba_status run_cross_bwd(const pba_cross_desc &d, const void *q, const void *k, 
     pba::pba_cross_delta_kernel<D><<<unsigned(blocks), 256, 0, stream>>>(dp);
     if (cudaGetLastError() != cudaSuccess) return PBA_ERR_CUDA;
     p.n_tiles = int(q_tiles);
-    if (!cross_map(&p.tm_fix0, q, D, d.Nq, d.H, d.B, d.q_stride) ||
-        !cross_map(&p.tm_fix1, dout, D, d.Nq, d.H, d.B, d.dout_stride))
-      return PBA_ERR_INVALID_ARG;
-    // without a key no unit has a step
-    if (d.Nk > 0 && (!cross_map(&p.tm_step0, k, D, d.Nk, d.Hkv, d.B, d.k_stride, pba::kXStep) ||
-                     !cross_map(&p.tm_step1, v, D, d.Nk, d.Hkv, d.B, d.v_stride, pba::kXStep)))
-      return PBA_ERR_INVALID_ARG;
     if (launch_cross_bwd<D, false>(p, grid_a, stream) != cudaSuccess) return PBA_ERR_CUDA;
   }
   if (d.Nk > 0) {
     p.n_tiles = int(k_tiles);
-    if (!cross_map(&p.tm_fix0, k, D, d.Nk, d.Hkv, d.B, d.k_stride) ||
-        !cross_map(&p.tm_fix1, v, D, d.Nk, d.Hkv, d.B, d.v_stride))
-      return PBA_ERR_INVALID_ARG;
-    if (d.Nq > 0 && (!cross_map(&p.tm_step0, q, D, d.Nq, d.H, d.B, d.q_stride, pba::kXStep) ||
-                     !cross_map(&p.tm_step1, dout, D, d.Nq, d.H, d.B, d.dout_stride, pba::kXStep)))
-      return PBA_ERR_INVALID_ARG;
     if (launch_cross_bwd<D, true>(p, grid_b, stream) != cudaSuccess) return PBA_ERR_CUDA;
   }
   return PBA_OK;

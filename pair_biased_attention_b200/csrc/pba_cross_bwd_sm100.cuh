@@ -31,9 +31,7 @@ namespace pba {
 constexpr int kXStep = 64;  // keys (A) or queries (B) of a step
 
 struct CrossBwdParams {
-  // (D, n, heads, B) bf16.  The unit's own rows (A: Q, dO; B: K, V): box
-  // {min(D, 64), 128, 1, 1}; the steps' (A: K, V; B: Q, dO): 64 rows
-  CUtensorMap tm_fix0, tm_fix1, tm_step0, tm_step1;
+  CUtensorMap tm_q, tm_k, tm_v, tm_do;  // (D, n, heads, B) bf16, box {min(D, 64), 64, 1, 1}
   int32_t B, H, Hkv, group, Nq, Nk;
   int32_t n_tiles;      // A: ceil(Nq / 128) per (b, h); B: ceil(Nk / 128) per (b, hkv)
   float tau;
@@ -165,8 +163,12 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
         const uint64_t pol = l2_policy_evict_last();
         // fixed tiles of the unit: A: Q, dO rows; B: K, V rows
         mbar_arrive_expect_tx(&bars[L::kBarFixFull], 2 * T::kBytes);
-        T::load(smem + L::kOffFix0, &p.tm_fix0, &bars[L::kBarFixFull], row0, h, b, pol);
-        T::load(smem + L::kOffFix1, &p.tm_fix1, &bars[L::kBarFixFull], row0, h, b, pol);
+        const CUtensorMap *fix0 = kB ? &p.tm_k : &p.tm_q, *fix1 = kB ? &p.tm_v : &p.tm_do;
+        const CUtensorMap *step0 = kB ? &p.tm_q : &p.tm_k, *step1 = kB ? &p.tm_do : &p.tm_v;
+        for (int half = 0; half < 2; ++half) {
+          T::template load<kXStep>(smem + L::kOffFix0, half, fix0, &bars[L::kBarFixFull], row0, h, b, pol);
+          T::template load<kXStep>(smem + L::kOffFix1, half, fix1, &bars[L::kBarFixFull], row0, h, b, pol);
+        }
         bool ok = true;
         int it = 0;
         for (; it < nsteps && ok; ++it) {
@@ -177,8 +179,8 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
           const int oh = kB ? h * p.group + it / q_tiles : h / p.group;
           uint64_t *full = &bars[L::kBarStepFull + s];
           mbar_arrive_expect_tx(full, 2 * S::kBytes);
-          S::load(smem + L::kOffStep0 + s * S::kBytes, &p.tm_step0, full, o0, oh, b, pol);
-          S::load(smem + L::kOffStep1 + s * S::kBytes, &p.tm_step1, full, o0, oh, b, pol);
+          S::template load<kXStep>(smem + L::kOffStep0 + s * S::kBytes, 0, step0, full, o0, oh, b, pol);
+          S::template load<kXStep>(smem + L::kOffStep1 + s * S::kBytes, 0, step1, full, o0, oh, b, pol);
         }
         // every copy issued lands before the CTA exits
         mbar_wait(&bars[L::kBarFixFull], 0, wc_drain);

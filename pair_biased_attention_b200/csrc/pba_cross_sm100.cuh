@@ -82,11 +82,14 @@ struct XTileLayout {
       *reinterpret_cast<uint4 *>(tile + slab * kSlabBytes + r * kRowBytes + chunk * 16) = make_uint4(0, 0, 0, 0);
     }
   }
-  static __device__ __forceinline__ void load(void *dst, const void *map, uint64_t *bar, int row, int h, int b,
+  // The part-th kBox rows of the tile, from a map whose boxes have that many.
+  template <int kBox>
+  static __device__ __forceinline__ void load(void *dst, int part, const void *map, uint64_t *bar, int row, int h, int b,
                                               uint64_t policy) {
 #pragma unroll
     for (int s = 0; s < kSlabs; ++s)
-      tma_load_4d(static_cast<uint8_t *>(dst) + s * kSlabBytes, map, bar, s * kSlabCols, row, h, b, policy);
+      tma_load_4d(static_cast<uint8_t *>(dst) + s * kSlabBytes + part * kBox * kRowBytes, map, bar, s * kSlabCols,
+                  row + part * kBox, h, b, policy);
   }
 };
 
@@ -318,7 +321,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
           if (kc >= L::kKVStages && !mbar_wait(&bars[L::kBarKEmpty + s], ((kc / L::kKVStages) - 1) & 1, wc))
             return false;
           mbar_arrive_expect_tx(&bars[L::kBarKFull + s], T::kBytes);
-          T::load(smem + L::kOffK + s * T::kBytes, &p.tm_k, &bars[L::kBarKFull + s], j * kXTile, un.h / p.group, un.b,
+          T::template load<kXTile>(smem + L::kOffK + s * T::kBytes, 0, &p.tm_k, &bars[L::kBarKFull + s], j * kXTile, un.h / p.group, un.b,
                   pol_keep);
           ++kc;
           return true;
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
           if (vc >= L::kKVStages && !mbar_wait(&bars[L::kBarVEmpty + s], ((vc / L::kKVStages) - 1) & 1, wc))
             return false;
           mbar_arrive_expect_tx(&bars[L::kBarVFull + s], T::kBytes);
-          T::load(smem + L::kOffV + s * T::kBytes, &p.tm_v, &bars[L::kBarVFull + s], j * kXTile, un.h / p.group, un.b,
+          T::template load<kXTile>(smem + L::kOffV + s * T::kBytes, 0, &p.tm_v, &bars[L::kBarVFull + s], j * kXTile, un.h / p.group, un.b,
                   pol_keep);
           ++vc;
           return true;
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
           if (!ok) break;
           mbar_arrive_expect_tx(&bars[L::kBarQFull], kXQTiles * T::kBytes);
           for (int w = 0; w < kXQTiles; ++w)
-            T::load(smem + L::kOffQ + w * T::kBytes, &p.tm_q, &bars[L::kBarQFull], un.q0 + w * kXTile, un.h, un.b,
+            T::template load<kXTile>(smem + L::kOffQ + w * T::kBytes, 0, &p.tm_q, &bars[L::kBarQFull], un.q0 + w * kXTile, un.h, un.b,
                     pol_stream);
           ++uc;
           ok = load_k(un, 0);
