@@ -80,15 +80,44 @@ cudaError_t set_up(K kern, int smem) {
   return e;
 }
 
-template <int D>
-cudaError_t launch_cross(const pba::CrossParams &p, int grid, cudaStream_t stream) {
-  auto kern = pba::pba_cross_sm100_kernel<D>;
+// `splits` > 1: clusters of that many blocks.
+template <typename K, typename P>
+cudaError_t launch_clusters(K kern, const P &p, int64_t grid, int threads, int splits, int smem, cudaStream_t stream) {
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = unsigned(splits), cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = stream;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int D, bool kShared>
+cudaError_t launch_cross(const pba::CrossParams &p, int64_t grid, cudaStream_t stream) {
+  auto kern = pba::pba_cross_sm100_kernel<D, kShared>;
   constexpr int smem = pba::CrossLayout<D>::kSmemAlloc;
   static PerDeviceOnce once;
   const cudaError_t err = once_per_device(once, [&] { return set_up(kern, smem); });
   if (err != cudaSuccess) return err;
-  kern<<<grid, pba::kXThreads, smem, stream>>>(p);
+  if (kShared) return launch_clusters(kern, p, grid, pba::kXThreads, p.splits, smem, stream);
+  kern<<<unsigned(grid), pba::kXThreads, smem, stream>>>(p);
   return cudaGetLastError();
+}
+
+// CTAs that share a unit of the tile kernel where there are fewer units than
+// SMs: a power of two (the join shares out 256 rows) such that the clusters
+// find room (a cluster lies within one of the chip's groups of SMs, so not all
+// SMs can be in one) and each CTA has two key tiles at least.
+int tile_splits(const pba_cross_desc &d, int64_t units) {
+  const int64_t tiles = ceil_div(d.Nk, pba::kXTile);
+  int s = 1;
+  while (s < pba::kXMaxSplits && units * s * 2 <= 132 && tiles >= s * 4) s *= 2;
+  return s;
 }
 
 template <int D>
@@ -117,8 +146,10 @@ pba_status run_tiles(const pba_cross_desc &d, const void *q, const void *k, cons
   const int sms = sm_count();
   if (p.err == nullptr || sms < 1) return PBA_ERR_CUDA;
   p.timeout_ns = wait_timeout_ns();
-  const int grid = int(std::min<int64_t>(n_units, sms));  // persistent: one CTA per SM
-  const cudaError_t e = launch_cross<D>(p, grid, stream);
+  p.splits = tile_splits(d, n_units);
+  // persistent, one CTA per SM, or a cluster for each unit
+  const int64_t grid = p.splits > 1 ? n_units * p.splits : std::min<int64_t>(n_units, sms);
+  const cudaError_t e = p.splits > 1 ? launch_cross<D, true>(p, grid, stream) : launch_cross<D, false>(p, grid, stream);
   return e == cudaSuccess ? PBA_OK : PBA_ERR_CUDA;
 }
 
@@ -126,7 +157,7 @@ pba_status run_tiles(const pba_cross_desc &d, const void *q, const void *k, cons
 // with at least one step per warp.
 int split_count(const pba_cross_desc &d, int64_t units, int blocks_per_sm) {
   const int64_t fit = 148 * blocks_per_sm / units, most = ceil_div(d.Nk, pba::kXsWarps * pba::kXsKeys);
-  return int(std::max<int64_t>(1, std::min<int64_t>({pba::kXsMaxSplits, fit, most})));
+  return int(std::max<int64_t>(1, std::min<int64_t>({pba::kXMaxSplits, fit, most})));
 }
 
 template <int D>
@@ -156,23 +187,25 @@ pba_status run_split(const pba_cross_desc &d, const void *q, const void *k, cons
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       }) != cudaSuccess)
     return PBA_ERR_CUDA;
-  cudaLaunchAttribute cluster;
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = unsigned(splits), cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(unsigned(units * splits));
-  cfg.blockDim = dim3(pba::kXsThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = &cluster;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? PBA_OK : PBA_ERR_CUDA;
+  return launch_clusters(kern, p, units * splits, pba::kXsThreads, splits, smem, stream) == cudaSuccess ? PBA_OK
+                                                                                                        : PBA_ERR_CUDA;
 }
 
-// Few rows per key head are bound by reading keys and values, and the split
-// kernel reads them once over the whole card.
-bool few_rows(const pba_cross_desc &d) { return d.H / d.Hkv * d.Nq <= 64; }
+// Whether the kernel for few rows is the faster one.  It reads keys and values
+// once for every 16 query rows of a key head, from L2 after the first time, at
+// about 9 TB/s over the card; the tile kernel takes about 1.45 us (2.2 at
+// D = 128) for 128 keys of a unit of 256 rows of one head, however few of them
+// there are, and 4 us more to begin and end.  Measured on either side, few rows
+// against tiles: 4 x 8 heads, 64 x 4096: 20.3 and 23.1 us, 96 x 4096: 34.7 and
+// 23.1; 16 heads on 4, 32 x 8192: 14.3 and 40.7; 4 x 32 heads on 8, D = 128,
+// 32 x 2048: 36.7 and 40.3, 64 x 2048: 70.7 and 40.7.
+bool few_rows(const pba_cross_desc &d) {
+  const double read = double(d.B * d.Hkv * ceil_div(d.H / d.Hkv * d.Nq, pba::kXsRows)) * double(d.Nk * d.D) * 4.0;
+  const int64_t units = d.B * d.H * ceil_div(d.Nq, pba::kXQTiles * pba::kXTile);
+  const int64_t splits = tile_splits(d, units);
+  const int64_t tiles = ceil_div(ceil_div(d.Nk, pba::kXTile), splits) * ceil_div(units * splits, 148);
+  return read / 9e6 <= double(tiles) * (d.D == 128 ? 2.2 : 1.45) + 4.0;
+}
 
 template <int D, bool kB>
 cudaError_t launch_cross_bwd(const pba::CrossBwdParams &p, int64_t grid, cudaStream_t stream) {

@@ -28,6 +28,11 @@
 // one.  D = 128: O0 and O1 take [256,512) and P lies over its own S, whose next
 // tile then waits for the product with V; the two query tiles alternate.
 //
+// With fewer units than SMs a thread-block cluster shares a unit: each of its
+// CTAs takes a share of the keys, leaves its O (not yet divided), maximum and
+// sum in shared memory, and the cluster joins them row by row through
+// distributed shared memory, always in the same order.
+//
 // Keys that do not take part cost the softmax nothing: warp 10 zeroes their
 // rows of K and V in shared memory, so that what lies there, NaN included, does
 // not matter, and in a tile that has any it fills one more column of K, 0 or
@@ -36,6 +41,7 @@
 // instead took 35 of 93 us at 2048 x 2048 keys, 32 heads, one key in ten masked.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cuda.h>
 
 #include "pba_ptx.cuh"
@@ -52,6 +58,7 @@ constexpr int kXWarpMma1 = 11;
 constexpr int kXRegsSoftmax = 224;
 constexpr int kXRegsOther = 56;
 constexpr int kXRegSplitTotal = 256 * kXRegsSoftmax + 128 * kXRegsOther;
+constexpr int kXMaxSplits = 8;  // CTAs of a cluster (the portable limit)
 constexpr float kXLog2e = 1.4426950408889634f;
 constexpr float kXLn2 = 0.6931471805599453f;
 
@@ -97,6 +104,7 @@ struct CrossParams {
   CUtensorMap tm_q, tm_k, tm_v;  // (D, n, heads, B) bf16, box {min(D, 64), 128, 1, 1}
   int32_t B, H, group, Nq, Nk;   // group = H / Hkv
   int32_t n_qblocks, n_units;
+  int32_t splits;                // CTAs of a cluster that share a unit (1: none does, and the grid is persistent)
   float tau;
   const int32_t *k_len;          // [B] or null
   const uint8_t *mask;           // [B][Nk] or null
@@ -224,14 +232,26 @@ struct CrossLayout {
   static constexpr int kBytes = kOffAbort + 4;
   static constexpr int kSmemAlloc = kBytes + 1024;  // room to align the base to 1024
   static_assert(kSmemAlloc <= 232448, "shared memory budget");
+  // A unit's O and (maximum, sum) for the join, where K, V and the mask columns
+  // were; the 16-byte chunks of a row in an order that spreads over the banks.
+  static constexpr int kOffJoinMl = kOffK + kXQTiles * kXTile * D * 4;
+  static_assert(kOffJoinMl + kXQTiles * kXTile * 8 <= kOffPartial, "join");
+  static __device__ __forceinline__ float4 *join_o(uint8_t *base, int r, int chunk) {
+    return reinterpret_cast<float4 *>(base + kOffK + (r * (D / 4) + (chunk ^ (r & 7))) * 16);
+  }
+  static __device__ __forceinline__ float2 *join_ml(uint8_t *base, int r) {
+    return reinterpret_cast<float2 *>(base + kOffJoinMl + r * 8);
+  }
   static constexpr __host__ __device__ uint32_t col_s(int w) { return uint32_t(w * kXTile); }
   static constexpr __host__ __device__ uint32_t col_p(int w) { return kAlias ? col_s(w) : 256u + w * 64; }
   static constexpr __host__ __device__ uint32_t col_o(int w) { return kAlias ? 256u + w * 128 : 384u + w * 64; }
 };
 
+// A CTA's part of a unit: nt key tiles from key0 on, of keys that end at `keys`.
 struct CrossUnit {
-  int b, h, q0, keys, nt;
+  int b, h, q0, keys, key0, nt;
 };
+template <bool kShared>
 __device__ __forceinline__ CrossUnit cross_unit(const CrossParams &p, int u) {
   const int qblk = u % p.n_qblocks, bh = u / p.n_qblocks;
   CrossUnit x;
@@ -239,11 +259,20 @@ __device__ __forceinline__ CrossUnit cross_unit(const CrossParams &p, int u) {
   x.h = bh - x.b * p.H;
   x.q0 = qblk * (kXQTiles * kXTile);
   x.keys = cross_keys(p.k_len, x.b, p.Nk);
-  x.nt = (x.keys + kXTile - 1) / kXTile;
+  const int tiles = (x.keys + kXTile - 1) / kXTile;
+  x.key0 = 0;
+  x.nt = tiles;
+  if (kShared) {
+    const int per = (tiles + p.splits - 1) / p.splits, part = int(blockIdx.x) % p.splits;
+    x.nt = max(0, min(per, tiles - part * per));
+    x.key0 = part * per * kXTile;
+  }
   return x;
 }
 
-template <int D>
+// kShared: a cluster of p.splits CTAs shares each unit; otherwise the grid is
+// persistent and p.splits is 1.
+template <int D, bool kShared>
 __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __grid_constant__ CrossParams p) {
   using L = CrossLayout<D>;
   using T = typename L::T;
@@ -255,7 +284,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int u_begin = blockIdx.x, u_step = gridDim.x;
+  const int u_begin = kShared ? blockIdx.x / p.splits : blockIdx.x, u_step = kShared ? p.n_units : gridDim.x;
   // whole tiles of keys that all take part: nothing for warp 10 to do
   const bool fix = p.mask != nullptr || p.k_len != nullptr || p.Nk % kXTile != 0;
   volatile int *partial = reinterpret_cast<volatile int *>(smem + L::kOffPartial);
@@ -321,7 +350,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
           if (kc >= L::kKVStages && !mbar_wait(&bars[L::kBarKEmpty + s], ((kc / L::kKVStages) - 1) & 1, wc))
             return false;
           mbar_arrive_expect_tx(&bars[L::kBarKFull + s], T::kBytes);
-          T::template load<kXTile>(smem + L::kOffK + s * T::kBytes, 0, &p.tm_k, &bars[L::kBarKFull + s], j * kXTile, un.h / p.group, un.b,
+          T::template load<kXTile>(smem + L::kOffK + s * T::kBytes, 0, &p.tm_k, &bars[L::kBarKFull + s], un.key0 + j * kXTile, un.h / p.group, un.b,
                   pol_keep);
           ++kc;
           return true;
@@ -331,13 +360,13 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
           if (vc >= L::kKVStages && !mbar_wait(&bars[L::kBarVEmpty + s], ((vc / L::kKVStages) - 1) & 1, wc))
             return false;
           mbar_arrive_expect_tx(&bars[L::kBarVFull + s], T::kBytes);
-          T::template load<kXTile>(smem + L::kOffV + s * T::kBytes, 0, &p.tm_v, &bars[L::kBarVFull + s], j * kXTile, un.h / p.group, un.b,
+          T::template load<kXTile>(smem + L::kOffV + s * T::kBytes, 0, &p.tm_v, &bars[L::kBarVFull + s], un.key0 + j * kXTile, un.h / p.group, un.b,
                   pol_keep);
           ++vc;
           return true;
         };
         for (int u = u_begin; u < p.n_units && ok; u += u_step) {
-          const CrossUnit un = cross_unit(p, u);
+          const CrossUnit un = cross_unit<kShared>(p, u);
           if (un.nt == 0) continue;
           // Q slot: free once the last score MMAs of the previous unit are done
           if (uc > 0) ok = mbar_wait(&bars[L::kBarQEmpty], (uc - 1) & 1, wc);
@@ -432,7 +461,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
       // D <= 64: S(j+1) before P V(j), so that the next scores are there when
       // the softmax has written P(j).  D = 128 (P over S): after it.
       for (int u = u_begin; u < p.n_units && ok; u += u_step) {
-        const int nt = cross_unit(p, u).nt;
+        const int nt = cross_unit<kShared>(p, u).nt;
         if (nt == 0) continue;
         ok = wait(L::kBarQFull, uc) && next_s();
         if (!ok) break;
@@ -496,10 +525,10 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
       };
       // in the order of the loads: K runs one tile ahead of V
       for (int u = u_begin; u < p.n_units && ok; u += u_step) {
-        const CrossUnit un = cross_unit(p, u);
+        const CrossUnit un = cross_unit<kShared>(p, u);
         if (un.nt == 0) continue;
         const uint8_t *mrow = p.mask != nullptr ? p.mask + int64_t(un.b) * p.mask_sb : nullptr;
-        auto bytes = [&](int j) { return cross_mask_bytes<4>(mrow, p.mask_vec4, j * kXTile, un.keys, lane); };
+        auto bytes = [&](int j) { return cross_mask_bytes<4>(mrow, p.mask_vec4, un.key0 + j * kXTile, un.keys, lane); };
         KeepWords<4> keep = cross_keep<4>(bytes(0));
         uint32_t next = un.nt > 1 ? bytes(1) : 0u;
         ok = fix_k(keep);
@@ -533,7 +562,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
     bool ok = true;
     int gt = 0;  // key tiles processed (all units)
     for (int u = u_begin; u < p.n_units && ok; u += u_step) {
-      const CrossUnit un = cross_unit(p, u);
+      const CrossUnit un = cross_unit<kShared>(p, u);
       float m_cur = -INFINITY;  // maximum used for P and l (raw scores)
       float neg_m = 0.f;        // -m_cur in log2 units (0 while there is none)
       float l = 0.f;
@@ -617,14 +646,36 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
       }
 
       // -------------------------------------------------------------- epilogue
-      const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
-      const int row = un.q0 + w * kXTile + t;
       if (un.nt > 0) {
         if (!ok) break;
         ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarODone + w], (gt - 1) & 1, wc));
         if (!ok) break;
         tc_fence_after_sync();
       }
+      if (kShared) {
+        // the unit's only one of this CTA: K and V are done with once both
+        // warpgroups are here, and their memory takes O for the join
+        named_bar_sync(1, 2 * kXTile);
+        const int r = w * kXTile + t;
+        if (un.nt > 0) {
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + c, o);
+            tmem_wait_ld();
+            reg_fence(o);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *L::join_o(smem, r, c / 4 + q) =
+                  make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]), __uint_as_float(o[4 * q + 2]),
+                              __uint_as_float(o[4 * q + 3]));
+          }
+        }
+        *L::join_ml(smem, r) = make_float2(m_cur, l);
+        break;
+      }
+      const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
+      const int row = un.q0 + w * kXTile + t;
       uint4 *op = reinterpret_cast<uint4 *>(p.out + un.b * p.out_sb + un.h * p.out_sh + int64_t(row) * p.out_sn);
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
@@ -657,6 +708,46 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
     }
   }
 
+  if (kShared) {
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    const CrossUnit un = cross_unit<kShared>(p, u_begin);
+    const float c_s = p.tau * kXLog2e;
+    const int rows = kXQTiles * kXTile / p.splits, row0 = int(cluster.block_rank()) * rows;
+    for (int at = threadIdx.x; at < rows * (D / 4); at += kXThreads) {
+      const int r = row0 + at / (D / 4), c = at % (D / 4), row = un.q0 + r;
+      if (row >= p.Nq) continue;
+      float2 ml[kXMaxSplits];
+      float mm = -INFINITY, ll = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int s = 0; s < kXMaxSplits; ++s) {
+        ml[s] = make_float2(-INFINITY, 0.f);
+        if (s < p.splits) ml[s] = *L::join_ml(cluster.map_shared_rank(smem, s), r);
+        mm = fmaxf(mm, ml[s].x);
+      }
+#pragma unroll
+      for (int s = 0; s < kXMaxSplits; ++s) {
+        if (ml[s].y > 0.f) {  // otherwise the part had no key, and left no O
+          const float a = ex2_approx((ml[s].x - mm) * c_s);
+          const float4 o = *L::join_o(cluster.map_shared_rank(smem, s), r, c);
+          ll = fmaf(a, ml[s].y, ll);
+          acc.x = fmaf(a, o.x, acc.x);
+          acc.y = fmaf(a, o.y, acc.y);
+          acc.z = fmaf(a, o.z, acc.z);
+          acc.w = fmaf(a, o.w, acc.w);
+        }
+      }
+      const float inv = ll > 0.f ? 1.f / ll : 0.f;
+      *reinterpret_cast<uint2 *>(p.out + un.b * p.out_sb + un.h * p.out_sh + int64_t(row) * p.out_sn + 4 * c) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (c == 0 && p.lse != nullptr)
+        p.lse[un.b * p.lse_sb + un.h * p.lse_sh + int64_t(row) * p.lse_sn] =
+            ll > 0.f ? fmaf(mm, p.tau, logf(ll)) : -INFINITY;
+    }
+    cluster.sync();  // no CTA leaves while another reads its shared memory
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();

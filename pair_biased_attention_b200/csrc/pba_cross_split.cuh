@@ -23,8 +23,6 @@
 // workspace, always in the same order.
 #pragma once
 
-#include <cooperative_groups.h>
-
 #include "pba_cross_sm100.cuh"
 
 namespace pba {
@@ -33,7 +31,6 @@ constexpr int kXsWarps = 4;
 constexpr int kXsThreads = 32 * kXsWarps;
 constexpr int kXsRows = 16;        // query rows of a block
 constexpr int kXsKeys = 16;        // keys of a warp's step
-constexpr int kXsMaxSplits = 8;    // blocks of a cluster (the portable limit)
 // Blocks on an SM and steps under way per warp, by what registers and shared
 // memory allow.
 template <int D>
@@ -323,10 +320,10 @@ __global__ void __launch_bounds__(kXsThreads, CrossSplitShape<D>::kBlocksPerSm)
   // asked for before the first is used
   for (int at = split * kXsThreads + threadIdx.x; at < live * (D / 4); at += splits * kXsThreads) {
     const int r = at / (D / 4), c = (at - r * (D / 4)) * 4;
-    float2 ml[kXsMaxSplits];
-    float4 x[kXsMaxSplits];
+    float2 ml[kXMaxSplits];
+    float4 x[kXMaxSplits];
 #pragma unroll
-    for (int s = 0; s < kXsMaxSplits; ++s) {
+    for (int s = 0; s < kXMaxSplits; ++s) {
       ml[s] = make_float2(-INFINITY, 0.f);
       x[s] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (s < splits) {
@@ -337,11 +334,11 @@ __global__ void __launch_bounds__(kXsThreads, CrossSplitShape<D>::kBlocksPerSm)
     }
     float mm = ml[0].x;
 #pragma unroll
-    for (int s = 1; s < kXsMaxSplits; ++s) mm = fmaxf(mm, ml[s].x);
+    for (int s = 1; s < kXMaxSplits; ++s) mm = fmaxf(mm, ml[s].x);
     float ll = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int s = 0; s < kXsMaxSplits; ++s) {
+    for (int s = 0; s < kXMaxSplits; ++s) {
       const float a = ml[s].x == -INFINITY ? 0.f : ex2_approx((ml[s].x - mm) * c_s);
       ll = fmaf(a, ml[s].y, ll);
       acc.x = fmaf(a, x[s].x, acc.x);

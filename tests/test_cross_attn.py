@@ -177,11 +177,41 @@ SHAPES = [
     (1, 6, 6, 17, 129),
     (1, 4, 1, 16, 640),
     (2, 2, 1, 33, 5),
-    (1, 3, 3, 65, 128),      # from here the tile kernel
+    (1, 3, 3, 65, 128),
     (2, 2, 2, 200, 300),
     (1, 4, 2, 257, 513),
     (1, 2, 1, 520, 64),
+    (2, 8, 4, 1000, 2049),   # tiles, units shared by clusters
+    (2, 8, 4, 513, 1000),
+    (2, 16, 8, 600, 1000),   # tiles, a CTA to a unit
+    (3, 32, 16, 520, 300),   # and several units to a CTA
 ]
+
+
+def _forward_kernel(B, H, Hkv, Nq, Nk, D):
+    """Which forward kernel the library's rule takes, so that the shapes here are known to reach each of them."""
+    up = lambda a, b: -(-a // b)  # noqa: E731
+    units, tiles, s = B * H * up(Nq, 256), up(Nk, 128), 1
+    while s < 8 and units * s * 2 <= 132 and tiles >= s * 4:
+        s *= 2
+    read = B * Hkv * up(H // Hkv * Nq, 16) * Nk * D * 4.0
+    if read / 9e6 <= up(tiles, s) * up(units * s, 148) * (2.2 if D == 128 else 1.45) + 4:
+        return "rows"
+    return "clusters" if s > 1 else "tiles" if units <= 148 else "persistent"
+
+
+def test_shapes_reach_every_forward_kernel():
+    for D in (32, 64, 128):
+        want = {"rows", "clusters", "tiles", "persistent"}
+        assert {_forward_kernel(*s, D) for s in SHAPES} == want
+        assert {_forward_kernel(*s, D) for s in MASKED} == {"rows", "clusters", "persistent"}
+        assert {_forward_kernel(*s, D) for s in NANS} == {"rows", "clusters", "tiles"}
+        assert _forward_kernel(*MANY, D) == "persistent"
+
+
+MASKED = [(8, 4, 2, 2, 300), (8, 4, 2, 150, 300), (8, 2, 1, 1000, 1100), (8, 8, 2, 800, 300)]
+NANS = [(2, 4, 4, 1, 333), (2, 4, 4, 300, 333), (2, 8, 4, 1000, 1303), (2, 16, 8, 600, 1000)]
+MANY = (7, 16, 4, 600, 700)
 
 
 @pytest.mark.gpu
@@ -195,12 +225,12 @@ def test_all_keys(cuda_device, shape, D):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("D", [32, 64, 128])
-@pytest.mark.parametrize("Nq", [2, 40, 150])
-def test_lengths_and_masks(cuda_device, Nq, D):
+@pytest.mark.parametrize("shape", MASKED)
+def test_lengths_and_masks(cuda_device, shape, D):
     """Lengths of 0, 1, inside and at the end of a tile, beyond Nk and below 0; masks that leave a sequence empty."""
-    B, H, Hkv, Nk = 8, 4, 2, 300
+    B, H, Hkv, Nq, Nk = shape
     q, k, v, dout, g = _inputs(B, H, Hkv, Nq, Nk, D, seed=D + Nq)
-    k_len = torch.tensor([0, 1, 127, 128, 129, 300, 5000, -3], dtype=torch.int32)
+    k_len = torch.tensor([0, 1, 127, 128, 129, Nk, 5000, -3], dtype=torch.int32)
     mask = (torch.rand((B, Nk), generator=g) < 0.8).to(torch.uint8) * 3
     mask[4] = 0
     mask[5, :256] = 0  # whole tiles without a key, then some
@@ -210,12 +240,12 @@ def test_lengths_and_masks(cuda_device, Nq, D):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("D", [32, 64, 128])
-@pytest.mark.parametrize("Nq", [1, 300])
-def test_what_does_not_count_is_not_used(cuda_device, Nq, D):
+@pytest.mark.parametrize("shape", NANS)
+def test_what_does_not_count_is_not_used(cuda_device, shape, D):
     """NaN and infinities behind the lengths and under the mask change no bit."""
-    B, H, Hkv, Nk = 2, 4, 4, 333
+    B, H, Hkv, Nq, Nk = shape
     q, k, v, dout, g = _inputs(B, H, Hkv, Nq, Nk, D, seed=7)
-    k_len = torch.tensor([200, 333], dtype=torch.int32)
+    k_len = torch.tensor([200, Nk], dtype=torch.int32)
     mask = (torch.rand((B, Nk), generator=g) < 0.7).to(torch.uint8)
     for args in ((k_len, None), (None, mask), (k_len, mask)):
         keep = _keep(B, Nk, *args)[:, None, :, None]
@@ -227,10 +257,10 @@ def test_what_does_not_count_is_not_used(cuda_device, Nq, D):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("Nq", [3, 140])
-def test_strides(cuda_device, Nq):
+@pytest.mark.parametrize("shape", [(2, 4, 2, 3, 150), (2, 8, 4, 520, 1000), (2, 16, 8, 600, 700)])
+def test_strides(cuda_device, shape):
     """Heads inside the token axis, padded rows, outputs given by the caller; what lies around an output stays."""
-    B, H, Hkv, Nk, D = 2, 4, 2, 150, 64
+    (B, H, Hkv, Nq, Nk), D = shape, 64
     q, k, v, dout, _ = _inputs(B, H, Hkv, Nq, Nk, D, seed=3)
     want = _check(q, k, v, dout)
 
@@ -253,16 +283,16 @@ def test_strides(cuda_device, Nq):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("Nq", [2, 130])
-def test_scales_and_large_scores(cuda_device, Nq):
+@pytest.mark.parametrize("Nq,H", [(2, 2), (1500, 8), (2000, 40)])
+def test_scales_and_large_scores(cuda_device, Nq, H):
     """A given scale, and scores far enough apart that rows keep one key (the running maximum is raised often)."""
-    q, k, v, dout, _ = _inputs(1, 2, 2, Nq, 400, 64, seed=5, std=4.0)
+    q, k, v, dout, _ = _inputs(1, H, H, Nq, 400, 64, seed=5, std=4.0)
     _check(q, k, v, dout)
     _check(q, k, v, dout, scale=1.0)
     _check(q, k, v, dout, scale=1e-3)
     # scores that rise tile by tile
-    k = (torch.arange(400)[None, None, :, None] / 100.0 * torch.ones(1, 2, 400, 64)).to(torch.bfloat16)
-    q = torch.full((1, 2, Nq, 64), 1.0, dtype=torch.bfloat16)
+    k = (torch.arange(400)[None, None, :, None] / 100.0 * torch.ones(1, H, 400, 64)).to(torch.bfloat16)
+    q = torch.full((1, H, Nq, 64), 1.0, dtype=torch.bfloat16)
     _check(q, k, v, dout, scale=1.0)
     _check(-q, k, v, dout, scale=1.0)
 
@@ -312,7 +342,7 @@ def test_repeatable_other_stream_and_captured(cuda_device, shape):
 @pytest.mark.gpu
 def test_many_units_walk_the_card(cuda_device):
     """More units than SMs, of different lengths, some empty: every ring and barrier phase runs on across units."""
-    B, H, Hkv, Nq, Nk, D = 7, 16, 4, 600, 700, 64
+    (B, H, Hkv, Nq, Nk), D = MANY, 64
     q, k, v, dout, g = _inputs(B, H, Hkv, Nq, Nk, D, seed=13)
     k_len = torch.tensor([700, 0, 130, 1, 0, 512, 333], dtype=torch.int32)
     _check(q, k, v, dout, k_len)
