@@ -323,7 +323,8 @@ typedef enum { PBA_RELPOS_CLIP = 0, PBA_RELPOS_LOG = 1, PBA_RELPOS_LOG_CAUSAL = 
 
 /*
  *   B, H, Nq, Nk   as in pba_attn_desc (B position sets; 1 to share a bias);
- *                  B and H up to 65535, B * Nq up to 2^31 - 1
+ *                  B and H up to 65535, Nq up to 2^30, Nk and B * Nq up to
+ *                  2^31 - 2^20 - 1
  *   dtype          of table, base and out (backward: of dbias)
  *   rows           rows of the table: the buckets, and one more with groups;
  *                  at most 1025
@@ -440,8 +441,8 @@ PBA_API pba_status pba_block_norm_backward(const pba_norm_desc *desc, const void
  *   O_i = sum_j softmax_j( tau q_i.k_j ) v_j  over the keys j < k_len[b] with
  *         key_mask[b][j] != 0
  * Heads may be grouped: head h reads key head h / (H / Hkv).
- *   B, H, Hkv, Nq, Nk, D   H a multiple of Hkv, H <= 65535; Nq, Nk >= 0; D 32,
- *                  64 or 128
+ *   B, H, Hkv, Nq, Nk, D   H a multiple of Hkv, H <= 65535; Nq and Nk from 0 to
+ *                  2^31 - 4097; D 32, 64 or 128
  *   dtype          PBA_BF16 (of q, k, v, out, dout and the gradients)
  *   softmax_scale  tau; 0 selects 1/sqrt(D)
  *   *_stride       (b, h, n) in elements, feature stride 1.  q, k, v, dout:

@@ -705,6 +705,8 @@ def pba_block_norm_backward(h, dh, dy, f=None, gate=None, scale=None, post=None,
     Returns dx, df, dgate (the inputs' dtype) and dscale, dpost_w, dpost_b,
     dpre_w, dpre_b ([C], fp32); None for what was not given."""
     ref = h if h is not None else dh
+    if ref is None:
+        raise ValueError("h and dh cannot both be None")
     code, param_code, params = _norm_params(ref, kind, post, pre, scale)
     _here((h, dh, dy, f, gate, scale, *params), "h dh dy f gate scale post_w post_b pre_w pre_b")
     C = ref.shape[-1]

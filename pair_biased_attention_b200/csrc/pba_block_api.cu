@@ -79,8 +79,9 @@ int32_t log_border(int e, int m, int t, int far) {
 
 pba_status check_relpos(const pba_relpos_desc *d, bool groups) {
   if (d == nullptr) return PBA_ERR_INVALID_ARG;
-  if (d->B < 1 || d->H < 1 || d->B > 65535 || d->H > 65535 || d->Nq < 0 || d->Nk < 0 || d->Nq > kMaxI32 ||
-      d->Nk > kMaxI32 - 512 || d->B * d->Nq > kMaxI32 || d->Nq > (1 << 30))
+  // B * Nq and Nk: the kernels step beyond them by less than 2^20, in 32 bits
+  if (d->B < 1 || d->H < 1 || d->B > 65535 || d->H > 65535 || d->Nq < 0 || d->Nk < 0 || d->Nq > (1 << 30) ||
+      d->Nk > kMaxI32 - (1 << 20) || d->B * d->Nq > kMaxI32 - (1 << 20))
     return PBA_ERR_INVALID_ARG;
   if (!known_dtype(d->dtype)) return PBA_ERR_UNSUPPORTED;
   const int buckets = d->rows - (groups ? 1 : 0);
@@ -423,7 +424,9 @@ pba_status pba_block_norm_forward(const pba_norm_desc *desc, const void *x, cons
 pba_status pba_block_norm_backward_workspace(const pba_norm_desc *desc, int64_t *bytes) {
   if (desc == nullptr || bytes == nullptr || desc->rows < 0 || desc->C < 1) return PBA_ERR_INVALID_ARG;
   if (desc->C > pba::kNormMaxC) return PBA_ERR_UNSUPPORTED;
-  *bytes = desc->rows == 0 ? 0 : norm_blocks(desc->rows, norm_block(desc->C, norm_channels(desc->dtype, true))) * pba::kNormParams * desc->C * 4;
+  const int64_t blocks =
+      desc->rows == 0 ? 0 : norm_blocks(desc->rows, norm_block(desc->C, norm_channels(desc->dtype, true)));
+  *bytes = blocks * pba::kNormParams * desc->C * 4;
   return PBA_OK;
 }
 

@@ -22,7 +22,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 pba_status check_cross(const pba_cross_desc *d) {
   if (d == nullptr) return PBA_ERR_INVALID_ARG;
   if (d->B < 1 || d->H < 1 || d->Hkv < 1 || d->Nq < 0 || d->Nk < 0) return PBA_ERR_INVALID_ARG;
-  if (d->B > kMaxI32 || d->H > 65535 || d->Nq > kMaxI32 - 256 || d->Nk > kMaxI32 - 256) return PBA_ERR_INVALID_ARG;
+  if (d->B > kMaxI32 || d->H > 65535 || d->Nq > kMaxI32 - 4096 || d->Nk > kMaxI32 - 4096)
+    return PBA_ERR_INVALID_ARG;
   if (d->H % d->Hkv != 0) return PBA_ERR_INVALID_ARG;
   if (d->dtype != PBA_BF16) return PBA_ERR_UNSUPPORTED;
   if (d->D != 32 && d->D != 64 && d->D != 128) return PBA_ERR_UNSUPPORTED;
@@ -133,7 +134,7 @@ pba_status run_tiles(const pba_cross_desc &d, const void *q, const void *k, cons
   p.B = int(d.B), p.H = int(d.H), p.group = int(d.H / d.Hkv), p.Nq = int(d.Nq), p.Nk = int(d.Nk);
   p.n_qblocks = int(ceil_div(d.Nq, pba::kXQTiles * pba::kXTile));
   const int64_t n_units = d.B * d.H * p.n_qblocks;
-  if (n_units > kMaxI32) return PBA_ERR_INVALID_ARG;
+  if (n_units > kMaxI32 - 65536) return PBA_ERR_INVALID_ARG;
   p.n_units = int(n_units);
   p.tau = cross_tau(&d);
   p.k_len = k_len;
@@ -168,7 +169,8 @@ pba_status run_split(const pba_cross_desc &d, const void *q, const void *k, cons
   p.B = int(d.B), p.H = int(d.H), p.Hkv = int(d.Hkv), p.group = int(d.H / d.Hkv), p.Nq = int(d.Nq), p.Nk = int(d.Nk);
   p.row_tiles = int(ceil_div(d.H / d.Hkv * d.Nq, pba::kXsRows));
   p.tau = cross_tau(&d);
-  p.q = static_cast<const uint16_t *>(q), p.k = static_cast<const uint16_t *>(k), p.v = static_cast<const uint16_t *>(v);
+  p.q = static_cast<const uint16_t *>(q);
+  p.k = static_cast<const uint16_t *>(k), p.v = static_cast<const uint16_t *>(v);
   p.q_sb = d.q_stride[0], p.q_sh = d.q_stride[1], p.q_sn = d.q_stride[2];
   p.k_sb = d.k_stride[0], p.k_sh = d.k_stride[1], p.k_sn = d.k_stride[2];
   p.v_sb = d.v_stride[0], p.v_sh = d.v_stride[1], p.v_sn = d.v_stride[2];
@@ -200,6 +202,7 @@ pba_status run_split(const pba_cross_desc &d, const void *q, const void *k, cons
 // 23.1; 16 heads on 4, 32 x 8192: 14.3 and 40.7; 4 x 32 heads on 8, D = 128,
 // 32 x 2048: 36.7 and 40.3, 64 x 2048: 70.7 and 40.7.
 bool few_rows(const pba_cross_desc &d) {
+  if (d.H / d.Hkv * d.Nq > kMaxI32 - pba::kXsRows) return false;  // rows of a key head count in 32 bits
   const double read = double(d.B * d.Hkv * ceil_div(d.H / d.Hkv * d.Nq, pba::kXsRows)) * double(d.Nk * d.D) * 4.0;
   const int64_t units = d.B * d.H * ceil_div(d.Nq, pba::kXQTiles * pba::kXTile);
   const int64_t splits = tile_splits(d, units);
@@ -225,11 +228,11 @@ pba_status run_cross_bwd(const pba_cross_desc &d, const void *q, const void *k, 
   pba::CrossBwdParams p;
   std::memset(&p, 0, sizeof(p));
   // a side without rows is loaded by no unit
-  if (d.Nq > 0 && (!cross_map(&p.tm_q, q, D, d.Nq, d.H, d.B, d.q_stride, pba::kXStep) ||
-                   !cross_map(&p.tm_do, dout, D, d.Nq, d.H, d.B, d.dout_stride, pba::kXStep)))
+  if (d.Nq > 0 && (!cross_map(&p.tm_q, q, D, d.Nq, d.H, d.B, d.q_stride, pba::kXBox) ||
+                   !cross_map(&p.tm_do, dout, D, d.Nq, d.H, d.B, d.dout_stride, pba::kXBox)))
     return PBA_ERR_INVALID_ARG;
-  if (d.Nk > 0 && (!cross_map(&p.tm_k, k, D, d.Nk, d.Hkv, d.B, d.k_stride, pba::kXStep) ||
-                   !cross_map(&p.tm_v, v, D, d.Nk, d.Hkv, d.B, d.v_stride, pba::kXStep)))
+  if (d.Nk > 0 && (!cross_map(&p.tm_k, k, D, d.Nk, d.Hkv, d.B, d.k_stride, pba::kXBox) ||
+                   !cross_map(&p.tm_v, v, D, d.Nk, d.Hkv, d.B, d.v_stride, pba::kXBox)))
     return PBA_ERR_INVALID_ARG;
   p.B = int(d.B), p.H = int(d.H), p.Hkv = int(d.Hkv), p.group = int(d.H / d.Hkv), p.Nq = int(d.Nq), p.Nk = int(d.Nk);
   p.tau = cross_tau(&d);

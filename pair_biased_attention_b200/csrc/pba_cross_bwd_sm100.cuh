@@ -7,31 +7,40 @@
 //     dk_j = tau sum dS_ij q_i,  dv_j = sum P_ij dO_i     (kernel B, over the
 //                                 queries of every head that shares key head)
 //
-// Kernel A walks the keys of one 128-row query tile, 64 at a step: S = Q K^T and
-// dP = dO V^T into Tensor Memory, dS in registers and back to Tensor Memory as
-// bf16, dQ += dS K.  Kernel B walks the queries, head by head of the group, of
-// one 128-row key tile: S^T = K Q^T, dP^T = V dO^T, then dV += P^T dO and
+// Kernel A walks the keys of one 128-row query tile: S = Q K^T and dP = dO V^T
+// into Tensor Memory, dS in registers and back to Tensor Memory as bf16,
+// dQ += dS K.  Kernel B walks the queries, head by head of the group, of one
+// 128-row key tile: S^T = K Q^T, dP^T = V dO^T, then dV += P^T dO and
 // dK += dS^T Q.  No atomics and nothing of size Nq Nk in memory: each gradient
 // is summed in one accumulator in one order.
 //
 // One CTA per unit, 384 threads: warps 0-7 two compute warpgroups (row =
-// thread = Tensor Memory lane), which take the steps in turn, each with its own
-// S and dP, so that one's exponentials run while the other waits for its scores
-// or stores; warp 8 the TMA producer, warps 9 and 11 the MMAs, warp 10
-// in kernel A takes out the keys that do not take part, as in the forward (their
-// rows of K and V are zeros, their scores -inf).  For D <= 64 a warpgroup's next
-// S and dP are issued as soon as these have been read; at D = 128 P and dS lie
-// over S and dP, so they wait for the products that read them.
+// thread = Tensor Memory lane), warp 8 the TMA producer, warps 9 and 11 the
+// MMAs, warp 10 in kernel A takes out the keys that do not take part, as in the
+// forward (their rows of K and V are zeros, their scores -inf).
+//   D <= 64: a step is 128 columns, 64 for each warpgroup; its successor's S
+//     and dP are issued as soon as both have read theirs.
+//   D = 128: Tensor Memory holds no second copy of P and dS, so they lie over S
+//     and dP and the next ones wait for the products that read them.  A step is
+//     64 columns there, with S and dP of its own for each warpgroup, which take
+//     the steps in turn: one computes while the other's products run.
+// Measured at 2 x 16 heads x 2048 x 2048, both kernels and Delta, a key mask /
+// none: D = 64 189 / 186 us (taking 64-wide steps in turn: 197 / 183),
+// D = 32 176 / 174 (188 / 176), D = 128 272 / 269 us.  At D = 64 that is
+// 0.46 PFLOP/s counting each product of the formulas once, 0.64 with the scores
+// and dP that B computes again; what is left is the exponentials' and the
+// selects' instructions between the products, and the last wave of 512 units
+// on 148 SMs.
 #pragma once
 
 #include "pba_cross_sm100.cuh"
 
 namespace pba {
 
-constexpr int kXStep = 64;  // keys (A) or queries (B) of a step
+constexpr int kXBox = 64;  // rows of a tile load
 
 struct CrossBwdParams {
-  CUtensorMap tm_q, tm_k, tm_v, tm_do;  // (D, n, heads, B) bf16, box {min(D, 64), 64, 1, 1}
+  CUtensorMap tm_q, tm_k, tm_v, tm_do;  // (D, n, heads, B) bf16, box {min(D, 64), kXBox, 1, 1}
   int32_t B, H, Hkv, group, Nq, Nk;
   int32_t n_tiles;      // A: ceil(Nq / 128) per (b, h); B: ceil(Nk / 128) per (b, hkv)
   float tau;
@@ -48,19 +57,22 @@ struct CrossBwdParams {
 
 template <int D>
 struct CrossBwdLayout {
-  using T = XTileLayout<D>;          // the unit's rows
-  using S = XTileLayout<D, kXStep>;  // a step's
   static constexpr bool kAlias = D == 128;
-  static constexpr int kStages = D == 128 ? 4 : 6;
+  static constexpr int kTurns = kAlias ? 2 : 1;   // warpgroups that take steps in turn (1: they share each)
+  static constexpr int kStep = kAlias ? 64 : 128;  // keys (A) or queries (B) of a step
+  static constexpr int kPer = kStep / 32;
+  using T = XTileLayout<D>;         // the unit's rows
+  using S = XTileLayout<D, kStep>;  // a step's
+  static constexpr int kStages = 4;
   static constexpr int kOffFix0 = 0;
   static constexpr int kOffFix1 = kOffFix0 + T::kBytes;
   static constexpr int kOffStep0 = kOffFix1 + T::kBytes;             // [stage]
   static constexpr int kOffStep1 = kOffStep0 + kStages * S::kBytes;  // [stage]
-  // B: per compute warp -lse log2(e) and -Delta of the step's 64 query columns,
-  // double-buffered by the parity of the warpgroup's steps
-  static constexpr int kRowvFloats = 2 * kXStep;
+  // B: per compute warp -lse log2(e) and -Delta of its 64 query columns of a
+  // step, double-buffered by the parity of the warpgroup's steps
+  static constexpr int kRowvFloats = 2 * 64;
   static constexpr int kOffRowv = kOffStep1 + kStages * S::kBytes;
-  static constexpr int kMaskBytes = kXStep * XMaskTile::kRowBytes;
+  static constexpr int kMaskBytes = kStep * XMaskTile::kRowBytes;
   static constexpr int kOffOnes = kOffRowv + 2 * 8 * kRowvFloats * 4;
   static constexpr int kOffMask = kOffOnes + kXTile * XMaskTile::kRowBytes;  // [stage]
   static constexpr int kOffPartial = kOffMask + kStages * kMaskBytes;        // [stage]: the tile needs its column
@@ -70,23 +82,24 @@ struct CrossBwdLayout {
   static constexpr int kBarStepFull = 1;
   static constexpr int kBarStepEmpty = kBarStepFull + kStages;
   static constexpr int kBarStepReady = kBarStepEmpty + kStages;  // A: keys that do not take part are out
-  static constexpr int kBarSFull = kBarStepReady + kStages;  // [warpgroup], and so on
-  static constexpr int kBarSFree = kBarSFull + 2;
-  static constexpr int kBarGFull = kBarSFree + 2;  // P / dS written to Tensor Memory
-  static constexpr int kBarGDone = kBarGFull + 2;  // the accumulating MMAs of a step are done
-  static constexpr int kBarDrain = kBarGDone + 2;
+  static constexpr int kBarSFull = kBarStepReady + kStages;  // [turn], and so on
+  static constexpr int kBarSFree = kBarSFull + kTurns;
+  static constexpr int kBarGFull = kBarSFree + kTurns;  // P / dS written to Tensor Memory
+  static constexpr int kBarGDone = kBarGFull + kTurns;  // the accumulating MMAs of a step are done
+  static constexpr int kBarDrain = kBarGDone + kTurns;
   static constexpr int kNumBars = kBarDrain + 2;
   static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
   static constexpr int kOffAbort = kOffTmemSlot + 4;
   static constexpr int kBytes = kOffAbort + 4;
   static constexpr int kSmemAlloc = kBytes + 1024;
   static_assert(kSmemAlloc <= 232448, "shared memory budget");
-  // Tensor Memory columns, per warpgroup g: S and dP of 64 columns each, P and
-  // dS as bf16 of 32 each (at D = 128 over S and dP); then the accumulators
-  static constexpr __host__ __device__ uint32_t col_s(int g) { return 128u * g; }
-  static constexpr __host__ __device__ uint32_t col_dp(int g) { return 128u * g + 64; }
-  static constexpr __host__ __device__ uint32_t col_p(int g) { return kAlias ? col_s(g) : 256u + 64 * g; }
-  static constexpr __host__ __device__ uint32_t col_ds(int g) { return kAlias ? col_dp(g) : 288u + 64 * g; }
+  // Tensor Memory columns of warpgroup g: 64 each of S and dP, 32 each of P and
+  // dS as bf16; then the accumulators.  Shared steps have S, dP, P and dS of
+  // both warpgroups next to each other.
+  static constexpr __host__ __device__ uint32_t col_s(int g) { return (kAlias ? 128u : 64u) * g; }
+  static constexpr __host__ __device__ uint32_t col_dp(int g) { return kAlias ? 128u * g + 64 : 128u + 64 * g; }
+  static constexpr __host__ __device__ uint32_t col_p(int g) { return kAlias ? col_s(g) : 256u + 32 * g; }
+  static constexpr __host__ __device__ uint32_t col_ds(int g) { return kAlias ? col_dp(g) : 320u + 32 * g; }
   static constexpr uint32_t kColAcc0 = kAlias ? 256 : 384, kColAcc1 = kColAcc0 + D;
   static_assert(kColAcc1 + D <= 512, "Tensor Memory budget");
 };
@@ -111,10 +124,10 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
   const int h = bh % heads, b = bh / heads;  // A: query head; B: key head
   const int row0 = tile * kXTile;
   const int keys = cross_keys(p.k_len, b, p.Nk);
-  const int q_tiles = (p.Nq + kXStep - 1) / kXStep;
+  const int q_tiles = (p.Nq + L::kStep - 1) / L::kStep;
   // B: a key tile with no key that counts has no steps (its gradients are 0)
-  const int nsteps = kB ? (row0 < keys ? p.group * q_tiles : 0) : (keys + kXStep - 1) / kXStep;
-  const bool fix = !kB && (p.mask != nullptr || p.k_len != nullptr || p.Nk % kXStep != 0);
+  const int nsteps = kB ? (row0 < keys ? p.group * q_tiles : 0) : (keys + L::kStep - 1) / L::kStep;
+  const bool fix = !kB && (p.mask != nullptr || p.k_len != nullptr || p.Nk % L::kStep != 0);
   volatile int *partial = reinterpret_cast<volatile int *>(smem + L::kOffPartial);
 
   if (threadIdx.x == 0) {
@@ -124,10 +137,10 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
       mbar_init(&bars[L::kBarStepEmpty + s], 1);  // the commit after the step's last MMAs
       mbar_init(&bars[L::kBarStepReady + s], 32);
     }
-    for (int g = 0; g < 2; ++g) {
+    for (int g = 0; g < L::kTurns; ++g) {
       mbar_init(&bars[L::kBarSFull + g], 1);
-      mbar_init(&bars[L::kBarSFree + g], kXTile);
-      mbar_init(&bars[L::kBarGFull + g], kXTile);
+      mbar_init(&bars[L::kBarSFree + g], 2 * kXTile / L::kTurns);
+      mbar_init(&bars[L::kBarGFull + g], 2 * kXTile / L::kTurns);
       mbar_init(&bars[L::kBarGDone + g], 1);
     }
     mbar_init(&bars[L::kBarDrain], 1);
@@ -166,8 +179,8 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
         const CUtensorMap *fix0 = kB ? &p.tm_k : &p.tm_q, *fix1 = kB ? &p.tm_v : &p.tm_do;
         const CUtensorMap *step0 = kB ? &p.tm_q : &p.tm_k, *step1 = kB ? &p.tm_do : &p.tm_v;
         for (int half = 0; half < 2; ++half) {
-          T::template load<kXStep>(smem + L::kOffFix0, half, fix0, &bars[L::kBarFixFull], row0, h, b, pol);
-          T::template load<kXStep>(smem + L::kOffFix1, half, fix1, &bars[L::kBarFixFull], row0, h, b, pol);
+          T::template load<kXBox>(smem + L::kOffFix0, half, fix0, &bars[L::kBarFixFull], row0, h, b, pol);
+          T::template load<kXBox>(smem + L::kOffFix1, half, fix1, &bars[L::kBarFixFull], row0, h, b, pol);
         }
         bool ok = true;
         int it = 0;
@@ -175,12 +188,14 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
           const int s = it % L::kStages;
           if (it >= L::kStages) ok = mbar_wait(&bars[L::kBarStepEmpty + s], ((it / L::kStages) - 1) & 1, wc);
           if (!ok) break;
-          const int o0 = (kB ? it % q_tiles : it) * kXStep;
+          const int o0 = (kB ? it % q_tiles : it) * L::kStep;
           const int oh = kB ? h * p.group + it / q_tiles : h / p.group;
           uint64_t *full = &bars[L::kBarStepFull + s];
           mbar_arrive_expect_tx(full, 2 * S::kBytes);
-          S::template load<kXStep>(smem + L::kOffStep0 + s * S::kBytes, 0, step0, full, o0, oh, b, pol);
-          S::template load<kXStep>(smem + L::kOffStep1 + s * S::kBytes, 0, step1, full, o0, oh, b, pol);
+          for (int part = 0; part < L::kStep / kXBox; ++part) {
+            S::template load<kXBox>(smem + L::kOffStep0 + s * S::kBytes, part, step0, full, o0, oh, b, pol);
+            S::template load<kXBox>(smem + L::kOffStep1 + s * S::kBytes, part, step1, full, o0, oh, b, pol);
+          }
         }
         // every copy issued lands before the CTA exits
         mbar_wait(&bars[L::kBarFixFull], 0, wc_drain);
@@ -196,7 +211,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
       // waits hold up the other, and the accumulators see one order.  The whole
       // warp walks through the loop and one lane issues: the operand
       // descriptors then stay in uniform registers.
-      constexpr uint32_t idesc_s = idesc_bf16_f32(kXTile, kXStep, false);  // both operands K-major
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kXTile, L::kStep, false);  // both operands K-major
       constexpr uint32_t idesc_g = idesc_bf16_f32(kXTile, D, true);        // B MN-major
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t smem0 = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
@@ -210,7 +225,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
         const uint32_t ones_lo = smem_desc_lo(smem0 + L::kOffOnes, 16);
         if (ok) ok = wait(L::kBarFixFull, 0);
         for (int it = 0; it < nsteps && ok; ++it) {
-          const int s = it % L::kStages, g = it & 1, n = it >> 1;
+          const int s = it % L::kStages, g = it % L::kTurns, n = it / L::kTurns;
           const int full = (fix ? L::kBarStepReady : L::kBarStepFull) + s;
           const int read = (L::kAlias ? L::kBarGDone : L::kBarSFree) + g;
           ok = n > 0 ? warp_wait2(&bars[full], it / L::kStages, &bars[read], n - 1, wc) : wait(full, it / L::kStages);
@@ -241,12 +256,12 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
         // acc += G X with G (bf16, in Tensor Memory) and X an MN-major tile
         auto issue_g = [&](uint32_t acc, uint32_t gcol, uint32_t x_lo, bool more) {
 #pragma unroll
-          for (int kk = 0; kk < kXStep / 16; ++kk)
+          for (int kk = 0; kk < L::kStep / 16; ++kk)
             mma_bf16_ts(acc, gcol + kk * 8, desc_join(x_lo + S::mn_step(kk), S::kDescHi), idesc_g,
                         (more || kk > 0) ? 1u : 0u);
         };
         for (int it = 0; it < nsteps && ok; ++it) {
-          const int s = it % L::kStages, g = it & 1, n = it >> 1;
+          const int s = it % L::kStages, g = it % L::kTurns, n = it / L::kTurns;
           // the step's tiles are there: its scores came from them
           if (!(ok = wait(L::kBarGFull + g, n))) break;
           tc_fence_after_sync();
@@ -272,11 +287,11 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
       // ================================================================ A: keys that do not take part
       const uint8_t *mrow = p.mask != nullptr ? p.mask + int64_t(b) * p.mask_sb : nullptr;
       bool ok = true;
-      uint32_t next = nsteps > 0 ? cross_mask_bytes<2>(mrow, false, 0, keys, lane) : 0u;
+      uint32_t next = nsteps > 0 ? cross_mask_bytes<L::kPer>(mrow, false, 0, keys, lane) : 0u;
       for (int it = 0; it < nsteps && ok; ++it) {
         const int s = it % L::kStages;
-        const KeepWords<2> keep = cross_keep<2>(next);
-        if (it + 1 < nsteps) next = cross_mask_bytes<2>(mrow, false, (it + 1) * kXStep, keys, lane);
+        const KeepWords<L::kPer> keep = cross_keep<L::kPer>(next);
+        if (it + 1 < nsteps) next = cross_mask_bytes<L::kPer>(mrow, false, (it + 1) * L::kStep, keys, lane);
         ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarStepFull + s], (it / L::kStages) & 1, wc));
         if (!ok) break;
         const bool any = !keep.all();
@@ -294,7 +309,9 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
   } else {
     // ================================================================ compute warpgroups
     setmaxnreg_inc<kXRegsSoftmax>();
-    const int g = warp >> 2;           // takes the steps g, g + 2, ...
+    const int g = warp >> 2;           // shared steps: takes 64 columns; in turn: the steps g, g + 2, ...
+    constexpr bool kShare = L::kTurns == 1;
+    const int turn = kShare ? 0 : g, col0 = kShare ? 64 * g : 0;
     const int t = threadIdx.x & 127;   // row of the unit's tile = Tensor Memory lane
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const int r = row0 + t;            // A: query row; B: key row
@@ -323,7 +340,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
         const int qh = h * p.group + step / q_tiles;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int qi = (step % q_tiles) * kXStep + lane + 32 * e;
+          const int qi = (step % q_tiles) * L::kStep + col0 + lane + 32 * e;
           if (qi < p.Nq) {
             nlse[e] = p.lse[b * p.lse_sb + qh * p.lse_sh + int64_t(qi) * p.lse_sn];
             ndelta[e] = p.delta[(int64_t(b) * p.H + qh) * p.Nq + qi];
@@ -331,24 +348,24 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
         }
       }
     };
-    if (g < nsteps) load_cols(g);
+    if (turn < nsteps) load_cols(turn);
     bool ok = true;
     int n = 0;  // steps of this warpgroup so far
-    for (int it = g; it < nsteps && ok; it += 2, ++n) {
+    for (int it = turn; it < nsteps && ok; it += L::kTurns, ++n) {
       const float clse[2] = {nlse[0], nlse[1]}, cdelta[2] = {ndelta[0], ndelta[1]};
-      if (it + 2 < nsteps) load_cols(it + 2);
+      if (it + L::kTurns < nsteps) load_cols(it + L::kTurns);
       float *rv = reinterpret_cast<float *>(smem + L::kOffRowv) + ((n & 1) * 8 + warp) * L::kRowvFloats;
       if (kB) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int col = lane + 32 * e;
-          const int qi = (it % q_tiles) * kXStep + col;
+          const int qi = (it % q_tiles) * L::kStep + col0 + col;
           rv[col] = qi >= p.Nq ? -INFINITY : (clse[e] == -INFINITY ? 0.f : -clse[e] * kXLog2e);
           rv[64 + col] = qi < p.Nq ? -cdelta[e] : 0.f;
         }
         __syncwarp();
       }
-      ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarSFull + g], n & 1, wc));
+      ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarSFull + turn], n & 1, wc));
       if (!ok) break;
       tc_fence_after_sync();
       const float2 cs2 = make_float2(c_s, c_s);
@@ -363,7 +380,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
       reg_fence(dpv);
       // the warpgroup's next S and dP may overwrite these columns
       tc_fence_before_sync();
-      if (!L::kAlias) mbar_arrive(&bars[L::kBarSFree + g]);
+      if (!L::kAlias) mbar_arrive(&bars[L::kBarSFree + turn]);
       // two quarters of 32 columns, each stored to Tensor Memory before the next is formed
 #pragma unroll
       for (int qt = 0; qt < 2; ++qt) {
@@ -383,14 +400,15 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
             const int i = c + 2 * e;
             const float2 a = ffma2(make_float2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])), cs2, nl[e]);
             const float2 pe = make_float2(ex2_approx(a.x), ex2_approx(a.y));
-            const float2 ds = fmul2(pe, fadd2(make_float2(__uint_as_float(dpv[i]), __uint_as_float(dpv[i + 1])), nd[e]));
+            const float2 dp = make_float2(__uint_as_float(dpv[i]), __uint_as_float(dpv[i + 1]));
+            const float2 ds = fmul2(pe, fadd2(dp, nd[e]));
             if (kB) pk[j4 * 2 + e] = pack_bf16x2(pe.x, pe.y);
             dk[j4 * 2 + e] = pack_bf16x2(ds.x, ds.y);
           }
         }
         if (!L::kAlias && qt == 0 && n > 0) {
           // the accumulating MMAs of its last step read what the stores below overwrite
-          ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarGDone + g], (n - 1) & 1, wc));
+          ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarGDone + turn], (n - 1) & 1, wc));
           if (!ok) break;
           tc_fence_after_sync();
         }
@@ -400,7 +418,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
       if (!ok) break;
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(&bars[L::kBarGFull + g]);
+      mbar_arrive(&bars[L::kBarGFull + turn]);
     }
     // -------------------------------------------------------------- epilogue
     // all steps, the other warpgroup's too, are in the accumulators

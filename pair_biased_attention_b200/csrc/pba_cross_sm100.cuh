@@ -91,8 +91,8 @@ struct XTileLayout {
   }
   // The part-th kBox rows of the tile, from a map whose boxes have that many.
   template <int kBox>
-  static __device__ __forceinline__ void load(void *dst, int part, const void *map, uint64_t *bar, int row, int h, int b,
-                                              uint64_t policy) {
+  static __device__ __forceinline__ void load(void *dst, int part, const void *map, uint64_t *bar, int row, int h,
+                                              int b, uint64_t policy) {
 #pragma unroll
     for (int s = 0; s < kSlabs; ++s)
       tma_load_4d(static_cast<uint8_t *>(dst) + s * kSlabBytes + part * kBox * kRowBytes, map, bar, s * kSlabCols,
@@ -350,8 +350,8 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
           if (kc >= L::kKVStages && !mbar_wait(&bars[L::kBarKEmpty + s], ((kc / L::kKVStages) - 1) & 1, wc))
             return false;
           mbar_arrive_expect_tx(&bars[L::kBarKFull + s], T::kBytes);
-          T::template load<kXTile>(smem + L::kOffK + s * T::kBytes, 0, &p.tm_k, &bars[L::kBarKFull + s], un.key0 + j * kXTile, un.h / p.group, un.b,
-                  pol_keep);
+          T::template load<kXTile>(smem + L::kOffK + s * T::kBytes, 0, &p.tm_k, &bars[L::kBarKFull + s],
+                                   un.key0 + j * kXTile, un.h / p.group, un.b, pol_keep);
           ++kc;
           return true;
         };
@@ -360,8 +360,8 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
           if (vc >= L::kKVStages && !mbar_wait(&bars[L::kBarVEmpty + s], ((vc / L::kKVStages) - 1) & 1, wc))
             return false;
           mbar_arrive_expect_tx(&bars[L::kBarVFull + s], T::kBytes);
-          T::template load<kXTile>(smem + L::kOffV + s * T::kBytes, 0, &p.tm_v, &bars[L::kBarVFull + s], un.key0 + j * kXTile, un.h / p.group, un.b,
-                  pol_keep);
+          T::template load<kXTile>(smem + L::kOffV + s * T::kBytes, 0, &p.tm_v, &bars[L::kBarVFull + s],
+                                   un.key0 + j * kXTile, un.h / p.group, un.b, pol_keep);
           ++vc;
           return true;
         };
@@ -373,8 +373,8 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
           if (!ok) break;
           mbar_arrive_expect_tx(&bars[L::kBarQFull], kXQTiles * T::kBytes);
           for (int w = 0; w < kXQTiles; ++w)
-            T::template load<kXTile>(smem + L::kOffQ + w * T::kBytes, 0, &p.tm_q, &bars[L::kBarQFull], un.q0 + w * kXTile, un.h, un.b,
-                    pol_stream);
+            T::template load<kXTile>(smem + L::kOffQ + w * T::kBytes, 0, &p.tm_q, &bars[L::kBarQFull],
+                                     un.q0 + w * kXTile, un.h, un.b, pol_stream);
           ++uc;
           ok = load_k(un, 0);
           for (int j = 0; j < un.nt && ok; ++j) {
@@ -423,7 +423,8 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
             mma_bf16_ss(tS, desc_join(q_lo + T::k_step(kk), T::kDescHi), desc_join(k_lo + T::k_step(kk), T::kDescHi),
                         idesc_s, kk > 0 ? 1u : 0u);
           if (masked)
-            mma_bf16_ss(tS, desc_join(ones_lo, XMaskTile::kDescHi), desc_join(mask_lo, XMaskTile::kDescHi), idesc_s, 1u);
+            mma_bf16_ss(tS, desc_join(ones_lo, XMaskTile::kDescHi), desc_join(mask_lo, XMaskTile::kDescHi), idesc_s,
+                        1u);
           tc_commit(&bars[L::kBarSFull + w]);
           tc_commit(&bars[L::kBarKEmpty + s]);
         }
@@ -646,16 +647,16 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
       }
 
       // -------------------------------------------------------------- epilogue
-      if (un.nt > 0) {
-        if (!ok) break;
+      if (un.nt > 0 && ok) {
         ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars[L::kBarODone + w], (gt - 1) & 1, wc));
-        if (!ok) break;
         tc_fence_after_sync();
       }
       if (kShared) {
         // the unit's only one of this CTA: K and V are done with once both
-        // warpgroups are here, and their memory takes O for the join
+        // warpgroups are here, and their memory takes O for the join.  A warp
+        // that gave up a wait comes here too, and leaves nothing.
         named_bar_sync(1, 2 * kXTile);
+        if (!ok) break;
         const int r = w * kXTile + t;
         if (un.nt > 0) {
 #pragma unroll
@@ -674,7 +675,8 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
         *L::join_ml(smem, r) = make_float2(m_cur, l);
         break;
       }
-      const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
+      if (!ok) break;
+      const float inv_l = l == 0.f ? 0.f : 1.f / l;  // 0: no key
       const int row = un.q0 + w * kXTile + t;
       uint4 *op = reinterpret_cast<uint4 *>(p.out + un.b * p.out_sb + un.h * p.out_sh + int64_t(row) * p.out_sn);
 #pragma unroll
@@ -704,7 +706,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
       }
       if (row < p.Nq && p.lse != nullptr)
         p.lse[un.b * p.lse_sb + un.h * p.lse_sh + int64_t(row) * p.lse_sn] =
-            (l > 0.f) ? fmaf(neg_m, -kXLn2, logf(l)) : -INFINITY;
+            l == 0.f ? -INFINITY : fmaf(neg_m, -kXLn2, logf(l));
     }
   }
 
@@ -729,7 +731,7 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
       }
 #pragma unroll
       for (int s = 0; s < kXMaxSplits; ++s) {
-        if (ml[s].y > 0.f) {  // otherwise the part had no key, and left no O
+        if (ml[s].y != 0.f) {  // otherwise the part had no key, and left no O
           const float a = ex2_approx((ml[s].x - mm) * c_s);
           const float4 o = *L::join_o(cluster.map_shared_rank(smem, s), r, c);
           ll = fmaf(a, ml[s].y, ll);
@@ -739,12 +741,12 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_sm100_kernel(const __g
           acc.w = fmaf(a, o.w, acc.w);
         }
       }
-      const float inv = ll > 0.f ? 1.f / ll : 0.f;
+      const float inv = ll == 0.f ? 0.f : 1.f / ll;
       *reinterpret_cast<uint2 *>(p.out + un.b * p.out_sb + un.h * p.out_sh + int64_t(row) * p.out_sn + 4 * c) =
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
       if (c == 0 && p.lse != nullptr)
         p.lse[un.b * p.lse_sb + un.h * p.lse_sh + int64_t(row) * p.lse_sn] =
-            ll > 0.f ? fmaf(mm, p.tau, logf(ll)) : -INFINITY;
+            ll == 0.f ? -INFINITY : fmaf(mm, p.tau, logf(ll));
     }
     cluster.sync();  // no CTA leaves while another reads its shared memory
   }

@@ -346,13 +346,13 @@ __global__ void __launch_bounds__(kXsThreads, CrossSplitShape<D>::kBlocksPerSm)
       acc.z = fmaf(a, x[s].z, acc.z);
       acc.w = fmaf(a, x[s].w, acc.w);
     }
-    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;  // 0: no key
     const int row = tile * kXsRows + r;
     const int hr = row / p.Nq, h = hk * p.group + hr, i = row - hr * p.Nq;
     const uint2 w = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     *reinterpret_cast<uint2 *>(p.out + b * p.out_sb + h * p.out_sh + int64_t(i) * p.out_sn + c) = w;
     if (c == 0 && p.lse != nullptr)
-      p.lse[b * p.lse_sb + h * p.lse_sh + int64_t(i) * p.lse_sn] = ll > 0.f ? fmaf(mm, p.tau, logf(ll)) : -INFINITY;
+      p.lse[b * p.lse_sb + h * p.lse_sh + int64_t(i) * p.lse_sn] = ll == 0.f ? -INFINITY : fmaf(mm, p.tau, logf(ll));
   }
   cluster.sync();  // no block leaves while another reads its shared memory
 }

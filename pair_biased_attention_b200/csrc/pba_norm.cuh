@@ -144,7 +144,8 @@ struct RowStream {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         if (sizeof(W) == 2) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) r.v[(4 * i + k) % (E / 2)] = make_float2(bf16lo_to_f32(w[k]), bf16hi_to_f32(w[k]));
+          for (int k = 0; k < 4; ++k)
+            r.v[(4 * i + k) % (E / 2)] = make_float2(bf16lo_to_f32(w[k]), bf16hi_to_f32(w[k]));
         } else {
 #pragma unroll
           for (int k = 0; k < 2; ++k)

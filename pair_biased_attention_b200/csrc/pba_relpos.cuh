@@ -305,11 +305,9 @@ __global__ void __launch_bounds__(kRelposGradThreads, 4) relpos_grad_kernel(cons
     const int far = rule.far, far_hi = rule.kind == 2 ? 0 : far;
     const bool groups = rule.cross >= 0;
     // The keys' positions and groups wait in shared memory for where single
-    // ones are needed; what stays in registers are the weights 1 and 0 of the
-    // eight's members of the queries' group, and the members' range.
-    float2 in[4], ex[4] = {};  // and of the others
-#pragma unroll
-    for (int e = 0; e < 4; ++e) in[e] = make_float2(1.f, 1.f);
+    // ones are needed; what stays in registers is which of the eight are
+    // members of the queries' group, bit e for key e, and the members' range.
+    uint32_t members = 0xFFu;
     int k_min = 2147483647, k_max = -2147483647 - 1;
     {
       int k[8], kg[8] = {};
@@ -326,7 +324,6 @@ __global__ void __launch_bounds__(kRelposGradThreads, 4) relpos_grad_kernel(cons
     // q_lo behind (a bound that saturates is never passed, so this holds at the
     // ends of the range, where a few more values go one by one)
     int q_hi = sub_sat(k_min, far_hi - 1), q_lo = add_sat(k_max, far - 1);
-    bool outside = false;  // some are of another group
     int group = 0;
     bool first = true;
     float2 lo[4] = {}, hi[4] = {}, cross[4] = {};
@@ -359,20 +356,13 @@ __global__ void __launch_bounds__(kRelposGradThreads, 4) relpos_grad_kernel(cons
       if (groups && (first || qq.y != group)) {
         first = false;
         group = qq.y;
-        // no member: any place will do, its weights are 0
         k_min = 2147483647, k_max = -2147483647 - 1;
-        outside = false;
+        members = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int2 key = keys[e * threads];
-          const bool member = key.y == group;
-          outside = outside || !member;
-          const float weight = member ? 1.f : 0.f;
-          if (e & 1)
-            in[e >> 1].y = weight, ex[e >> 1].y = 1.f - weight;
-          else
-            in[e >> 1].x = weight, ex[e >> 1].x = 1.f - weight;
-          if (member) {
+          if (key.y == group) {
+            members |= 1u << e;
             k_min = min(k_min, key.x);
             k_max = max(k_max, key.x);
           }
@@ -380,17 +370,29 @@ __global__ void __launch_bounds__(kRelposGradThreads, 4) relpos_grad_kernel(cons
         q_hi = sub_sat(k_min, far_hi - 1);
         q_lo = add_sat(k_max, far - 1);
       }
-      if (outside) {
+      float2 v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          cross[e] = ffma2(x.pair(e), ex[e], cross[e]);
+      for (int e = 0; e < 4; ++e) v[e] = x.pair(e);
+      if (members == 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cross[e] = fadd2(cross[e], v[e]);
+      } else if (members != 0xFFu) {
+        // selected, not multiplied by 0 or 1: an infinity or a NaN stays in its row
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool mx = (members >> (2 * e)) & 1u, my = (members >> (2 * e + 1)) & 1u;
+          cross[e] = fadd2(cross[e], make_float2(mx ? 0.f : v[e].x, my ? 0.f : v[e].y));
+          v[e] = make_float2(mx ? v[e].x : 0.f, my ? v[e].y : 0.f);
+        }
       }
-      if (qq.x < q_hi) {
+      if (members == 0) {
+        // nothing is left
+      } else if (qq.x < q_hi) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) hi[e] = ffma2(x.pair(e), in[e], hi[e]);
+        for (int e = 0; e < 4; ++e) hi[e] = fadd2(hi[e], v[e]);
       } else if (qq.x > q_lo) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) lo[e] = ffma2(x.pair(e), in[e], lo[e]);
+        for (int e = 0; e < 4; ++e) lo[e] = fadd2(lo[e], v[e]);
       } else {
         const int k_lo = sub_sat(qq.x, far), k_hi = add_sat(qq.x, far);
 #pragma unroll 4

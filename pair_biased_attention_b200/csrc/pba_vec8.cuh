@@ -129,8 +129,9 @@ struct Ring8 {
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        typename T::Word *to = reinterpret_cast<typename T::Word *>(slot + (e * kSize / 16) * stride) + e % (16 / kSize);
-        *to = e < n ? p[e] : typename T::Word(0);
+        using W = typename T::Word;
+        W *to = reinterpret_cast<W *>(slot + (e * kSize / 16) * stride) + e % (16 / kSize);
+        *to = e < n ? p[e] : W(0);
       }
     }
   }
