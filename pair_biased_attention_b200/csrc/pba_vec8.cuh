@@ -135,12 +135,6 @@ struct Ring8 {
       }
     }
   }
-  // element e alone
-  static __device__ __forceinline__ float one(const uint8_t *slot, int stride, const typename T::Word *p, bool inner,
-                                              int e) {
-    const int at = e * int(sizeof(typename T::Word)) + (!kVec && inner ? int(reinterpret_cast<uintptr_t>(p) & 15) : 0);
-    return T::to_f32(*reinterpret_cast<const typename T::Word *>(slot + (at >> 4) * stride + (at & 15)));
-  }
   // `p` as in the fetch: its place inside its aligned word
   static __device__ __forceinline__ Raw8<T> take(const uint8_t *slot, int stride, const typename T::Word *p,
                                                  bool inner) {
