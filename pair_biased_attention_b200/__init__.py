@@ -557,7 +557,7 @@ def _matrix_strides(name, t, shape, dtype):
 
 
 def pba_relpos_bias_forward(table, q_pos, k_pos, rule="clip", max_distance=0, q_group=None, k_group=None, base=None,
-                        out=None, stream=None):
+                            out=None, stream=None):
     """The learned relative position bias: out[b,h,i,j] = table[r, h] (+ base),
     r the bucket of k_pos[b,j] - q_pos[b,i]; the bias argument of pba_forward
     and pba_partial.
@@ -594,7 +594,7 @@ def pba_relpos_bias_forward(table, q_pos, k_pos, rule="clip", max_distance=0, q_
 
 
 def pba_relpos_bias_backward(dbias, q_pos, k_pos, rows, rule="clip", max_distance=0, q_group=None, k_group=None,
-                         stream=None):
+                             stream=None):
     """The gradient of pba_relpos_bias_forward's table: dbias [B,H,Nq,Nk] (bf16 or
     fp32, pba_backward's for instance) summed over the pairs of each of the
     table's ``rows`` rows.  Position arrays of one sequence are shared by the
@@ -608,7 +608,8 @@ def pba_relpos_bias_backward(dbias, q_pos, k_pos, rows, rule="clip", max_distanc
     d.out_stride[:] = _matrix_strides("dbias", dbias, (d.B, H, d.Nq, d.Nk), dbias.dtype)
     lib = load_library()
     need = ctypes.c_int64()
-    _check("pba_relpos_bias_backward_workspace", lib.pba_relpos_bias_backward_workspace(ctypes.byref(d), ctypes.byref(need)))
+    _check("pba_relpos_bias_backward_workspace",
+           lib.pba_relpos_bias_backward_workspace(ctypes.byref(d), ctypes.byref(need)))
     with _alloc_on(stream):
         dtable = dbias.new_empty((d.rows, H), dtype=torch.float32)
         work = dbias.new_empty(need.value, dtype=torch.uint8)
@@ -672,8 +673,8 @@ def _norm_params(ref, kind, post, pre, scale):
     return code, _dtype_code(dtype or ref.dtype), (post_w, post_b, pre_w, pre_b)
 
 
-def pba_block_norm_forward(x, f=None, gate=None, scale=None, post=None, pre=None, kind="layer", eps=1e-5, h=None, y=None,
-                       stream=None):
+def pba_block_norm_forward(x, f=None, gate=None, scale=None, post=None, pre=None, kind="layer", eps=1e-5, h=None,
+                           y=None, stream=None):
     """The norms before and after a block with its gate and residual scale:
     h = x + scale * sigmoid(gate) * post(f), y = pre(h).
 
@@ -699,7 +700,7 @@ def pba_block_norm_forward(x, f=None, gate=None, scale=None, post=None, pre=None
 
 
 def pba_block_norm_backward(h, dh, dy, f=None, gate=None, scale=None, post=None, pre=None, kind="layer", eps=1e-5,
-                        stream=None):
+                            stream=None):
     """Gradients of pba_block_norm_forward.  h is the forward's h (read with pre
     only), dh and dy the gradients of h and y (dh None: zero; dy with pre).
     Returns dx, df, dgate (the inputs' dtype) and dscale, dpost_w, dpost_b,

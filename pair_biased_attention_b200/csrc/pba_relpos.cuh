@@ -10,8 +10,9 @@
 // Parallelism Framework for Biomolecular Modeling", Table 1 "Attn Pair Bias")
 // is this matrix or has it added; the pages name no rule for the positions.
 //
-// Both directions read or write N^2 H elements (and the base), so the row of the table is found once per pair of positions
-// and the arithmetic per element is a shared-memory read and a store.
+// Both directions read or write N^2 H elements (and the base), so the row of
+// the table is found once per pair of positions for all heads, and the
+// arithmetic per element is a shared-memory read and a store, or an addition.
 #pragma once
 
 #include "pba_vec8.cuh"
@@ -132,6 +133,9 @@ __device__ __forceinline__ void load_keys8(const int32_t *p, int c, int Nk, bool
 // The block's columns of the table wait in shared memory, row-contiguous, so
 // that neighbouring distances fall into neighbouring banks; bf16 keeps two
 // heads per word, one read serving both.
+// Measured at 4096 x 4096 x 16 heads, bf16, with a base: 180 us, 6.0 TB/s, 0.91
+// of a copy's rate.  Without the base's ring, its loads one head ahead in
+// registers, that was 279 us.
 template <typename T, bool kVec, bool kBase>
 __global__ void __launch_bounds__(kRelposThreads) relpos_fwd_kernel(const __grid_constant__ RelposParams p) {
   constexpr bool kBf = sizeof(typename T::Word) == 2;
