@@ -17,6 +17,12 @@
 // go through shared memory.  Bound by the bytes read and written, and close
 // behind by the instructions per element: channels are worked on in packed
 // pairs, and a thread takes 32 bytes of every tensor where its registers allow.
+// Measured, bf16: 1024^2 rows of 128 channels with both layer norms, gate and
+// scale (5 tensors, 1.34 GB) 290 us, 4.6 TB/s, where the instructions bound it
+// (three blocks of 256 threads an SM, or scalar arithmetic, 314 us, were no
+// faster); the lighter forms, one norm or none, reach 6.0 to 6.3 TB/s.  The
+// gradients at 512^2 rows (8 tensors, 0.54 GB) 155 us, 3.5 TB/s, bound by
+// instructions as well: each element meets five products' worth of sums.
 #pragma once
 
 #include "pba_vec8.cuh"
