@@ -18,11 +18,11 @@
 // behind by the instructions per element: channels are worked on in packed
 // pairs, and a thread takes 32 bytes of every tensor where its registers allow.
 // Measured, bf16: 1024^2 rows of 128 channels with both layer norms, gate and
-// scale (5 tensors, 1.34 GB) 290 us, 4.6 TB/s, where the instructions bound it
-// (three blocks of 256 threads an SM, or scalar arithmetic, 314 us, were no
-// faster); the lighter forms, one norm or none, reach 6.0 to 6.3 TB/s.  The
-// gradients at 512^2 rows (8 tensors, 0.54 GB) 155 us, 3.5 TB/s, bound by
-// instructions as well: each element meets five products' worth of sums.
+// scale (5 tensors, 1.34 GB) 229 us, 5.9 TB/s, 0.89 of a copy's rate.  With the
+// parameters unpacked from L1 for every row and the rows' addresses multiplied
+// out it was 283 us, bound by instructions; three blocks of 256 threads an SM
+// were no faster, scalar arithmetic took 314 us.  The gradients at 512^2 rows
+// (8 tensors, 0.54 GB) 141 us, 3.8 TB/s, bound by instructions: 157 us before.
 #pragma once
 
 #include "pba_vec8.cuh"
@@ -101,47 +101,54 @@ struct Place {
 // asynchronous copies and reads alone: about 100 KB on their way per SM, which
 // is what it takes to keep HBM busy (one row ahead in registers, 48 KB, reached
 // 0.69 of the rate).  Other rows are read element by element when they are
-// needed.
-template <typename T, bool kVec, int E, int kArrays, int kStages>
+// needed.  Every tensor has a pointer that walks down its rows.
+template <typename T, bool kVec, int E, int kArrays, int kStages, int kThreads>
 struct RowStream {
   using W = typename T::Word;
-  static constexpr int kWords = E * int(sizeof(W)) / 16;                 // 16-byte words of a row
+  static constexpr int kWords = E * int(sizeof(W)) / 16;  // 16-byte words of a row
+  static constexpr int kPer = kWords * 8 / E;             // words of an eight
   static constexpr int kThreadBytes = kVec ? kArrays * kStages * kWords * 16 : 0;
-  uint8_t *slot;  // this thread's first word of the stage in turn
-  int threads, stage;
+  const Place<kVec, E> &at;
+  int word_bytes;  // from a word of the ring to the thread's next
+  uint8_t *ring, *stage;
+  const uint8_t *src[kArrays];  // kVec: the row to be fetched next, else the one to be read next
+  int64_t by[kArrays];
 
-  __device__ __forceinline__ explicit RowStream(uint8_t *smem) {
-    threads = blockDim.x * blockDim.y;
-    slot = smem + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
-    stage = 0;
+  __device__ __forceinline__ RowStream(uint8_t *smem, const Place<kVec, E> &place) : at(place) {
+    word_bytes = 16 * (kThreads == kNormNarrowThreads ? kNormNarrowThreads : int(blockDim.x));
+    ring = stage = smem + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
   }
-  __device__ __forceinline__ uint8_t *word(int array, int i) const {
-    return slot + ((stage * kArrays + array) * kWords + i) * threads * 16;
+  // rows first, first + step, ... of a tensor
+  __device__ __forceinline__ void open(int array, const void *base, int64_t stride, int64_t first, int64_t step) {
+    src[array] = static_cast<const uint8_t *>(base) + (first * stride + at.channel(0)) * int64_t(sizeof(W));
+    by[array] = step * stride * int64_t(sizeof(W));
   }
-  // starts copying a row of tensor `array` into the stage in turn; zeros for a
+  __device__ __forceinline__ uint8_t *word(int array, int i) const { return stage + (array * kWords + i) * word_bytes; }
+  // starts copying the tensor's next row into the stage in turn; zeros for a
   // row past the end and for channels past the last
-  __device__ __forceinline__ void fetch(int array, const void *base, int64_t row_offset, bool row,
-                                        const Place<kVec, E> &at) {
-    if (!kVec) return;
-    constexpr int kPer = kWords * 8 / E;  // words of an eight
-    const uint8_t *p = reinterpret_cast<const uint8_t *>(static_cast<const W *>(base) + (row ? row_offset : 0));
+  __device__ __forceinline__ void fetch(int array, bool row) {
+    if constexpr (kVec) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      const int first = 8 * (i / kPer);  // first channel of the word's eight, as an element of the thread's
-      const bool ok = row && at.has(first);
-      const int offset = at.channel(first) * int(sizeof(W)) + (i % kPer) * 16;
-      cp_async16_part(word(array, i), p + (ok ? offset : 0), ok ? 16 : 0);
+      for (int i = 0; i < kWords; ++i) {
+        if (row && at.has(8 * (i / kPer)))
+          cp_async16(word(array, i), src[array] + (i / kPer) * at.lanes * 8 * int(sizeof(W)) + (i % kPer) * 16);
+        else
+          *reinterpret_cast<uint4 *>(word(array, i)) = make_uint4(0, 0, 0, 0);
+      }
+      src[array] += by[array];
     }
   }
-  __device__ __forceinline__ void close() {  // the stage's last fetch has been started
-    if (kVec) cp_async_commit();
+  __device__ __forceinline__ void turn() {  // the stage's last fetch has been started
+    if constexpr (kVec) {
+      cp_async_commit();
+      constexpr int kStageWords = kArrays * kWords;
+      stage = stage == ring + (kStages - 1) * kStageWords * word_bytes ? ring : stage + kStageWords * word_bytes;
+    }
   }
-  __device__ __forceinline__ void turn() { stage = stage + 1 == kStages ? 0 : stage + 1; }
   __device__ __forceinline__ void wait() const {
     if (kVec) cp_async_wait<kStages - 1>();
   }
-  __device__ __forceinline__ Channels<E> get(int array, const void *base, int64_t row_offset, bool row,
-                                             const Place<kVec, E> &at) const {
+  __device__ __forceinline__ Channels<E> get(int array, bool row) {
     Channels<E> r;
     if (kVec) {
 #pragma unroll
@@ -159,36 +166,43 @@ struct RowStream {
         }
       }
     } else {
-      const W *p = static_cast<const W *>(base) + row_offset;
+      const W *p = reinterpret_cast<const W *>(src[array]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) r.at(e) = row && at.has(e) ? T::to_f32(p[at.channel(e)]) : 0.f;
+      for (int e = 0; e < E; ++e) r.at(e) = row && at.has(e) ? T::to_f32(p[e * at.lanes]) : 0.f;
+      src[array] += by[array];
     }
     return r;
   }
 };
 
+// The rows of an output that a thread writes, one after the other.
 template <typename T, bool kVec, int E>
-__device__ __forceinline__ void store_row(void *base, int64_t row_offset, bool row, const Place<kVec, E> &at,
-                                          Channels<E> &c) {
+struct RowOut {
   using W = typename T::Word;
-  if (!row) return;
-  W *p = static_cast<W *>(base) + row_offset;
+  W *dst;
+  int64_t by;
+  __device__ __forceinline__ RowOut(void *base, int64_t stride, int64_t first, int64_t step)
+      : dst(static_cast<W *>(base) + first * stride), by(step * stride) {}
+  __device__ __forceinline__ void put(bool row, const Place<kVec, E> &at, Channels<E> &c) {
+    if (row) {
 #pragma unroll
-  for (int j = 0; j < E / 8; ++j) {
-    if (kVec) {
-      const float2 *v = c.v + 4 * j;
-      const float x[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
-      if (at.has(8 * j)) store8<T, true>(p + at.channel(8 * j), 8, 1, x);
-    } else {
+      for (int j = 0; j < E / 8; ++j) {
+        if (kVec) {
+          const float2 *v = c.v + 4 * j;
+          const float x[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+          if (at.has(8 * j)) store8<T, true>(dst + at.channel(8 * j), 8, 1, x);
+        } else {
 #pragma unroll
-      for (int e = 8 * j; e < 8 * j + 8; ++e)
-        if (at.has(e)) p[at.channel(e)] = T::from_f32(c.at(e));
+          for (int e = 8 * j; e < 8 * j + 8; ++e)
+            if (at.has(e)) dst[at.channel(e)] = T::from_f32(c.at(e));
+        }
+      }
     }
+    dst += by;
   }
-}
+};
 
 // A thread's channels of a per-channel parameter as fp32 (0 past the end).
-// Parameters stay in L1: they are read for every row.
 template <bool kVec, int E>
 __device__ __forceinline__ Channels<E> param(const void *p, bool f32, const Place<kVec, E> &at) {
   Channels<E> r;
@@ -217,6 +231,64 @@ __device__ __forceinline__ Channels<E> param(const void *p, bool f32, const Plac
   }
   return r;
 }
+
+// The parameters as the kernels multiply with them, for every row anew: N
+// tensors of C channels.  Narrow rows find them in shared memory as fp32
+// (unpacking bf16 from L1 took a tenth of the instructions); for wide ones,
+// whose ring fills it, they come from L1.
+template <bool kWide, bool kVec, int E, int N>
+struct Params {
+  static constexpr int kChannels = 32 * E;  // of the widest narrow row
+  static constexpr int kFloats = kWide ? 1 : N * kChannels;
+  float *buf;
+  const NormParams &p;
+  const Place<kVec, E> &at;
+  // kVec: the halves of the eights in two planes, so that neighbouring threads
+  // read neighbouring words
+  __device__ __forceinline__ float *slot(int k, int c) const {
+    return buf + k * kChannels + (kVec ? ((c >> 2) & 1) * (kChannels / 2) + (c >> 3) * 4 + (c & 3) : c);
+  }
+  // load(c): the parameter's channel c.  The caller synchronises.
+  template <typename F>
+  __device__ __forceinline__ void stage(int k, bool there, F load) {
+    if constexpr (!kWide) {
+      if (!there) return;
+      for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < kChannels; c += kNormNarrowThreads)
+        *slot(k, c) = c < p.C ? load(c) : 0.f;
+    }
+  }
+  __device__ __forceinline__ float one(const void *t, int c) const {
+    return p.param_f32 ? static_cast<const float *>(t)[c] : Bf16::to_f32(static_cast<const uint16_t *>(t)[c]);
+  }
+  // number k; wide: `t`, times `scale` where that is given
+  __device__ __forceinline__ Channels<E> get(int k, const void *t, const void *scale = nullptr) const {
+    Channels<E> r;
+    if constexpr (kWide) {
+      r = param(t, p.param_f32, at);
+      if (scale != nullptr) {
+        const Channels<E> s = param(scale, p.param_f32, at);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) r.v[i] = fmul2(r.v[i], s.v[i]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < E / 8; ++j) {
+        if (kVec) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float4 x = *reinterpret_cast<const float4 *>(slot(k, at.channel(8 * j) + 4 * half));
+            r.v[4 * j + 2 * half] = make_float2(x.x, x.y);
+            r.v[4 * j + 2 * half + 1] = make_float2(x.z, x.w);
+          }
+        } else {
+#pragma unroll
+          for (int e = 8 * j; e < 8 * j + 8; ++e) r.at(e) = *slot(k, at.channel(e));
+        }
+      }
+    }
+    return r;
+  }
+};
 
 // Sums of N values over the threads of a row.  kWide: the row is the block
 // (a multiple of 32 threads), `buf` holds 2 x N x 32 floats used in turn;
@@ -316,76 +388,95 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
   return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
 
+template <int kThreads>
+__host__ __device__ constexpr int norm_fwd_stages() {
+  return kThreads == 1024 ? 2 : 4;
+}
 template <typename T, bool kVec, int kThreads>
-using NormFwdStream = RowStream<T, kVec, norm_fwd_channels<T>(), 3, kThreads == 1024 ? 2 : 4>;
+using NormFwdStream = RowStream<T, kVec, norm_fwd_channels<T>(), 3, norm_fwd_stages<kThreads>(), kThreads>;
 
 template <typename T, bool kVec, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
     block_norm_fwd_kernel(const __grid_constant__ NormParams p) {
   constexpr bool kWide = kThreads > kNormNarrowThreads;
   constexpr int E = norm_fwd_channels<T>();
+  using Par = Params<kWide, kVec, E, 4>;
   __shared__ float buf[kWide ? 2 * 32 : 1];
+  __shared__ __align__(16) float param_buf[Par::kFloats];
   extern __shared__ __align__(16) uint8_t norm_smem[];
   const Place<kVec, E> at(p.C);
   RowSum<kWide, 1> sum{buf, int(blockDim.x), 0};
   const int64_t step = int64_t(gridDim.x) * blockDim.y;
-  NormFwdStream<T, kVec, kThreads> in(norm_smem);
-  int64_t ahead = int64_t(blockIdx.x) * blockDim.y + threadIdx.y, r = ahead;
+  NormFwdStream<T, kVec, kThreads> in(norm_smem, at);
+  int64_t r = int64_t(blockIdx.x) * blockDim.y + threadIdx.y, ahead = r;
+  const bool post = p.post_w != nullptr;
+  in.open(0, p.x, p.x_s, r, step);
+  if (p.f != nullptr) in.open(1, p.f, p.f_s, r, step);
+  if (p.gate != nullptr) in.open(2, p.gate, p.gate_s, r, step);
+  RowOut<T, kVec, E> h_out(p.h, p.h_s, r, step), y_out(p.y, p.y_s, r, step);
   auto fetch = [&]() {
     const bool row = ahead < p.rows;
-    in.fetch(0, p.x, ahead * p.x_s, row, at);
-    if (p.f != nullptr) in.fetch(1, p.f, ahead * p.f_s, row, at);
-    if (p.gate != nullptr) in.fetch(2, p.gate, ahead * p.gate_s, row, at);
-    in.close();
+    in.fetch(0, row);
+    if (p.f != nullptr) in.fetch(1, row);
+    if (p.gate != nullptr) in.fetch(2, row);
     in.turn();
     ahead += step;
   };
-  for (int i = 0; i < (kThreads == 1024 ? 2 : 4); ++i) fetch();
+  for (int i = 0; i < norm_fwd_stages<kThreads>(); ++i) fetch();
+  // h = x + sigmoid(gate) (a v + b), v the normalised f: the scale is part of
+  // the weight a and the bias b.  y = pre_w v + pre_b.
+  const void *a_of = post ? p.post_w : p.scale, *a_scale = post ? p.scale : nullptr;
+  Par par{param_buf, p, at};
+  par.stage(0, a_of != nullptr,
+            [&](int c) { return par.one(a_of, c) * (a_scale != nullptr ? par.one(a_scale, c) : 1.f); });
+  par.stage(1, p.post_b != nullptr,
+            [&](int c) { return par.one(p.post_b, c) * (p.scale != nullptr ? par.one(p.scale, c) : 1.f); });
+  par.stage(2, p.pre_w != nullptr, [&](int c) { return par.one(p.pre_w, c); });
+  par.stage(3, p.pre_b != nullptr, [&](int c) { return par.one(p.pre_b, c); });
+  if (!kWide) __syncthreads();
   // every thread of a warp runs the same number of rounds: a row past the
   // end is carried along as zeros
   for (int64_t r0 = int64_t(blockIdx.x) * blockDim.y; r0 < p.rows; r0 += step, r += step) {
     const bool row = r < p.rows;
     in.wait();
-    Channels<E> h = in.get(0, p.x, r * p.x_s, row, at), u, g;
-    if (p.f != nullptr) u = in.get(1, p.f, r * p.f_s, row, at);
-    if (p.gate != nullptr) g = in.get(2, p.gate, r * p.gate_s, row, at);
+    Channels<E> h = in.get(0, row), u, g;
+    if (p.f != nullptr) u = in.get(1, row);
+    if (p.gate != nullptr) g = in.get(2, row);
     fetch();
     if (p.f != nullptr) {
-      if (p.post_w != nullptr) {
-        const float rs = centre<kWide>(u, p, at, sum);
-        const Channels<E> w = param(p.post_w, p.param_f32, at);
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) u.v[i] = fmul2(u.v[i], fmul2(w.v[i], both(rs)));
+      const float rs = post ? centre<kWide>(u, p, at, sum) : 1.f;
+      if (a_of != nullptr) {
+        const Channels<E> a = par.get(0, a_of, a_scale);
         if (p.post_b != nullptr) {
-          const Channels<E> b = param(p.post_b, p.param_f32, at);
+          const Channels<E> b = par.get(1, p.post_b, p.scale);
 #pragma unroll
-          for (int i = 0; i < E / 2; ++i) u.v[i] = fadd2(u.v[i], b.v[i]);
+          for (int i = 0; i < E / 2; ++i) u.v[i] = ffma2(u.v[i], fmul2(a.v[i], both(rs)), b.v[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i) u.v[i] = fmul2(u.v[i], fmul2(a.v[i], both(rs)));
         }
       }
       if (p.gate != nullptr) {
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) u.v[i] = fmul2(u.v[i], sigmoid2(g.v[i]));
-      }
-      if (p.scale != nullptr) {
-        const Channels<E> s = param(p.scale, p.param_f32, at);
+        for (int i = 0; i < E / 2; ++i) h.v[i] = ffma2(u.v[i], sigmoid2(g.v[i]), h.v[i]);
+      } else {
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) u.v[i] = fmul2(u.v[i], s.v[i]);
+        for (int i = 0; i < E / 2; ++i) h.v[i] = fadd2(h.v[i], u.v[i]);
       }
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) h.v[i] = fadd2(h.v[i], u.v[i]);
-      store_row<T>(p.h, r * p.h_s, row, at, h);
+      h_out.put(row, at, h);
     }
     if (p.pre_w != nullptr) {
       const float rs = centre<kWide>(h, p, at, sum);
-      const Channels<E> w = param(p.pre_w, p.param_f32, at);
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) h.v[i] = fmul2(h.v[i], fmul2(w.v[i], both(rs)));
+      const Channels<E> w = par.get(2, p.pre_w);
       if (p.pre_b != nullptr) {
-        const Channels<E> b = param(p.pre_b, p.param_f32, at);
+        const Channels<E> b = par.get(3, p.pre_b);
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) h.v[i] = fadd2(h.v[i], b.v[i]);
+        for (int i = 0; i < E / 2; ++i) h.v[i] = ffma2(h.v[i], fmul2(w.v[i], both(rs)), b.v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) h.v[i] = fmul2(h.v[i], fmul2(w.v[i], both(rs)));
       }
-      store_row<T>(p.y, r * p.y_s, row, at, h);
+      y_out.put(row, at, h);
     }
   }
 }
@@ -402,7 +493,7 @@ __host__ __device__ constexpr int norm_bwd_stages() {
   return (kThreads == 1024 ? 4 : 8) / int(sizeof(typename T::Word));
 }
 template <typename T, bool kVec, int kThreads>
-using NormBwdStream = RowStream<T, kVec, kNormBwdChannels, 5, norm_bwd_stages<T, kThreads>()>;
+using NormBwdStream = RowStream<T, kVec, kNormBwdChannels, 5, norm_bwd_stages<T, kThreads>(), kThreads>;
 
 template <typename T, bool kVec, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
@@ -410,6 +501,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
   constexpr bool kWide = kThreads > kNormNarrowThreads;
   constexpr int E = kNormBwdChannels;
   using Ch = Channels<E>;
+  using Par = Params<kWide, kVec, E, 4>;
+  __shared__ __align__(16) float param_buf[Par::kFloats];
   __shared__ float buf[kWide ? 2 * 2 * 32 : kNormNarrowThreads * E];
   const Place<kVec, E> at(p.C);
   RowSum<kWide, 2> sum{buf, int(blockDim.x), 0};
@@ -417,33 +510,47 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
   Ch acc[kNormParams] = {};
   const bool pre = p.pre_w != nullptr, post = p.post_w != nullptr;
   extern __shared__ __align__(16) uint8_t norm_smem[];
-  NormBwdStream<T, kVec, kThreads> in(norm_smem);
-  int64_t ahead = int64_t(blockIdx.x) * blockDim.y + threadIdx.y, r = ahead;
+  NormBwdStream<T, kVec, kThreads> in(norm_smem, at);
+  int64_t r = int64_t(blockIdx.x) * blockDim.y + threadIdx.y, ahead = r;
+  if (p.dh != nullptr) in.open(0, p.dh, p.dh_s, r, step);
+  if (pre) {
+    in.open(1, p.h, p.h_s, r, step);
+    in.open(2, p.dy, p.dy_s, r, step);
+  }
+  if (p.f != nullptr) in.open(3, p.f, p.f_s, r, step);
+  if (p.gate != nullptr) in.open(4, p.gate, p.gate_s, r, step);
+  using Out = RowOut<T, kVec, E>;
+  Out dx_out(p.dx, p.dx_s, r, step), df_out(p.df, p.df_s, r, step), dg_out(p.dgate, p.dgate_s, r, step);
   auto fetch = [&]() {
     const bool row = ahead < p.rows;
-    if (p.dh != nullptr) in.fetch(0, p.dh, ahead * p.dh_s, row, at);
+    if (p.dh != nullptr) in.fetch(0, row);
     if (pre) {
-      in.fetch(1, p.h, ahead * p.h_s, row, at);
-      in.fetch(2, p.dy, ahead * p.dy_s, row, at);
+      in.fetch(1, row);
+      in.fetch(2, row);
     }
-    if (p.f != nullptr) in.fetch(3, p.f, ahead * p.f_s, row, at);
-    if (p.gate != nullptr) in.fetch(4, p.gate, ahead * p.gate_s, row, at);
-    in.close();
+    if (p.f != nullptr) in.fetch(3, row);
+    if (p.gate != nullptr) in.fetch(4, row);
     in.turn();
     ahead += step;
   };
   for (int i = 0; i < norm_bwd_stages<T, kThreads>(); ++i) fetch();
+  Par par{param_buf, p, at};
+  par.stage(0, p.scale != nullptr, [&](int c) { return par.one(p.scale, c); });
+  par.stage(1, post, [&](int c) { return par.one(p.post_w, c); });
+  par.stage(2, p.post_b != nullptr, [&](int c) { return par.one(p.post_b, c); });
+  par.stage(3, pre, [&](int c) { return par.one(p.pre_w, c); });
+  if (!kWide) __syncthreads();
   for (int64_t r0 = int64_t(blockIdx.x) * blockDim.y; r0 < p.rows; r0 += step, r += step) {
     const bool row = r < p.rows;
     in.wait();
     Ch t = {}, h = {}, dy = {}, f = {}, g = {};
-    if (p.dh != nullptr) t = in.get(0, p.dh, r * p.dh_s, row, at);
+    if (p.dh != nullptr) t = in.get(0, row);
     if (pre) {
-      h = in.get(1, p.h, r * p.h_s, row, at);
-      dy = in.get(2, p.dy, r * p.dy_s, row, at);
+      h = in.get(1, row);
+      dy = in.get(2, row);
     }
-    if (p.f != nullptr) f = in.get(3, p.f, r * p.f_s, row, at);
-    if (p.gate != nullptr) g = in.get(4, p.gate, r * p.gate_s, row, at);
+    if (p.f != nullptr) f = in.get(3, row);
+    if (p.gate != nullptr) g = in.get(4, row);
     fetch();
     float2 rs = both(1.f);  // of h and of f
     Ch u = f;               // the block's output after its norm
@@ -456,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
       rs = centre2<kWide>(h, none, p, at, sum);
     }
     if (pre) {
-      const Ch w = param(p.pre_w, p.param_f32, at);
+      const Ch w = par.get(3, p.pre_w);
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
         h.v[i] = fmul2(h.v[i], both(rs.x));
@@ -471,15 +578,15 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
       for (int i = 0; i < E / 2; ++i)
         t.v[i] = ffma2(both(rs.x), ffma2(h.v[i], both(b), fadd2(dy.v[i], both(a))), t.v[i]);
     }
-    store_row<T>(p.dx, r * p.dx_s, row, at, t);
+    dx_out.put(row, at, t);
     if (p.f != nullptr) {
       Ch w;
       if (post) {
-        w = param(p.post_w, p.param_f32, at);
+        w = par.get(1, p.post_w);
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) u.v[i] = fmul2(f.v[i], w.v[i]);
         if (p.post_b != nullptr) {
-          const Ch b = param(p.post_b, p.param_f32, at);
+          const Ch b = par.get(2, p.post_b);
 #pragma unroll
           for (int i = 0; i < E / 2; ++i) u.v[i] = fadd2(u.v[i], b.v[i]);
         }
@@ -495,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
         acc[0].v[i] = ffma2(t.v[i], u.v[i], acc[0].v[i]);
       }
       if (p.scale != nullptr) {
-        const Ch sc = param(p.scale, p.param_f32, at);
+        const Ch sc = par.get(0, p.scale);
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) t.v[i] = fmul2(t.v[i], sc.v[i]);
       }
@@ -503,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
 #pragma unroll
         for (int i = 0; i < E / 2; ++i)
           g.v[i] = fmul2(fmul2(t.v[i], u.v[i]), fadd2(both(1.f), make_float2(-s.v[i].x, -s.v[i].y)));
-        store_row<T>(p.dgate, r * p.dgate_s, row, at, g);
+        dg_out.put(row, at, g);
       }
       if (post) {
 #pragma unroll
@@ -519,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
         for (int i = 0; i < E / 2; ++i)
           t.v[i] = fmul2(both(rs.y), ffma2(f.v[i], both(b), fadd2(t.v[i], both(a))));
       }
-      store_row<T>(p.df, r * p.df_s, row, at, t);
+      df_out.put(row, at, t);
     }
   }
   // the block's sums: its rows' threads of a channel added in order
