@@ -62,13 +62,14 @@ struct Whole {
 };
 
 // Where row e + t of a logarithmic side begins: the smallest whole d with
-// d >= e (far / e)^(t / m), that is d^m >= e^(m-t) far^t.  The root is taken
-// in long double; where it lies too near a whole number to say on which side,
-// the whole numbers are compared.
+// d >= e (far / e)^(t / m), that is d^m >= e^(m-t) far^t.  The root is good to
+// 3e-15 of itself (far / e is below 2^31, so the exponent's rounding counts 21
+// times, the other three once); where it lies too near a whole number to say on
+// which side, the whole numbers are compared.
 int32_t log_border(int e, int m, int t, int far) {
-  const long double x = e * std::pow((long double)(far) / e, (long double)(t) / m);
-  const long double near = std::round(x);
-  if (std::fabs(x - near) > 1e-6L) return int32_t(std::ceil(x));
+  const double x = e * std::pow(double(far) / e, double(t) / m);
+  const double near = std::round(x);
+  if (std::fabs(x - near) > 1e-13 * x) return int32_t(std::ceil(x));
   Whole have, need;
   for (int i = 0; i < m; ++i) {
     have.times(uint32_t(near));
