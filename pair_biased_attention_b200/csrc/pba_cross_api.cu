@@ -210,9 +210,9 @@ bool few_rows(const pba_cross_desc &d) {
   return read / 9e6 <= double(tiles) * (d.D == 128 ? 2.2 : 1.45) + 4.0;
 }
 
-template <int D, bool kB>
+template <int D>
 cudaError_t launch_cross_bwd(const pba::CrossBwdParams &p, int64_t grid, cudaStream_t stream) {
-  auto kern = pba::pba_cross_bwd_sm100_kernel<D, kB>;
+  auto kern = pba::pba_cross_bwd_sm100_kernel<D>;
   constexpr int smem = pba::CrossBwdLayout<D>::kSmemAlloc;
   static PerDeviceOnce once;
   const cudaError_t err = once_per_device(once, [&] { return set_up(kern, smem); });
@@ -247,7 +247,7 @@ pba_status run_cross_bwd(const pba_cross_desc &d, const void *q, const void *k, 
   p.timeout_ns = wait_timeout_ns();
   const int64_t q_tiles = ceil_div(d.Nq, pba::kXTile), k_tiles = ceil_div(d.Nk, pba::kXTile);
   const int64_t grid_a = d.B * d.H * q_tiles, grid_b = d.B * d.Hkv * k_tiles;
-  if (grid_a > kMaxI32 || grid_b > kMaxI32 || d.H / d.Hkv * q_tiles * 2 > kMaxI32) return PBA_ERR_INVALID_ARG;
+  if (grid_a + grid_b > kMaxI32 || d.H / d.Hkv * q_tiles * 2 > kMaxI32) return PBA_ERR_INVALID_ARG;
   if (d.Nq > 0) {
     pba::CrossDeltaParams dp;
     dp.dout = static_cast<const uint16_t *>(dout), dp.out = static_cast<const uint16_t *>(out);
@@ -260,14 +260,14 @@ pba_status run_cross_bwd(const pba_cross_desc &d, const void *q, const void *k, 
     if (blocks > kMaxI32) return PBA_ERR_INVALID_ARG;
     pba::pba_cross_delta_kernel<D><<<unsigned(blocks), 256, 0, stream>>>(dp);
     if (cudaGetLastError() != cudaSuccess) return PBA_ERR_CUDA;
-    p.n_tiles = int(q_tiles);
-    if (launch_cross_bwd<D, false>(p, grid_a, stream) != cudaSuccess) return PBA_ERR_CUDA;
   }
-  if (d.Nk > 0) {
-    p.n_tiles = int(k_tiles);
-    if (launch_cross_bwd<D, true>(p, grid_b, stream) != cudaSuccess) return PBA_ERR_CUDA;
-  }
-  return PBA_OK;
+  p.q_tiles = int(q_tiles), p.k_tiles = int(k_tiles);
+  p.units_a = int(grid_a), p.units_b = int(grid_b);
+  // a unit of kind B passes over the queries of a group with four products a
+  // step, one of kind A over the keys with three
+  p.b_first = 4 * p.group * q_tiles >= 3 * k_tiles;
+  if (grid_a + grid_b == 0) return PBA_OK;
+  return launch_cross_bwd<D>(p, grid_a + grid_b, stream) == cudaSuccess ? PBA_OK : PBA_ERR_CUDA;
 }
 
 }  // namespace

@@ -3,20 +3,20 @@
 // over the keys that take part,
 //     Delta_i = sum_d dO_id O_id                         (pba_cross_delta_kernel)
 //     dS_ij   = P_ij (dO_i . v_j - Delta_i)
-//     dq_i = tau sum_j dS_ij k_j                          (kernel A)
-//     dk_j = tau sum dS_ij q_i,  dv_j = sum P_ij dO_i     (kernel B, over the
+//     dq_i = tau sum_j dS_ij k_j                          (kind A)
+//     dk_j = tau sum dS_ij q_i,  dv_j = sum P_ij dO_i     (kind B, over the
 //                                 queries of every head that shares key head)
 //
-// Kernel A walks the keys of one 128-row query tile: S = Q K^T and dP = dO V^T
+// A unit of kind A walks the keys of one 128-row query tile: S = Q K^T and dP = dO V^T
 // into Tensor Memory, dS in registers and back to Tensor Memory as bf16,
-// dQ += dS K.  Kernel B walks the queries, head by head of the group, of one
+// dQ += dS K.  One of kind B walks the queries, head by head of the group, of one
 // 128-row key tile: S^T = K Q^T, dP^T = V dO^T, then dV += P^T dO and
 // dK += dS^T Q.  No atomics and nothing of size Nq Nk in memory: each gradient
 // is summed in one accumulator in one order.
 //
 // One CTA per unit, 384 threads: warps 0-7 two compute warpgroups (row =
 // thread = Tensor Memory lane), warp 8 the TMA producer, warps 9 and 11 the
-// MMAs, warp 10 in kernel A takes out the keys that do not take part, as in the
+// MMAs, warp 10 in kind A takes out the keys that do not take part, as in the
 // forward (their rows of K and V are zeros, their scores -inf).
 //   D <= 64: a step is 128 columns, 64 for each warpgroup; its successor's S
 //     and dP are issued as soon as both have read theirs.
@@ -24,13 +24,15 @@
 //     and dP and the next ones wait for the products that read them.  A step is
 //     64 columns there, with S and dP of its own for each warpgroup, which take
 //     the steps in turn: one computes while the other's products run.
-// Measured at 2 x 16 heads x 2048 x 2048, both kernels and Delta, a key mask /
-// none: D = 64 189 / 186 us (taking 64-wide steps in turn: 197 / 183),
-// D = 32 176 / 174 (188 / 176), D = 128 272 / 269 us.  At D = 64 that is
-// 0.46 PFLOP/s counting each product of the formulas once, 0.64 with the scores
-// and dP that B computes again; what is left is the exponentials' and the
-// selects' instructions between the products, and the last wave of 512 units
-// on 148 SMs.
+// Both kinds are one launch, so that their last waves overlap.  Measured at
+// 2 x 16 heads x 2048 x 2048 with Delta, a key mask / none: D = 64 166 / 162 us
+// (in two launches 189 / 184; 64-wide steps in turn instead of shared ones 8 us
+// more with the mask), D = 32 157 / 154, D = 128 238 / 235 (275 / 270).  At
+// D = 64 that is 0.53 PFLOP/s counting each product of the formulas once, 0.74
+// with the scores and dP that B computes again; what is left is the
+// exponentials' and the conversions' instructions between the products.  Delta
+// summed by kind A's threads for their rows, without its launch of 7 us, was
+// slower (D = 128 by 13 us): their rows are read in 16-byte pieces.
 #pragma once
 
 #include "pba_cross_sm100.cuh"
@@ -42,7 +44,9 @@ constexpr int kXBox = 64;  // rows of a tile load
 struct CrossBwdParams {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;  // (D, n, heads, B) bf16, box {min(D, 64), kXBox, 1, 1}
   int32_t B, H, Hkv, group, Nq, Nk;
-  int32_t n_tiles;      // A: ceil(Nq / 128) per (b, h); B: ceil(Nk / 128) per (b, hkv)
+  int32_t q_tiles;      // A: units per (b, h), ceil(Nq / 128)
+  int32_t k_tiles;      // B: units per (b, hkv), ceil(Nk / 128)
+  int32_t units_a, units_b, b_first;
   float tau;
   const int32_t *k_len;
   const uint8_t *mask;
@@ -104,9 +108,9 @@ struct CrossBwdLayout {
   static_assert(kColAcc1 + D <= 512, "Tensor Memory budget");
 };
 
-// kB = false: kernel A (dq); kB = true: kernel B (dk, dv).
+// kB = false: a unit of kind A (dq); kB = true: of kind B (dk, dv).
 template <int D, bool kB>
-__global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const __grid_constant__ CrossBwdParams p) {
+__device__ __forceinline__ void cross_bwd_unit(const CrossBwdParams &p, int unit) {
   using L = CrossBwdLayout<D>;
   using T = typename L::T;
   using S = typename L::S;
@@ -118,8 +122,9 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int tile = blockIdx.x % p.n_tiles;
-  const int bh = blockIdx.x / p.n_tiles;
+  const int n_tiles = kB ? p.k_tiles : p.q_tiles;
+  const int tile = unit % n_tiles;
+  const int bh = unit / n_tiles;
   const int heads = kB ? p.Hkv : p.H;
   const int h = bh % heads, b = bh / heads;  // A: query head; B: key head
   const int row0 = tile * kXTile;
@@ -461,6 +466,19 @@ __global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const
   __syncthreads();
   tc_fence_after_sync();
   if (warp == kXWarpMma) tmem_dealloc(tmem, 512);
+}
+
+// One launch for both kinds: neither reads what the other writes, and their last
+// waves fill up with each other's units.  The kind with the longer units goes
+// first.
+template <int D>
+__global__ void __launch_bounds__(kXThreads, 1) pba_cross_bwd_sm100_kernel(const __grid_constant__ CrossBwdParams p) {
+  const int at = blockIdx.x, first = p.b_first ? p.units_b : p.units_a;
+  const int unit = at < first ? at : at - first;
+  if ((at < first) == (p.b_first != 0))
+    cross_bwd_unit<D, true>(p, unit);
+  else
+    cross_bwd_unit<D, false>(p, unit);
 }
 
 struct CrossDeltaParams {
