@@ -231,7 +231,7 @@ int64_t norm_blocks(int64_t rows, dim3 block) {
 bool norm_vec(const pba_norm_desc *d, const void *const *rows, const int64_t *strides, int n_rows,
               const void *const *params, int n_params) {
   const int64_t m = 16 / dtype_size(d->dtype);
-  if (d->C % 8 != 0) return false;
+  if (d->C % m != 0) return false;
   for (int i = 0; i < n_rows; ++i)
     if (rows[i] != nullptr && (!aligned16(rows[i]) || (d->rows > 1 && strides[i] % m != 0))) return false;
   for (int i = 0; i < n_params; ++i)
@@ -255,10 +255,29 @@ cudaError_t start_norm(const pba::NormParams &p, bool backward, unsigned grid, d
   using Fwd = pba::NormFwdStream<T, kVec, kThreads>;
   using Bwd = pba::NormBwdStream<T, kVec, kThreads>;
   static_assert(kThreads * Fwd::kThreadBytes <= kNormSmem && kThreads * Bwd::kThreadBytes <= kNormSmem, "ring");
-  return backward ? start_norm_kernel(pba::block_norm_bwd_kernel<T, kVec, kThreads>, once[1],
-                                      threads * Bwd::kThreadBytes, p, grid, block, st)
-                  : start_norm_kernel(pba::block_norm_fwd_kernel<T, kVec, kThreads>, once[0],
-                                      threads * Fwd::kThreadBytes, p, grid, block, st);
+  if (!backward)
+    return start_norm_kernel(pba::block_norm_fwd_kernel<T, kVec, kThreads>, once[0], threads * Fwd::kThreadBytes, p,
+                             grid, block, st);
+  const int smem = threads * Bwd::kThreadBytes;
+  if constexpr (kVec && kThreads <= 512) {
+    // the sets of parts that have a kernel of their own
+    constexpr int kAll = pba::norm_parts(true, true, true, true), kNoGate = pba::norm_parts(true, false, true, true),
+                  kNoPost = pba::norm_parts(true, true, false, true), kAdd = pba::norm_parts(true, false, false, true),
+                  kNorm = pba::norm_parts(false, false, false, true);
+    static PerDeviceOnce known[5];
+    const int parts = p.dh == nullptr ? -1
+                                      : pba::norm_parts(p.f != nullptr, p.gate != nullptr, p.post_w != nullptr,
+                                                        p.pre_w != nullptr);
+    auto start = [&](auto kern, int i) { return start_norm_kernel(kern, known[i], smem, p, grid, block, st); };
+    switch (parts) {
+      case kAll: return start(pba::block_norm_bwd_kernel<T, kVec, kThreads, kAll>, 0);
+      case kNoGate: return start(pba::block_norm_bwd_kernel<T, kVec, kThreads, kNoGate>, 1);
+      case kNoPost: return start(pba::block_norm_bwd_kernel<T, kVec, kThreads, kNoPost>, 2);
+      case kAdd: return start(pba::block_norm_bwd_kernel<T, kVec, kThreads, kAdd>, 3);
+      case kNorm: return start(pba::block_norm_bwd_kernel<T, kVec, kThreads, kNorm>, 4);
+    }
+  }
+  return start_norm_kernel(pba::block_norm_bwd_kernel<T, kVec, kThreads, -1>, once[1], smem, p, grid, block, st);
 }
 
 template <typename T, bool kVec>

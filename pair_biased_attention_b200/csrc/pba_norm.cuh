@@ -17,12 +17,15 @@
 // go through shared memory.  Bound by the bytes read and written, and close
 // behind by the instructions per element: channels are worked on in packed
 // pairs, and a thread takes 32 bytes of every tensor where its registers allow.
-// Measured, bf16: 1024^2 rows of 128 channels with both layer norms, gate and
-// scale (5 tensors, 1.34 GB) 229 us, 5.9 TB/s, 0.89 of a copy's rate.  With the
+// Measured: 1024^2 rows of 128 channels, bf16, with both layer norms, gate and
+// scale (5 tensors, 1.34 GB) 237 us, 5.7 TB/s, 0.86 of a copy's rate.  With the
 // parameters unpacked from L1 for every row and the rows' addresses multiplied
 // out it was 283 us, bound by instructions; three blocks of 256 threads an SM
 // were no faster, scalar arithmetic took 314 us.  The gradients at 512^2 rows
-// (8 tensors, 0.54 GB) 141 us, 3.8 TB/s, bound by instructions: 157 us before.
+// (8 tensors, 0.54 GB) 109 us, 4.9 TB/s.  fp32 rows: 5.4 to 5.7 TB/s either way.
+// Rows of a block, where a row's sums meet at barriers and a block has one row
+// under way, are slower: 32768 rows of 768, bf16, residual and RMS norm 5.1 and
+// 4.2 TB/s forward and backward, with all parts 2.3 and 3.2.
 #pragma once
 
 #include "pba_vec8.cuh"
@@ -82,19 +85,22 @@ __device__ __forceinline__ float dot(const Channels<E> &x, const Channels<E> &y)
   return t.x + t.y;
 }
 
-// Where a thread's channels lie.  kVec (16-byte aligned rows, C a multiple of
-// 8): eights number threadIdx.x, threadIdx.x + blockDim.x, each there or not
-// as a whole.  Otherwise every blockDim.x-th channel from threadIdx.x on, so
-// that neighbouring threads still touch neighbouring channels.
-template <bool kVec, int E>
+// Where a thread's channels lie.  kVec (16-byte aligned rows): words of 16
+// bytes, G channels, number threadIdx.x, + blockDim.x, ..., each there or not as
+// a whole.  Otherwise every blockDim.x-th channel from threadIdx.x on.  Either
+// way neighbouring threads touch neighbouring places (32 bytes a thread in one
+// piece, half a sector to an access, held fp32 rows at 3.9 TB/s).
+template <bool kVec, int E, int G>
 struct Place {
   int lanes, t, C;
   __device__ __forceinline__ explicit Place(int channels) : lanes(blockDim.x), t(threadIdx.x), C(channels) {}
-  __device__ __forceinline__ int channel(int e) const {
-    return kVec ? 8 * (t + (e >> 3) * lanes) + (e & 7) : t + e * lanes;
-  }
-  __device__ __forceinline__ bool has(int e) const { return channel(kVec ? e & ~7 : e) < C; }
+  __device__ __forceinline__ int channel(int e) const { return kVec ? G * (t + e / G * lanes) + e % G : t + e * lanes; }
+  __device__ __forceinline__ bool has(int e) const { return channel(kVec ? e / G * G : e) < C; }
 };
+template <typename T>
+__host__ __device__ constexpr int norm_word() {
+  return 16 / int(sizeof(typename T::Word));
+}
 
 // A thread's channels of `kArrays` tensors, row after row.  Aligned rows run
 // through a ring in shared memory, kStages rows deep, that the thread fills with
@@ -105,16 +111,16 @@ struct Place {
 template <typename T, bool kVec, int E, int kArrays, int kStages, int kThreads>
 struct RowStream {
   using W = typename T::Word;
-  static constexpr int kWords = E * int(sizeof(W)) / 16;  // 16-byte words of a row
-  static constexpr int kPer = kWords * 8 / E;             // words of an eight
+  static constexpr int G = norm_word<T>();
+  static constexpr int kWords = E / G;  // 16-byte words of a row
   static constexpr int kThreadBytes = kVec ? kArrays * kStages * kWords * 16 : 0;
-  const Place<kVec, E> &at;
+  const Place<kVec, E, G> &at;
   int word_bytes;  // from a word of the ring to the thread's next
   uint8_t *ring, *stage;
   const uint8_t *src[kArrays];  // kVec: the row to be fetched next, else the one to be read next
   int64_t by[kArrays];
 
-  __device__ __forceinline__ RowStream(uint8_t *smem, const Place<kVec, E> &place) : at(place) {
+  __device__ __forceinline__ RowStream(uint8_t *smem, const Place<kVec, E, G> &place) : at(place) {
     word_bytes = 16 * (kThreads == kNormNarrowThreads ? kNormNarrowThreads : int(blockDim.x));
     ring = stage = smem + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
   }
@@ -130,8 +136,8 @@ struct RowStream {
     if constexpr (kVec) {
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
-        if (row && at.has(8 * (i / kPer)))
-          cp_async16(word(array, i), src[array] + (i / kPer) * at.lanes * 8 * int(sizeof(W)) + (i % kPer) * 16);
+        if (row && at.has(G * i))
+          cp_async16(word(array, i), src[array] + i * at.lanes * 16);
         else
           *reinterpret_cast<uint4 *>(word(array, i)) = make_uint4(0, 0, 0, 0);
       }
@@ -179,23 +185,28 @@ struct RowStream {
 template <typename T, bool kVec, int E>
 struct RowOut {
   using W = typename T::Word;
+  static constexpr int G = norm_word<T>();
   W *dst;
   int64_t by;
   __device__ __forceinline__ RowOut(void *base, int64_t stride, int64_t first, int64_t step)
       : dst(static_cast<W *>(base) + first * stride), by(step * stride) {}
-  __device__ __forceinline__ void put(bool row, const Place<kVec, E> &at, Channels<E> &c) {
+  __device__ __forceinline__ void put(bool row, const Place<kVec, E, G> &at, Channels<E> &c) {
     if (row) {
+      if (kVec) {
 #pragma unroll
-      for (int j = 0; j < E / 8; ++j) {
-        if (kVec) {
-          const float2 *v = c.v + 4 * j;
-          const float x[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
-          if (at.has(8 * j)) store8<T, true>(dst + at.channel(8 * j), 8, 1, x);
-        } else {
+        for (int i = 0; i < E / G; ++i) {
+          uint32_t w[4];
 #pragma unroll
-          for (int e = 8 * j; e < 8 * j + 8; ++e)
-            if (at.has(e)) dst[at.channel(e)] = T::from_f32(c.at(e));
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = c.v[(G == 8 ? 4 * i + k : 2 * i + k / 2) % (E / 2)];
+            w[k] = G == 8 ? pack_bf16x2(v.x, v.y) : __float_as_uint(k & 1 ? v.y : v.x);
+          }
+          if (at.has(G * i)) st_stream16(dst + at.channel(G * i), make_uint4(w[0], w[1], w[2], w[3]));
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (at.has(e)) dst[at.channel(e)] = T::from_f32(c.at(e));
       }
     }
     dst += by;
@@ -203,31 +214,31 @@ struct RowOut {
 };
 
 // A thread's channels of a per-channel parameter as fp32 (0 past the end).
-template <bool kVec, int E>
-__device__ __forceinline__ Channels<E> param(const void *p, bool f32, const Place<kVec, E> &at) {
+template <bool kVec, int E, int G>
+__device__ __forceinline__ Channels<E> param(const void *p, bool f32, const Place<kVec, E, G> &at) {
   Channels<E> r;
 #pragma unroll
-  for (int j = 0; j < E / 8; ++j) {
-    float x[8] = {};
+  for (int i = 0; i < E / 4; ++i) {  // four channels at a time
+    float x[4] = {};
     if (kVec) {
-      if (at.has(8 * j)) {
+      if (at.has(4 * i)) {
         if (f32) {
-          const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at.channel(8 * j));
-          const float4 a = __ldg(q), b = __ldg(q + 1);
-          x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+          const float4 a = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at.channel(4 * i)));
+          x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
         } else {
-          unpack8(__ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at.channel(8 * j))), x);
+          const uint2 a = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + at.channel(4 * i)));
+          x[0] = bf16lo_to_f32(a.x), x[1] = bf16hi_to_f32(a.x), x[2] = bf16lo_to_f32(a.y), x[3] = bf16hi_to_f32(a.y);
         }
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (at.has(8 * j + e))
-          x[e] = f32 ? __ldg(static_cast<const float *>(p) + at.channel(8 * j + e))
-                     : Bf16::to_f32(__ldg(static_cast<const uint16_t *>(p) + at.channel(8 * j + e)));
+      for (int e = 0; e < 4; ++e)
+        if (at.has(4 * i + e))
+          x[e] = f32 ? __ldg(static_cast<const float *>(p) + at.channel(4 * i + e))
+                     : Bf16::to_f32(__ldg(static_cast<const uint16_t *>(p) + at.channel(4 * i + e)));
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.v[4 * j + i] = make_float2(x[2 * i], x[2 * i + 1]);
+    r.v[2 * i] = make_float2(x[0], x[1]);
+    r.v[2 * i + 1] = make_float2(x[2], x[3]);
   }
   return r;
 }
@@ -236,17 +247,17 @@ __device__ __forceinline__ Channels<E> param(const void *p, bool f32, const Plac
 // tensors of C channels.  Narrow rows find them in shared memory as fp32
 // (unpacking bf16 from L1 took a tenth of the instructions); for wide ones,
 // whose ring fills it, they come from L1.
-template <bool kWide, bool kVec, int E, int N>
+template <bool kWide, bool kVec, int E, int G, int N>
 struct Params {
   static constexpr int kChannels = 32 * E;  // of the widest narrow row
   static constexpr int kFloats = kWide ? 1 : N * kChannels;
   float *buf;
   const NormParams &p;
-  const Place<kVec, E> &at;
-  // kVec: the halves of the eights in two planes, so that neighbouring threads
-  // read neighbouring words
+  const Place<kVec, E, G> &at;
+  // eights: their halves in two planes, so that neighbouring threads read
+  // neighbouring words
   __device__ __forceinline__ float *slot(int k, int c) const {
-    return buf + k * kChannels + (kVec ? ((c >> 2) & 1) * (kChannels / 2) + (c >> 3) * 4 + (c & 3) : c);
+    return buf + k * kChannels + (kVec && G == 8 ? ((c >> 2) & 1) * (kChannels / 2) + (c >> 3) * 4 + (c & 3) : c);
   }
   // load(c): the parameter's channel c.  The caller synchronises.
   template <typename F>
@@ -272,17 +283,14 @@ struct Params {
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < E / 8; ++j) {
+      for (int i = 0; i < E / 4; ++i) {
         if (kVec) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float4 x = *reinterpret_cast<const float4 *>(slot(k, at.channel(8 * j) + 4 * half));
-            r.v[4 * j + 2 * half] = make_float2(x.x, x.y);
-            r.v[4 * j + 2 * half + 1] = make_float2(x.z, x.w);
-          }
+          const float4 x = *reinterpret_cast<const float4 *>(slot(k, at.channel(4 * i)));
+          r.v[2 * i] = make_float2(x.x, x.y);
+          r.v[2 * i + 1] = make_float2(x.z, x.w);
         } else {
 #pragma unroll
-          for (int e = 8 * j; e < 8 * j + 8; ++e) r.at(e) = *slot(k, at.channel(e));
+          for (int e = 4 * i; e < 4 * i + 4; ++e) r.at(e) = *slot(k, at.channel(e));
         }
       }
     }
@@ -328,25 +336,21 @@ struct RowSum {
 };
 
 // x - mean; channels past the end stay 0.
-template <bool kVec, int E>
-__device__ __forceinline__ void take_mean(Channels<E> &x, float mean, const Place<kVec, E> &at) {
+template <bool kVec, int E, int G>
+__device__ __forceinline__ void take_mean(Channels<E> &x, float mean, const Place<kVec, E, G> &at) {
+  if (kVec) {
 #pragma unroll
-  for (int j = 0; j < E / 8; ++j) {
-    if (kVec) {
-      const float2 m = both(at.has(8 * j) ? -mean : 0.f);
+    for (int i = 0; i < E / 2; ++i) x.v[i] = fadd2(x.v[i], both(at.has(2 * i) ? -mean : 0.f));
+  } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x.v[4 * j + i] = fadd2(x.v[4 * j + i], m);
-    } else {
-#pragma unroll
-      for (int e = 8 * j; e < 8 * j + 8; ++e) x.at(e) = at.has(e) ? x.at(e) - mean : 0.f;
-    }
+    for (int e = 0; e < E; ++e) x.at(e) = at.has(e) ? x.at(e) - mean : 0.f;
   }
 }
 
 // Subtracts the mean (layer norm) and returns the reciprocal root of the mean
 // square of what is left.
-template <bool kWide, bool kVec, int E>
-__device__ __forceinline__ float centre(Channels<E> &x, const NormParams &p, const Place<kVec, E> &at,
+template <bool kWide, bool kVec, int E, int G>
+__device__ __forceinline__ float centre(Channels<E> &x, const NormParams &p, const Place<kVec, E, G> &at,
                                         RowSum<kWide, 1> &sum) {
   float v[1];
   if (p.layer) {
@@ -359,9 +363,9 @@ __device__ __forceinline__ float centre(Channels<E> &x, const NormParams &p, con
   return rsqrtf(fmaf(v[0], p.inv_c, p.eps));
 }
 // The same for two rows at once.
-template <bool kWide, bool kVec, int E>
+template <bool kWide, bool kVec, int E, int G>
 __device__ __forceinline__ float2 centre2(Channels<E> &x, Channels<E> &y, const NormParams &p,
-                                          const Place<kVec, E> &at, RowSum<kWide, 2> &sum) {
+                                          const Place<kVec, E, G> &at, RowSum<kWide, 2> &sum) {
   float v[2];
   if (p.layer) {
     v[0] = x.total(), v[1] = y.total();
@@ -400,25 +404,26 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
     block_norm_fwd_kernel(const __grid_constant__ NormParams p) {
   constexpr bool kWide = kThreads > kNormNarrowThreads;
   constexpr int E = norm_fwd_channels<T>();
-  using Par = Params<kWide, kVec, E, 4>;
+  using Par = Params<kWide, kVec, E, norm_word<T>(), 4>;
   __shared__ float buf[kWide ? 2 * 32 : 1];
   __shared__ __align__(16) float param_buf[Par::kFloats];
   extern __shared__ __align__(16) uint8_t norm_smem[];
-  const Place<kVec, E> at(p.C);
+  constexpr int G = norm_word<T>();
+  const Place<kVec, E, G> at(p.C);
   RowSum<kWide, 1> sum{buf, int(blockDim.x), 0};
   const int64_t step = int64_t(gridDim.x) * blockDim.y;
   NormFwdStream<T, kVec, kThreads> in(norm_smem, at);
   int64_t r = int64_t(blockIdx.x) * blockDim.y + threadIdx.y, ahead = r;
-  const bool post = p.post_w != nullptr;
+  const bool post = p.post_w != nullptr, pre = p.pre_w != nullptr, has_f = p.f != nullptr, has_gate = p.gate != nullptr;
   in.open(0, p.x, p.x_s, r, step);
-  if (p.f != nullptr) in.open(1, p.f, p.f_s, r, step);
-  if (p.gate != nullptr) in.open(2, p.gate, p.gate_s, r, step);
+  if (has_f) in.open(1, p.f, p.f_s, r, step);
+  if (has_gate) in.open(2, p.gate, p.gate_s, r, step);
   RowOut<T, kVec, E> h_out(p.h, p.h_s, r, step), y_out(p.y, p.y_s, r, step);
   auto fetch = [&]() {
     const bool row = ahead < p.rows;
     in.fetch(0, row);
-    if (p.f != nullptr) in.fetch(1, row);
-    if (p.gate != nullptr) in.fetch(2, row);
+    if (has_f) in.fetch(1, row);
+    if (has_gate) in.fetch(2, row);
     in.turn();
     ahead += step;
   };
@@ -431,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
             [&](int c) { return par.one(a_of, c) * (a_scale != nullptr ? par.one(a_scale, c) : 1.f); });
   par.stage(1, p.post_b != nullptr,
             [&](int c) { return par.one(p.post_b, c) * (p.scale != nullptr ? par.one(p.scale, c) : 1.f); });
-  par.stage(2, p.pre_w != nullptr, [&](int c) { return par.one(p.pre_w, c); });
+  par.stage(2, pre, [&](int c) { return par.one(p.pre_w, c); });
   par.stage(3, p.pre_b != nullptr, [&](int c) { return par.one(p.pre_b, c); });
   if (!kWide) __syncthreads();
   // every thread of a warp runs the same number of rounds: a row past the
@@ -440,10 +445,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
     const bool row = r < p.rows;
     in.wait();
     Channels<E> h = in.get(0, row), u, g;
-    if (p.f != nullptr) u = in.get(1, row);
-    if (p.gate != nullptr) g = in.get(2, row);
+    if (has_f) u = in.get(1, row);
+    if (has_gate) g = in.get(2, row);
     fetch();
-    if (p.f != nullptr) {
+    if (has_f) {
       const float rs = post ? centre<kWide>(u, p, at, sum) : 1.f;
       if (a_of != nullptr) {
         const Channels<E> a = par.get(0, a_of, a_scale);
@@ -456,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
           for (int i = 0; i < E / 2; ++i) u.v[i] = fmul2(u.v[i], fmul2(a.v[i], both(rs)));
         }
       }
-      if (p.gate != nullptr) {
+      if (has_gate) {
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) h.v[i] = ffma2(u.v[i], sigmoid2(g.v[i]), h.v[i]);
       } else {
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
       }
       h_out.put(row, at, h);
     }
-    if (p.pre_w != nullptr) {
+    if (pre) {
       const float rs = centre<kWide>(h, p, at, sum);
       const Channels<E> w = par.get(2, p.pre_w);
       if (p.pre_b != nullptr) {
@@ -495,62 +500,75 @@ __host__ __device__ constexpr int norm_bwd_stages() {
 template <typename T, bool kVec, int kThreads>
 using NormBwdStream = RowStream<T, kVec, kNormBwdChannels, 5, norm_bwd_stages<T, kThreads>(), kThreads>;
 
-template <typename T, bool kVec, int kThreads>
+// kParts: which parts there are (norm_parts), known when the kernel is built for
+// the usual sets of them, with dh; or -1, asked at run time.  The formulas are
+// long enough for that to count: 512^2 rows of 128 channels, bf16, all parts 141
+// us asked and 109 known, residual and layer norm 108 and 77.  The forward
+// gained nothing by it.
+__host__ __device__ constexpr int norm_parts(bool f, bool gate, bool post, bool pre) {
+  return f + 2 * gate + 4 * post + 8 * pre;
+}
+template <typename T, bool kVec, int kThreads, int kParts>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
     block_norm_bwd_kernel(const __grid_constant__ NormParams p) {
   constexpr bool kWide = kThreads > kNormNarrowThreads;
   constexpr int E = kNormBwdChannels;
   using Ch = Channels<E>;
-  using Par = Params<kWide, kVec, E, 4>;
+  using Par = Params<kWide, kVec, E, norm_word<T>(), 4>;
   __shared__ __align__(16) float param_buf[Par::kFloats];
   __shared__ float buf[kWide ? 2 * 2 * 32 : kNormNarrowThreads * E];
-  const Place<kVec, E> at(p.C);
+  constexpr int G = norm_word<T>();
+  const Place<kVec, E, G> at(p.C);
   RowSum<kWide, 2> sum{buf, int(blockDim.x), 0};
   const int64_t step = int64_t(gridDim.x) * blockDim.y;
   Ch acc[kNormParams] = {};
-  const bool pre = p.pre_w != nullptr, post = p.post_w != nullptr;
+  constexpr bool kKnown = kParts >= 0;
+  const bool has_f = kKnown ? kParts & 1 : p.f != nullptr, has_gate = kKnown ? kParts & 2 : p.gate != nullptr;
+  const bool post = kKnown ? kParts & 4 : p.post_w != nullptr, pre = kKnown ? kParts & 8 : p.pre_w != nullptr;
+  const bool has_dh = kKnown || p.dh != nullptr;
+  const bool has_scale = p.scale != nullptr, has_post_b = p.post_b != nullptr, layer = p.layer;
   extern __shared__ __align__(16) uint8_t norm_smem[];
   NormBwdStream<T, kVec, kThreads> in(norm_smem, at);
   int64_t r = int64_t(blockIdx.x) * blockDim.y + threadIdx.y, ahead = r;
-  if (p.dh != nullptr) in.open(0, p.dh, p.dh_s, r, step);
+  if (has_dh) in.open(0, p.dh, p.dh_s, r, step);
   if (pre) {
     in.open(1, p.h, p.h_s, r, step);
     in.open(2, p.dy, p.dy_s, r, step);
   }
-  if (p.f != nullptr) in.open(3, p.f, p.f_s, r, step);
-  if (p.gate != nullptr) in.open(4, p.gate, p.gate_s, r, step);
+  if (has_f) in.open(3, p.f, p.f_s, r, step);
+  if (has_gate) in.open(4, p.gate, p.gate_s, r, step);
   using Out = RowOut<T, kVec, E>;
   Out dx_out(p.dx, p.dx_s, r, step), df_out(p.df, p.df_s, r, step), dg_out(p.dgate, p.dgate_s, r, step);
   auto fetch = [&]() {
     const bool row = ahead < p.rows;
-    if (p.dh != nullptr) in.fetch(0, row);
+    if (has_dh) in.fetch(0, row);
     if (pre) {
       in.fetch(1, row);
       in.fetch(2, row);
     }
-    if (p.f != nullptr) in.fetch(3, row);
-    if (p.gate != nullptr) in.fetch(4, row);
+    if (has_f) in.fetch(3, row);
+    if (has_gate) in.fetch(4, row);
     in.turn();
     ahead += step;
   };
   for (int i = 0; i < norm_bwd_stages<T, kThreads>(); ++i) fetch();
   Par par{param_buf, p, at};
-  par.stage(0, p.scale != nullptr, [&](int c) { return par.one(p.scale, c); });
+  par.stage(0, has_scale, [&](int c) { return par.one(p.scale, c); });
   par.stage(1, post, [&](int c) { return par.one(p.post_w, c); });
-  par.stage(2, p.post_b != nullptr, [&](int c) { return par.one(p.post_b, c); });
+  par.stage(2, has_post_b, [&](int c) { return par.one(p.post_b, c); });
   par.stage(3, pre, [&](int c) { return par.one(p.pre_w, c); });
   if (!kWide) __syncthreads();
   for (int64_t r0 = int64_t(blockIdx.x) * blockDim.y; r0 < p.rows; r0 += step, r += step) {
     const bool row = r < p.rows;
     in.wait();
     Ch t = {}, h = {}, dy = {}, f = {}, g = {};
-    if (p.dh != nullptr) t = in.get(0, row);
+    if (has_dh) t = in.get(0, row);
     if (pre) {
       h = in.get(1, row);
       dy = in.get(2, row);
     }
-    if (p.f != nullptr) f = in.get(3, row);
-    if (p.gate != nullptr) g = in.get(4, row);
+    if (has_f) f = in.get(3, row);
+    if (has_gate) g = in.get(4, row);
     fetch();
     float2 rs = both(1.f);  // of h and of f
     Ch u = f;               // the block's output after its norm
@@ -573,19 +591,19 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
       }
       float v[2] = {dy.total(), dot(dy, h)};
       sum(v);
-      const float a = p.layer ? -v[0] * p.inv_c : 0.f, b = -v[1] * p.inv_c;
+      const float a = layer ? -v[0] * p.inv_c : 0.f, b = -v[1] * p.inv_c;
 #pragma unroll
       for (int i = 0; i < E / 2; ++i)
         t.v[i] = ffma2(both(rs.x), ffma2(h.v[i], both(b), fadd2(dy.v[i], both(a))), t.v[i]);
     }
     dx_out.put(row, at, t);
-    if (p.f != nullptr) {
+    if (has_f) {
       Ch w;
       if (post) {
         w = par.get(1, p.post_w);
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) u.v[i] = fmul2(f.v[i], w.v[i]);
-        if (p.post_b != nullptr) {
+        if (has_post_b) {
           const Ch b = par.get(2, p.post_b);
 #pragma unroll
           for (int i = 0; i < E / 2; ++i) u.v[i] = fadd2(u.v[i], b.v[i]);
@@ -597,16 +615,16 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
       // and so is the weight that t is multiplied with below.
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
-        s.v[i] = p.gate != nullptr ? sigmoid2(g.v[i]) : both(1.f);
+        s.v[i] = has_gate ? sigmoid2(g.v[i]) : both(1.f);
         t.v[i] = fmul2(t.v[i], s.v[i]);
         acc[0].v[i] = ffma2(t.v[i], u.v[i], acc[0].v[i]);
       }
-      if (p.scale != nullptr) {
+      if (has_scale) {
         const Ch sc = par.get(0, p.scale);
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) t.v[i] = fmul2(t.v[i], sc.v[i]);
       }
-      if (p.gate != nullptr) {
+      if (has_gate) {
 #pragma unroll
         for (int i = 0; i < E / 2; ++i)
           g.v[i] = fmul2(fmul2(t.v[i], u.v[i]), fadd2(both(1.f), make_float2(-s.v[i].x, -s.v[i].y)));
@@ -621,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
         }
         float v[2] = {t.total(), dot(t, f)};
         sum(v);
-        const float a = p.layer ? -v[0] * p.inv_c : 0.f, b = -v[1] * p.inv_c;
+        const float a = layer ? -v[0] * p.inv_c : 0.f, b = -v[1] * p.inv_c;
 #pragma unroll
         for (int i = 0; i < E / 2; ++i)
           t.v[i] = fmul2(both(rs.y), ffma2(f.v[i], both(b), fadd2(t.v[i], both(a))));

@@ -185,6 +185,18 @@ def test_every_combination(cuda_device, parts, kind, dtype):
         _check_backward(d, dh, dy, kind, 1e-5)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("parts", [p for p in PARTS if "pre" in p and "scale" not in p], ids=lambda p: "-".join(p))
+def test_sets_of_parts_over_many_rows(cuda_device, parts, kind, dtype):
+    """The sets of parts whose gradients have kernels of their own and the others, with several rows to a thread and a
+    ragged end: rows that share a block, and rows of a block."""
+    for rows, C in ((20001, 64), (1500, 512)):
+        d, dh, dy = _inputs(rows, C, dtype, parts, kind, seed=rows)
+        _check_backward(d, dh, dy, kind, 1e-5)
+
+
 SHAPES = [(1, 1), (1, 8), (7, 100), (300, 128), (33, 256), (5, 257), (9, 384), (2, 768), (3, 1021), (2, 4096),
           (3, 4100), (2, 8192), (1000, 24)]
 
