@@ -349,8 +349,8 @@ typedef struct {
  *   base  [B][H][Nq][Nk] device, desc->dtype, or NULL; may be `out` itself.
  *         The sum is taken in fp32 and rounded once.
  *   out   [B][H][Nq][Nk] device, desc->dtype
- * Rows move as 16-byte words when out (and base) start on 16 bytes and every
- * stride is a multiple of 16 bytes, element by element otherwise.
+ * bf16 rows move as 16-byte words when out (and base) start on 16 bytes and
+ * every stride is a multiple of 16 bytes; others element by element.
  */
 PBA_API pba_status pba_relpos_bias_forward(const pba_relpos_desc *desc, const int32_t *q_pos, const int32_t *k_pos,
                                        const int32_t *q_group, const int32_t *k_group, const void *table,

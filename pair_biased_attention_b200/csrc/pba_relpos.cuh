@@ -114,8 +114,8 @@ __device__ __forceinline__ int relpos_row(const RelposRule &r, const RelposLooku
   return relpos_search(r, look.borders, rel);
 }
 
-// The positions (or groups) of a thread's eight keys, in the order of load8;
-// those past the row as its last key.
+// The positions (or groups) of a thread's eight keys, consecutive (kVec)
+// or every 32nd; those past the row as its last key.
 template <bool kVec>
 __device__ __forceinline__ void load_keys8(const int32_t *p, int c, int Nk, bool vec, int (&k)[8]) {
   if (kVec && vec && c + 8 <= Nk) {
@@ -244,12 +244,15 @@ __global__ void __launch_bounds__(kRelposThreads) relpos_fwd_kernel(const __grid
             for (int i = 0; i < 4; ++i) y[2 * i] = raw.pair(i).x, y[2 * i + 1] = raw.pair(i).y;
             fetch();
           } else {
-            load8<T, false>(base + h * p.base_s[1], n, 32, y);
+            load8<T>(base + h * p.base_s[1], n, 32, y);
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] += y[e];
         }
-        store8<T, kVec>(out + h * p.out_s[1], n, 32, x);
+        if constexpr (kVec)
+          store8_word(out + h * p.out_s[1], n, x);
+        else
+          store8<T>(out + h * p.out_s[1], n, 32, x);
       }
     }
     row += drow;

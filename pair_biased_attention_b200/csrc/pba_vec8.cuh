@@ -21,73 +21,36 @@ struct F32 {
   static __device__ __forceinline__ float from_f32(float x) { return x; }
 };
 
-// 16-byte global accesses marked for first eviction: rows that one launch
-// touches once.
-__device__ __forceinline__ uint4 ld_stream16(const void *p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
+// A 16-byte store that leaves L1 alone: rows that one launch writes once.
 __device__ __forceinline__ void st_stream16(void *p, uint4 v) {
   asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
                : "memory");
 }
 
-__device__ __forceinline__ void unpack8(const uint4 v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[2 * e] = bf16lo_to_f32(w[e]);
-    x[2 * e + 1] = bf16hi_to_f32(w[e]);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
-}
-
-// Eight elements of a row, of which the first n (0 to 8) exist; the others
-// read as 0 and are not written.  kVec: p[0 .. 8) on a 16-byte boundary, whole
-// eights moved as 16-byte words (a shorter one element by element, so that it
-// never touches what lies behind it).  Otherwise p[0], p[step], p[2 step], ...:
-// neighbouring threads then take neighbouring elements, which keeps accesses
-// coalesced on rows that start anywhere.
-template <typename T, bool kVec>
+// Eight elements of a row, p[0], p[step], p[2 step], ..., of which the first n
+// (0 to 8) exist; the others read as 0 and are not written.  Neighbouring
+// threads take neighbouring elements, which keeps accesses coalesced on rows
+// that start anywhere.
+template <typename T>
 __device__ __forceinline__ void load8(const typename T::Word *p, int n, int step, float (&x)[8]) {
-  if (kVec && n >= 8) {
-    if (sizeof(typename T::Word) == 2) {
-      unpack8(ld_stream16(p), x);
-    } else {
-      const uint4 a = ld_stream16(p), b = ld_stream16(p + 4);
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(w[e]);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = e < n ? T::to_f32(p[kVec ? e : e * step]) : 0.f;
-  }
+  for (int e = 0; e < 8; ++e) x[e] = e < n ? T::to_f32(p[e * step]) : 0.f;
 }
-
-template <typename T, bool kVec>
+template <typename T>
 __device__ __forceinline__ void store8(typename T::Word *p, int n, int step, const float (&x)[8]) {
-  if (kVec && n >= 8) {
-    if (sizeof(typename T::Word) == 2) {
-      st_stream16(p, pack8(x));
-    } else {
-      st_stream16(p, make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                                __float_as_uint(x[3])));
-      st_stream16(p + 4, make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]),
-                                    __float_as_uint(x[7])));
-    }
-  } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < n) p[kVec ? e : e * step] = T::from_f32(x[e]);
-  }
+  for (int e = 0; e < 8; ++e)
+    if (e < n) p[e * step] = T::from_f32(x[e]);
+}
+// Eight consecutive bf16 on a 16-byte boundary as one word; a shorter eight
+// element by element, so that it never touches what lies behind it.
+__device__ __forceinline__ void store8_word(uint16_t *p, int n, const float (&x)[8]) {
+  if (n >= 8)
+    st_stream16(p, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                              pack_bf16x2(x[6], x[7])));
+  else
+    store8<Bf16>(p, n, 1, x);
 }
 
 // Eight consecutive elements as they lie in memory: packed bf16 pairs, or fp32.
