@@ -11,7 +11,10 @@ Modeling", Table 1 "Attn Pair Bias" / "Triangle Attention", Figure 2):
     O = softmax_keys(tau Q K^T + bias + mask) V,  tau = 1/sqrt(D),
 computed in one pass (pba_forward) or as per-key-block partials (pba_partial)
 combined by the tiled-softmax merge (softmax_merge); triangle attention runs it
-along one axis of a pair tensor (tri_attn_forward).
+along one axis of a pair tensor (tri_attn_forward).  Around the block: the
+relative position bias that goes into it (pba_relpos_bias_forward, _backward),
+the norms, gate and residual on either side (pba_block_norm_*) and cross
+attention to an encoder's states (pba_cross_attn_*).
 """
 from __future__ import annotations
 

@@ -1,7 +1,7 @@
-// pba_vec8.cuh -- eight consecutive elements of a bf16 or fp32 row as fp32
-// registers: the unit of work of the elementwise kernels (relative position
-// bias, block norms).  16-byte accesses when the caller knows the row to be
-// aligned, element by element otherwise and at a ragged row end.
+// pba_vec8.cuh -- eight elements of a bf16 or fp32 row as fp32 registers, the unit
+// of work of the relative position kernels, with their stores and their rings
+// of asynchronous copies; the element types and the 16-byte store are the block
+// norms' too.
 #pragma once
 
 #include <cstdint>
