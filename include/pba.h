@@ -350,7 +350,9 @@ typedef struct {
  *         The sum is taken in fp32 and rounded once.
  *   out   [B][H][Nq][Nk] device, desc->dtype
  * bf16 rows move as 16-byte words when out (and base) start on 16 bytes and
- * every stride is a multiple of 16 bytes; others element by element.
+ * every stride is a multiple of 16 bytes; others element by element.  An out
+ * that goes to pba_forward or pba_partial keeps their alignment rules: bf16 rows
+ * of a ragged Nk lie a multiple of 8 elements apart.
  */
 PBA_API pba_status pba_relpos_bias_forward(const pba_relpos_desc *desc, const int32_t *q_pos, const int32_t *k_pos,
                                        const int32_t *q_group, const int32_t *k_group, const void *table,
