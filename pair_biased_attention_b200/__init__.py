@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -519,6 +520,13 @@ def _empty_as(t, dtype=None):
     return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
 
 
+def _int32(name, value):
+    """A whole number for a descriptor's int32, which would keep the low bits of others."""
+    if not -2 ** 31 <= value < 2 ** 31 or value != int(value):
+        raise ValueError(f"{name} must be a whole number of 32 bits, got {value}")
+    return int(value)
+
+
 _RELPOS_RULES = {"clip": PBA_RELPOS_CLIP, "log": PBA_RELPOS_LOG, "log_causal": PBA_RELPOS_LOG_CAUSAL}
 
 
@@ -549,7 +557,8 @@ def _relpos_desc(rows, H, dtype, q_pos, k_pos, rule, max_distance, q_group, k_gr
             raise ValueError(f"{name} has batch {shape[0]}, another argument has {B}")
         B = shape[0]
         strides.append(stride[0])
-    return PbaRelposDesc(B, H, Nq, Nk, _dtype_code(dtype), kind, rows, int(max_distance), *strides)
+    return PbaRelposDesc(B, H, Nq, Nk, _dtype_code(dtype), kind, _int32("rows", rows),
+                         _int32("max_distance", max_distance), *strides)
 
 
 def _matrix_strides(name, t, shape, dtype):
@@ -616,7 +625,7 @@ def pba_relpos_bias_backward(dbias, q_pos, k_pos, rows, rule="clip", max_distanc
     if dbias.dim() != 4:
         raise ValueError("dbias must be [B,H,Nq,Nk]")
     B, H = dbias.shape[:2]
-    d = _relpos_desc(int(rows), H, dbias.dtype, q_pos, k_pos, rule, max_distance, q_group, k_group, B)
+    d = _relpos_desc(rows, H, dbias.dtype, q_pos, k_pos, rule, max_distance, q_group, k_group, B)
     d.out_stride[:] = _matrix_strides("dbias", dbias, (d.B, H, d.Nq, d.Nk), dbias.dtype)
     lib = load_library()
     need = ctypes.c_int64()
@@ -755,6 +764,8 @@ def _cross_desc(q, k, v, k_len, key_mask, softmax_scale) -> PbaCrossDesc:
         raise ValueError(f"k and v must be {q.dtype}, got {k.dtype} and {v.dtype}")
     d = PbaCrossDesc(B, H, Hkv, Nq, Nk, D, _dtype_code(q.dtype), softmax_scale or 0.0, _bhn("q", q), _bhn("k", k),
                      _bhn("v", v))
+    if softmax_scale and (d.softmax_scale == 0 or math.isinf(d.softmax_scale) and not math.isinf(softmax_scale)):
+        raise ValueError(f"softmax_scale {softmax_scale} lies outside fp32")  # (0 would select 1/sqrt(D))
     if k_len is not None and (k_len.dtype != torch.int32 or k_len.dim() != 1 or k_len.shape[0] != B or
                               not k_len.is_contiguous()):
         raise ValueError(f"k_len must be a contiguous [{B}] int32 tensor")
