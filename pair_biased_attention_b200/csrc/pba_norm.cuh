@@ -391,6 +391,17 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
   const float2 d = fadd2(make_float2(ex2_approx(a.x), ex2_approx(a.y)), both(1.f));
   return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
+// The same and its complement 1 - sigmoid, which for positive x is the
+// exponential times the sigmoid: a difference would lose it next to 1 (at x = 8
+// a thousandth of it, from 17 on all).
+__device__ __forceinline__ float2 sigmoid2(float2 x, float2 &complement) {
+  const float2 a = fmul2(x, both(-1.4426950408889634f));
+  const float2 e = make_float2(ex2_approx(a.x), ex2_approx(a.y)), d = fadd2(e, both(1.f));
+  const float2 s = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  const float2 product = fmul2(e, s), difference = fadd2(both(1.f), make_float2(-s.x, -s.y));
+  complement = make_float2(x.x > 0.f ? product.x : difference.x, x.y > 0.f ? product.y : difference.y);
+  return s;
+}
 
 template <int kThreads>
 __host__ __device__ constexpr int norm_fwd_stages() {
@@ -609,13 +620,13 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
           for (int i = 0; i < E / 2; ++i) u.v[i] = fadd2(u.v[i], b.v[i]);
         }
       }
-      Ch s;  // sigmoid(gate)
+      Ch s;  // sigmoid(gate); g becomes 1 - sigmoid(gate)
       // A row past the end is all zeros here: its t, dy and h are.  Channels
       // past the end of a row may hold the mean's share in t; u is 0 there,
       // and so is the weight that t is multiplied with below.
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
-        s.v[i] = has_gate ? sigmoid2(g.v[i]) : both(1.f);
+        s.v[i] = has_gate ? sigmoid2(g.v[i], g.v[i]) : both(1.f);
         t.v[i] = fmul2(t.v[i], s.v[i]);
         acc[0].v[i] = ffma2(t.v[i], u.v[i], acc[0].v[i]);
       }
@@ -627,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
       if (has_gate) {
 #pragma unroll
         for (int i = 0; i < E / 2; ++i)
-          g.v[i] = fmul2(fmul2(t.v[i], u.v[i]), fadd2(both(1.f), make_float2(-s.v[i].x, -s.v[i].y)));
+          g.v[i] = fmul2(fmul2(t.v[i], u.v[i]), g.v[i]);
         dg_out.put(row, at, g);
       }
       if (post) {
