@@ -425,8 +425,9 @@ PBA_API pba_status pba_block_norm_forward(const pba_norm_desc *desc, const void 
  *   dx     dL/dx (= dL/dh through both paths); may be dh or dy itself
  *   df, dgate   required with f and with gate; may be f and gate themselves
  *   dscale, dpost_w, dpost_b, dpre_w, dpre_b [C] float, each or NULL: sums over
- *     the rows, taken in fp32 over a thread's rows and in 64 bits beyond, in a
- *     fixed order; not written when their parameter is NULL
+ *     the rows, taken in fp32 over at most 512 rows and in 64 bits beyond (a
+ *     block's share is kept as fp32), in a fixed order; not written when their
+ *     parameter is NULL
  *   workspace  as for pba_relpos_bias_backward, 4-byte aligned
  */
 PBA_API pba_status pba_block_norm_backward_workspace(const pba_norm_desc *desc, int64_t *bytes);

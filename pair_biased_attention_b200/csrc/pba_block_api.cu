@@ -221,10 +221,13 @@ int norm_channels(int dtype, bool backward) {
 }
 
 // Blocks of a launch: 512 threads to an SM, which is what the kernels'
-// registers leave room for, each walking over its share of the rows.
-int64_t norm_blocks(int64_t rows, dim3 block) {
+// registers leave room for, each walking over its share of the rows; for the
+// gradients so many times over that no thread's sums pass kNormMaxThreadRows.
+int64_t norm_blocks(int64_t rows, dim3 block, bool backward) {
   const int64_t per_sm = std::max<int64_t>(1, 512 / (int64_t(block.x) * block.y));
-  return std::max<int64_t>(1, std::min(ceil_div(rows, block.y), kPlanSms * per_sm));
+  int64_t full = kPlanSms * per_sm;
+  if (backward) full *= std::max<int64_t>(1, ceil_div(rows, full * block.y * pba::kNormMaxThreadRows));
+  return std::max<int64_t>(1, std::min(ceil_div(rows, block.y), full));
 }
 
 bool norm_vec(const pba_norm_desc *d, const void *const *rows, const int64_t *strides, int n_rows,
@@ -290,7 +293,7 @@ cudaError_t launch_norm(const pba::NormParams &p, bool backward, unsigned grid, 
 
 cudaError_t dispatch_norm(const pba::NormParams &p, int dtype, bool vec, bool backward, cudaStream_t st) {
   const dim3 block = norm_block(p.C, norm_channels(dtype, backward));
-  const unsigned grid = unsigned(norm_blocks(p.rows, block));
+  const unsigned grid = unsigned(norm_blocks(p.rows, block, backward));
   if (dtype == PBA_BF16)
     return vec ? launch_norm<pba::Bf16, true>(p, backward, grid, block, st)
                : launch_norm<pba::Bf16, false>(p, backward, grid, block, st);
@@ -448,7 +451,7 @@ pba_status pba_block_norm_backward_workspace(const pba_norm_desc *desc, int64_t 
   if (desc == nullptr || bytes == nullptr || desc->rows < 0 || desc->C < 1) return PBA_ERR_INVALID_ARG;
   if (desc->C > pba::kNormMaxC) return PBA_ERR_UNSUPPORTED;
   const int64_t blocks =
-      desc->rows == 0 ? 0 : norm_blocks(desc->rows, norm_block(desc->C, norm_channels(desc->dtype, true)));
+      desc->rows == 0 ? 0 : norm_blocks(desc->rows, norm_block(desc->C, norm_channels(desc->dtype, true)), true);
   *bytes = blocks * pba::kNormParams * desc->C * 4;
   return PBA_OK;
 }
@@ -490,7 +493,7 @@ pba_status pba_block_norm_backward(const pba_norm_desc *desc, const void *h, con
     if (!aligned_to(o, 4)) return PBA_ERR_INVALID_ARG;
     any = any || o != nullptr;
   }
-  const int64_t blocks = d.rows == 0 ? 0 : norm_blocks(d.rows, norm_block(d.C, norm_channels(d.dtype, true)));
+  const int64_t blocks = d.rows == 0 ? 0 : norm_blocks(d.rows, norm_block(d.C, norm_channels(d.dtype, true)), true);
   if (!aligned_to(workspace, 4) || workspace_bytes < blocks * pba::kNormParams * d.C * 4) return PBA_ERR_INVALID_ARG;
   s = check_device();
   if (s != PBA_OK) return s;

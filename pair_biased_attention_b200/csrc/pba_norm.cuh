@@ -28,6 +28,8 @@
 // 4.2 TB/s forward and backward, with all parts 2.3 and 3.2.
 #pragma once
 
+#include <cfloat>
+
 #include "pba_vec8.cuh"
 
 namespace pba {
@@ -35,6 +37,7 @@ namespace pba {
 constexpr int kNormMaxC = 8192;
 constexpr int kNormNarrowThreads = 256;
 constexpr int kNormParams = 5;  // dscale, dpost_w, dpost_b, dpre_w, dpre_b
+constexpr int kNormMaxThreadRows = 512;  // backward: rows that a thread adds up in fp32
 
 struct NormParams {
   int64_t rows;
@@ -391,15 +394,15 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
   const float2 d = fadd2(make_float2(ex2_approx(a.x), ex2_approx(a.y)), both(1.f));
   return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
-// The same and its complement 1 - sigmoid, which for positive x is the
-// exponential times the sigmoid: a difference would lose it next to 1 (at x = 8
-// a thousandth of it, from 17 on all).
+// The same and its complement 1 - sigmoid, as the exponential times the sigmoid: a
+// difference would lose it next to 1 (at x = 8 a thousandth of it, from 17 on
+// all).  Where the sigmoid is 0 the complement comes out as 0 too, not as 1: it is
+// only used times the sigmoid.
 __device__ __forceinline__ float2 sigmoid2(float2 x, float2 &complement) {
   const float2 a = fmul2(x, both(-1.4426950408889634f));
   const float2 e = make_float2(ex2_approx(a.x), ex2_approx(a.y)), d = fadd2(e, both(1.f));
   const float2 s = make_float2(rcp_approx(d.x), rcp_approx(d.y));
-  const float2 product = fmul2(e, s), difference = fadd2(both(1.f), make_float2(-s.x, -s.y));
-  complement = make_float2(x.x > 0.f ? product.x : difference.x, x.y > 0.f ? product.y : difference.y);
+  complement = fmul2(s, make_float2(fminf(e.x, FLT_MAX), fminf(e.y, FLT_MAX)));
   return s;
 }
 
@@ -502,8 +505,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
 //     dscale = sum over rows of sigmoid(gate) u t, and through each norm
 //     dv = (w dv' - mean(w dv') - v mean(w dv' v)) / rms   (mean only for layer norm)
 // The statistics are taken again from h and f, which the formulas need
-// anyway.  Sums over rows stay in each thread's registers for its channels,
-// then per block in shared memory, then in `part`, always in the same order.
+// anyway.  Sums over rows stay in each thread's registers for its channels, at
+// most kNormMaxThreadRows rows long in fp32; a block's rows are joined in 64 bits
+// in shared memory, and its share, rounded to fp32 once, goes to `part`, always in
+// the same order.
 template <typename T, int kThreads>
 __host__ __device__ constexpr int norm_bwd_stages() {
   return (kThreads == 1024 ? 4 : 8) / int(sizeof(typename T::Word));
@@ -658,29 +663,31 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
       df_out.put(row, at, t);
     }
   }
-  // the block's sums: its rows' threads of a channel added in order
+  // The block's sums.  Rows that share it: all its threads join, each eight rows of
+  // one channel in 64 bits, then the neighbouring lanes of the channel.
 #pragma unroll
   for (int k = 0; k < kNormParams; ++k) {
     float *dst = p.part + (int64_t(blockIdx.x) * kNormParams + k) * p.C;
-    if (!kWide) {
-      __syncthreads();
-      float *mine = buf + (threadIdx.y * blockDim.x + threadIdx.x) * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) mine[e] = acc[k].at(e);
-      __syncthreads();
-      if (threadIdx.y == 0) {
-        acc[k] = Ch{};
-        for (int y = 0; y < int(blockDim.y); ++y) {
-          const float *o = buf + (y * blockDim.x + threadIdx.x) * E;
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[k].at(e) += o[e];
-        }
-      }
-    }
-    if (kWide || threadIdx.y == 0) {
+    if (kWide) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (at.has(e)) dst[at.channel(e)] = acc[k].at(e);
+    } else {
+      __syncthreads();
+      const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+#pragma unroll
+      for (int e = 0; e < E; ++e) buf[tid * E + e] = acc[k].at(e);
+      __syncthreads();
+      const int lanes = blockDim.x, per = 32 / lanes;  // blockDim.y = 8 per
+      const int i = tid / per, first = tid & (per - 1);  // the row's channel number i, by place
+      double s = 0.0;
+#pragma unroll
+      for (int y = 0; y < kNormNarrowThreads / 32; ++y) s += double(buf[(first + y * per) * lanes * E + i]);
+      for (int o = per / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      Place<kVec, E, G> there(p.C);
+      there.t = i / E;
+      const int c = there.channel(i % E);
+      if (first == 0 && c < p.C) dst[c] = float(s);
     }
   }
 }
