@@ -366,9 +366,10 @@ PBA_API pba_status pba_relpos_bias_forward(const pba_relpos_desc *desc, const in
  *   workspace  device, 4-byte aligned, at least as many bytes as
  *           pba_relpos_bias_backward_workspace gives; nothing in it is read before
  *           it is written, and two calls that may overlap need two of them
- * (The gradient of base is dbias itself.)  Sums are taken in fp32 over at
- * most a few thousand terms each and in 64 bits beyond, always in the same
- * order: the same call gives the same bits.
+ * (The gradient of base is dbias itself.)  Sums are taken in fp32 over a
+ * thread's pairs, at most 4096 of a row one after the other, and by at most
+ * eight more additions over a block's threads; beyond the blocks in 64 bits.
+ * The order is always the same: the same call gives the same bits.
  */
 PBA_API pba_status pba_relpos_bias_backward_workspace(const pba_relpos_desc *desc, int64_t *bytes);
 PBA_API pba_status pba_relpos_bias_backward(const pba_relpos_desc *desc, const int32_t *q_pos, const int32_t *k_pos,

@@ -274,8 +274,9 @@ __global__ void __launch_bounds__(kRelposThreads) relpos_fwd_kernel(const __grid
 // values added one by one, into the thread's own column of a table in shared
 // memory; a block's queries lie row_splits apart, so that every block meets its
 // share of the diagonal.  No two threads add to the same word, and the order of
-// every sum is fixed.  The columns are added at the end of the block, the
-// blocks' tables by relpos_grad_sum_kernel.
+// every sum is fixed.  The columns are added at the end of the block, in fp32 (in
+// 64 bits that took 3 to 15 % of the call, for eight additions next to a thread's
+// 4096), the blocks' tables by relpos_grad_sum_kernel in 64 bits.
 // Measured at 4096 x 4096 x 16 heads, bf16, 66 rows with two chains: 151 us,
 // 3.6 TB/s, a little over half of HBM's rate.  Some 80 instructions per eight
 // elements, a tenth of them near the diagonal, are what bounds it, with four

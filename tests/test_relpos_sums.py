@@ -1,0 +1,26 @@
+"""The table's gradient takes every pair once."""
+import pytest
+import torch
+
+import block_ref as R
+import pair_biased_attention_b200 as pba
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("pad", [0, 3])  # rows on 16 bytes, and not
+@pytest.mark.parametrize("B,H,Nq,Nk,rule,buckets,far,groups", [
+    (1, 2, 1500, 264, "clip", 33, 0, True), (2, 1, 700, 1031, "log", 32, 128, False), (1, 3, 513, 40, "log_causal", 16, 64, True),
+    (1, 1, 4100, 9, "clip", 1, 0, False), (3, 2, 65, 2000, "log", 64, 1024, True)])
+def test_whole_numbers_are_exact(cuda_device, B, H, Nq, Nk, rule, buckets, far, groups, pad, dtype):
+    """Sums below 2^24 come out exactly in any order: a pair left out or taken twice shows."""
+    g = torch.Generator().manual_seed(Nq)
+    q, k = (torch.randint(0, 1500, (B, n), generator=g, dtype=torch.int32).sort(-1)[0] for n in (Nq, Nk))
+    qg, kg = ((torch.arange(n) * 3 // n).int().expand(B, n).contiguous() if groups else None for n in (Nq, Nk))
+    rows = buckets + groups
+    wide = torch.randint(-8, 9, (B, H, Nq, Nk + 13 - (Nk + 13) % 8 + 8), generator=g).to(dtype).cuda()
+    dbias = wide[..., pad:pad + Nk]
+    ref, _ = R.relpos_table_grad(dbias, R.relpos_rows(q, k, rows, rule, far, qg, kg), rows)
+    got = pba.pba_relpos_bias_backward(dbias, *[None if t is None else t.cuda() for t in (q, k)], rows, rule, far,
+                                       *[None if t is None else t.cuda() for t in (qg, kg)])
+    assert torch.equal(got.double().cpu(), ref)
