@@ -375,7 +375,9 @@ pba_status pba_relpos_bias_backward_workspace(const pba_relpos_desc *desc, int64
   if (s != PBA_OK) s = check_relpos(desc, true);
   if (s != PBA_OK) return s;
   if (bytes == nullptr) return PBA_ERR_INVALID_ARG;
-  *bytes = desc->Nq == 0 || desc->Nk == 0 ? 0 : grad_plan(desc).splits * desc->H * desc->rows * 4;
+  const int64_t splits = desc->Nq == 0 || desc->Nk == 0 ? 0 : grad_plan(desc).splits;
+  if (splits > kMaxI32) return PBA_ERR_INVALID_ARG;  // as the backward itself
+  *bytes = splits * desc->H * desc->rows * 4;
   return PBA_OK;
 }
 

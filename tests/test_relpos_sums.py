@@ -1,4 +1,7 @@
-"""The table's gradient takes every pair once."""
+"""The table's gradient takes every pair once, and its workspace is asked for
+within the call's limits."""
+import ctypes
+
 import pytest
 import torch
 
@@ -24,3 +27,16 @@ def test_whole_numbers_are_exact(cuda_device, B, H, Nq, Nk, rule, buckets, far, 
     got = pba.pba_relpos_bias_backward(dbias, *[None if t is None else t.cuda() for t in (q, k)], rows, rule, far,
                                        *[None if t is None else t.cuda() for t in (qg, kg)])
     assert torch.equal(got.double().cpu(), ref)
+
+
+def test_workspace_of_a_problem_beyond_the_limits():
+    """Where the number of partial tables passes 31 bits the backward refuses the call, and so does the question for its
+    workspace, whose bytes would pass 64."""
+    lib = pba.load_library()
+    d = pba.PbaRelposDesc()
+    d.B, d.H, d.Nq, d.Nk, d.dtype, d.rows = 65535, 65535, 32000, 2 ** 31 - 2 ** 21, pba.PBA_BF16, 1025
+    need = ctypes.c_int64()
+    assert lib.pba_relpos_bias_backward_workspace(ctypes.byref(d), ctypes.byref(need)) == pba.PBA_ERR_INVALID_ARG
+    d.B = d.H = 1
+    d.Nk = 4096
+    assert lib.pba_relpos_bias_backward_workspace(ctypes.byref(d), ctypes.byref(need)) == pba.PBA_OK and need.value > 0
