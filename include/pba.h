@@ -332,7 +332,8 @@ typedef enum { PBA_RELPOS_CLIP = 0, PBA_RELPOS_LOG = 1, PBA_RELPOS_LOG_CAUSAL = 
  *   *_pos_stride_b, *_group_stride_b   batch strides of the int32 arrays
  *                  (token stride 1); 0 shares one row with every b
  *   base_stride, out_stride            (b, h, query row) in elements, key
- *                  stride 1 (backward: out_stride is dbias's)
+ *                  stride 1 (backward: out_stride is dbias's); out's not 0 on an
+ *                  axis longer than 1, the others may be
  */
 typedef struct {
   int64_t B, H, Nq, Nk;
@@ -395,7 +396,8 @@ typedef enum { PBA_NORM_LAYER = 0, PBA_NORM_RMS = 1 } pba_norm_kind;
  *   dtype        of x, f, gate, h, y and their gradients
  *   param_dtype  of scale, post_w, post_b, pre_w, pre_b
  *   eps          at least 1e-30
- *   *_stride     row strides in elements, channel stride 1
+ *   *_stride     row strides in elements, channel stride 1; 0 shares one row of
+ *                an input with all rows (outputs: only where rows is 1)
  * Rows move as 16-byte words when every row base and parameter starts on 16
  * bytes and every stride is a multiple of 16 bytes, else element by element.
  */
@@ -451,7 +453,8 @@ PBA_API pba_status pba_block_norm_backward(const pba_norm_desc *desc, const void
  *   softmax_scale  tau; 0 selects 1/sqrt(D)
  *   *_stride       (b, h, n) in elements, feature stride 1.  q, k, v, dout:
  *                  positive multiples of 8 where the axis is longer than 1;
- *                  out: multiples of 8; lse: any
+ *                  out: multiples of 8; lse: any; neither 0 on an axis longer
+ *                  than 1 in the forward, which writes them
  *   mask_stride_b  row stride of key_mask [B][Nk] (key stride 1)
  * Few query rows per key head (a decoder's new tokens) run on kernels that
  * split the keys over the card; the result does not depend on the choice

@@ -7,6 +7,8 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
+#include <utility>
 
 #include "pba.h"
 #include "pba_host.cuh"
@@ -241,6 +243,13 @@ bool norm_vec(const pba_norm_desc *d, const void *const *rows, const int64_t *st
   return true;
 }
 
+// Outputs (null ones aside) whose rows lie on one another.
+bool norm_rows_overlap(const pba_norm_desc &d, std::initializer_list<std::pair<const void *, int64_t>> outputs) {
+  for (const auto &o : outputs)
+    if (o.first != nullptr && d.rows > 1 && o.second == 0) return true;
+  return false;
+}
+
 template <typename K>
 cudaError_t start_norm_kernel(K kern, PerDeviceOnce &once, int smem, const pba::NormParams &p, unsigned grid,
                               dim3 block, cudaStream_t st) {
@@ -332,7 +341,8 @@ pba_status pba_relpos_bias_forward(const pba_relpos_desc *desc, const int32_t *q
   if (q_pos == nullptr || k_pos == nullptr || table == nullptr || out == nullptr) return PBA_ERR_INVALID_ARG;
   const int size = dtype_size(d.dtype);
   if (!aligned_to(q_pos, 4) || !aligned_to(k_pos, 4) || !aligned_to(q_group, 4) || !aligned_to(k_group, 4) ||
-      !aligned_to(table, size) || !aligned_to(base, size) || !aligned_to(out, size))
+      !aligned_to(table, size) || !aligned_to(base, size) || !aligned_to(out, size) ||
+      !rows_apart(d.out_stride, d.B, d.H, d.Nq))
     return PBA_ERR_INVALID_ARG;
   s = check_device();
   if (s != PBA_OK) return s;
@@ -439,6 +449,7 @@ pba_status pba_block_norm_forward(const pba_norm_desc *desc, const void *x, cons
     if (!aligned_to(r, dtype_size(d.dtype))) return PBA_ERR_INVALID_ARG;
   for (const void *r : params)
     if (!aligned_to(r, dtype_size(d.param_dtype))) return PBA_ERR_INVALID_ARG;
+  if (norm_rows_overlap(d, {{h, d.h_stride}, {y, d.y_stride}})) return PBA_ERR_INVALID_ARG;
   s = check_device();
   if (s != PBA_OK) return s;
   pba::NormParams p;
@@ -483,6 +494,7 @@ pba_status pba_block_norm_backward(const pba_norm_desc *desc, const void *h, con
     if (!aligned_to(r, dtype_size(d.dtype))) return PBA_ERR_INVALID_ARG;
   for (const void *r : params)
     if (!aligned_to(r, dtype_size(d.param_dtype))) return PBA_ERR_INVALID_ARG;
+  if (norm_rows_overlap(d, {{dx, d.dx_stride}, {df, d.df_stride}, {dgate, d.dgate_stride}})) return PBA_ERR_INVALID_ARG;
   pba::NormSumParams sp;
   std::memset(&sp, 0, sizeof(sp));
   sp.out[0] = scale != nullptr ? dscale : nullptr;

@@ -284,7 +284,8 @@ pba_status pba_cross_attn_forward(const pba_cross_desc *desc, const void *q, con
   s = check_cross_inputs(d, q, k, v, k_len);
   if (s != PBA_OK) return s;
   if (out == nullptr || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 ||
-      !rows_ok(d.out_stride, d.B, d.H, d.Nq))
+      !rows_ok(d.out_stride, d.B, d.H, d.Nq) || !rows_apart(d.out_stride, d.B, d.H, d.Nq) ||
+      (lse != nullptr && !rows_apart(d.lse_stride, d.B, d.H, d.Nq)))
     return PBA_ERR_INVALID_ARG;
   s = check_device();
   if (s != PBA_OK) return s;

@@ -81,6 +81,12 @@ inline bool make_map(CUtensorMap *map, const void *base, const uint64_t dims[4],
 inline bool stride_ok_bf16(int64_t s, int64_t extent) { return extent <= 1 || (s > 0 && s % 8 == 0); }
 inline bool stride_ok_f32(int64_t s, int64_t extent) { return extent <= 1 || (s > 0 && s % 4 == 0); }
 
+// An output's (b, h, row) strides: 0 on an axis longer than 1 would write several
+// rows to one place.
+inline bool rows_apart(const int64_t s[3], int64_t B, int64_t H, int64_t N) {
+  return (B <= 1 || s[0] != 0) && (H <= 1 || s[1] != 0) && (N <= 1 || s[2] != 0);
+}
+
 // Whether the current device is one that the kernels were built for (sm_100a).
 inline pba_status check_device() {
   static PerDeviceOnce once;
