@@ -266,9 +266,14 @@ cudaError_t start_norm(const pba::NormParams &p, bool backward, unsigned grid, d
   using Fwd = pba::NormFwdStream<T, kVec, kThreads>;
   using Bwd = pba::NormBwdStream<T, kVec, kThreads>;
   static_assert(kThreads * Fwd::kThreadBytes <= kNormSmem && kThreads * Bwd::kThreadBytes <= kNormSmem, "ring");
-  if (!backward)
-    return start_norm_kernel(pba::block_norm_fwd_kernel<T, kVec, kThreads>, once[0], threads * Fwd::kThreadBytes, p,
-                             grid, block, st);
+  if (!backward) {
+    // bf16 rows forward, 16 channels to a thread, need 512 threads at most
+    if constexpr (kThreads == 1024 && pba::kNormMaxC / pba::norm_fwd_channels<T>() <= 512)
+      return cudaErrorInvalidConfiguration;
+    else
+      return start_norm_kernel(pba::block_norm_fwd_kernel<T, kVec, kThreads>, once[0], threads * Fwd::kThreadBytes, p,
+                               grid, block, st);
+  }
   const int smem = threads * Bwd::kThreadBytes;
   if constexpr (kVec && kThreads <= 512) {
     // the sets of parts that have a kernel of their own

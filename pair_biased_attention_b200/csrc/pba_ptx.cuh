@@ -166,10 +166,6 @@ __device__ __forceinline__ void cp_async16_part(void *dst_smem, const void *src,
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst_smem)), "l"(src), "r"(bytes)
                : "memory");
 }
-// 4 bytes (both addresses 4-byte aligned).
-__device__ __forceinline__ void cp_async4(void *dst_smem, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst_smem)), "l"(src) : "memory");
-}
 // Waits until at most N committed copy groups of this thread are under way.
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
