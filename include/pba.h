@@ -456,9 +456,10 @@ PBA_API pba_status pba_block_norm_backward(const pba_norm_desc *desc, const void
  *                  out: multiples of 8; lse: any; neither 0 on an axis longer
  *                  than 1 in the forward, which writes them
  *   mask_stride_b  row stride of key_mask [B][Nk] (key stride 1)
- * Few query rows per key head (a decoder's new tokens) run on kernels that
- * split the keys over the card; the result does not depend on the choice
- * beyond rounding, and every call gives the same bits again.
+ * Few query rows per key head (a decoder's new tokens) run on a kernel in which
+ * up to eight blocks share the keys of 16 rows; the result does not depend on the
+ * choice beyond rounding, and every call gives the same bits again on the same
+ * device.
  */
 typedef struct {
   int64_t B, H, Hkv, Nq, Nk, D;

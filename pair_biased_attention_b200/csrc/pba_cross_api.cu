@@ -81,49 +81,98 @@ cudaError_t set_up(K kern, int smem) {
   return e;
 }
 
-// `splits` > 1: clusters of that many blocks.
-template <typename K, typename P>
-cudaError_t launch_clusters(K kern, const P &p, int64_t grid, int threads, int splits, int smem, cudaStream_t stream) {
+// A launch in clusters of `splits` blocks.
+struct ClusterLaunch {
   cudaLaunchAttribute cluster;
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = unsigned(splits), cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(unsigned(grid));
-  cfg.blockDim = dim3(unsigned(threads));
-  cfg.dynamicSmemBytes = size_t(smem);
-  cfg.stream = stream;
-  cfg.attrs = &cluster;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  ClusterLaunch(int64_t grid, int threads, int splits, int smem, cudaStream_t stream) {
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = unsigned(splits), cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = stream;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = 1;
+  }
+  ClusterLaunch(const ClusterLaunch &) = delete;  // cfg points at cluster
+};
+
+// Clusters of 1 to kXMaxSplits blocks of a kernel that the current device holds
+// at once: [blocks].  A cluster lies within one of the chip's groups of SMs, whose
+// sizes differ, so this is less than the SMs' number divided (for one block an SM
+// 15 clusters of eight on 148 SMs, 33 of four), and a cluster more waits for a
+// whole round of the others.
+struct ClusterRoom {
+  PerDeviceOnce once;
+  int room[kMaxDevices][pba::kXMaxSplits + 1] = {};
+};
+template <typename K, typename F>
+cudaError_t cluster_room(ClusterRoom &r, K kern, int threads, int smem, F &&set_up_kernel, const int *&room) {
+  const cudaError_t e = once_per_device(r.once, [&]() -> cudaError_t {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = set_up_kernel();
+    for (int n = 1; n <= pba::kXMaxSplits && err == cudaSuccess; ++n) {
+      ClusterLaunch c(n, threads, n, smem, nullptr);
+      err = cudaOccupancyMaxActiveClusters(&r.room[dev][n], kern, &c.cfg);
+    }
+    return err;
+  });
+  if (e != cudaSuccess) return e;
+  int dev = 0;
+  const cudaError_t err = cudaGetDevice(&dev);
+  room = r.room[dev];
+  return err;
+}
+
+template <int D>
+cudaError_t tile_room(const int *&room) {
+  static ClusterRoom r;
+  constexpr int smem = pba::CrossLayout<D>::kSmemAlloc;
+  auto kern = pba::pba_cross_sm100_kernel<D, true>;
+  return cluster_room(r, kern, pba::kXThreads, smem, [&] { return set_up(kern, smem); }, room);
+}
+
+template <int D>
+cudaError_t split_room(const int *&room) {
+  static ClusterRoom r;
+  constexpr int smem = pba::cross_split_smem<D>();
+  auto kern = pba::pba_cross_split_kernel<D>;
+  return cluster_room(
+      r, kern, pba::kXsThreads, smem,
+      [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); }, room);
 }
 
 template <int D, bool kShared>
 cudaError_t launch_cross(const pba::CrossParams &p, int64_t grid, cudaStream_t stream) {
   auto kern = pba::pba_cross_sm100_kernel<D, kShared>;
   constexpr int smem = pba::CrossLayout<D>::kSmemAlloc;
+  if (kShared) {  // set up by tile_room
+    ClusterLaunch c(grid, pba::kXThreads, p.splits, smem, stream);
+    return cudaLaunchKernelEx(&c.cfg, kern, p);
+  }
   static PerDeviceOnce once;
   const cudaError_t err = once_per_device(once, [&] { return set_up(kern, smem); });
   if (err != cudaSuccess) return err;
-  if (kShared) return launch_clusters(kern, p, grid, pba::kXThreads, p.splits, smem, stream);
   kern<<<unsigned(grid), pba::kXThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
-// CTAs that share a unit of the tile kernel where there are fewer units than
-// SMs: a power of two (the join shares out 256 rows) such that the clusters
-// find room (a cluster lies within one of the chip's groups of SMs, so not all
-// SMs can be in one) and each CTA has two key tiles at least.
-int tile_splits(const pba_cross_desc &d, int64_t units) {
+// CTAs that share a unit of the tile kernel: as many as the device holds clusters
+// of for all units, a power of two (the join shares out 256 rows), each with two
+// key tiles at least.
+int tile_splits(const pba_cross_desc &d, int64_t units, const int *room) {
   const int64_t tiles = ceil_div(d.Nk, pba::kXTile);
   int s = 1;
-  while (s < pba::kXMaxSplits && units * s * 2 <= 132 && tiles >= s * 4) s *= 2;
+  while (s < pba::kXMaxSplits && units <= room[2 * s] && tiles >= s * 4) s *= 2;
   return s;
 }
 
 template <int D>
 pba_status run_tiles(const pba_cross_desc &d, const void *q, const void *k, const void *v, const int32_t *k_len,
-                     const uint8_t *mask, void *out, float *lse, cudaStream_t stream) {
+                     const uint8_t *mask, void *out, float *lse, const int *room, cudaStream_t stream) {
   pba::CrossParams p;
   std::memset(&p, 0, sizeof(p));
   if (!cross_map(&p.tm_q, q, D, d.Nq, d.H, d.B, d.q_stride)) return PBA_ERR_INVALID_ARG;
@@ -147,23 +196,25 @@ pba_status run_tiles(const pba_cross_desc &d, const void *q, const void *k, cons
   const int sms = sm_count();
   if (p.err == nullptr || sms < 1) return PBA_ERR_CUDA;
   p.timeout_ns = wait_timeout_ns();
-  p.splits = tile_splits(d, n_units);
+  p.splits = tile_splits(d, n_units, room);
   // persistent, one CTA per SM, or a cluster for each unit
   const int64_t grid = p.splits > 1 ? n_units * p.splits : std::min<int64_t>(n_units, sms);
   const cudaError_t e = p.splits > 1 ? launch_cross<D, true>(p, grid, stream) : launch_cross<D, false>(p, grid, stream);
   return e == cudaSuccess ? PBA_OK : PBA_ERR_CUDA;
 }
 
-// Blocks that share 16 query rows: as many as the card holds at once, each
-// with at least one step per warp.
-int split_count(const pba_cross_desc &d, int64_t units, int blocks_per_sm) {
-  const int64_t fit = 148 * blocks_per_sm / units, most = ceil_div(d.Nk, pba::kXsWarps * pba::kXsKeys);
-  return int(std::max<int64_t>(1, std::min<int64_t>({pba::kXMaxSplits, fit, most})));
+// Blocks that share 16 query rows: as many, up to a cluster, as the device holds
+// clusters of for all units, each with at least one step per warp.
+int split_count(const pba_cross_desc &d, int64_t units, const int *room) {
+  const int64_t most = std::min<int64_t>(pba::kXMaxSplits, ceil_div(d.Nk, pba::kXsWarps * pba::kXsKeys));
+  int n = 1;
+  while (n < most && units <= room[n + 1]) ++n;
+  return n;
 }
 
 template <int D>
 pba_status run_split(const pba_cross_desc &d, const void *q, const void *k, const void *v, const int32_t *k_len,
-                     const uint8_t *mask, void *out, float *lse, cudaStream_t stream) {
+                     const uint8_t *mask, void *out, float *lse, const int *room, cudaStream_t stream) {
   pba::CrossSplitParams p;
   std::memset(&p, 0, sizeof(p));
   p.B = int(d.B), p.H = int(d.H), p.Hkv = int(d.Hkv), p.group = int(d.H / d.Hkv), p.Nq = int(d.Nq), p.Nk = int(d.Nk);
@@ -180,17 +231,10 @@ pba_status run_split(const pba_cross_desc &d, const void *q, const void *k, cons
   p.lse = lse;
   p.lse_sb = d.lse_stride[0], p.lse_sh = d.lse_stride[1], p.lse_sn = d.lse_stride[2];
   const int64_t units = d.B * d.Hkv * p.row_tiles;
-  const int splits = split_count(d, units, pba::CrossSplitShape<D>::kBlocksPerSm);
+  const int splits = split_count(d, units, room);
   if (units * splits > kMaxI32) return PBA_ERR_INVALID_ARG;
-  auto kern = pba::pba_cross_split_kernel<D>;
-  constexpr int smem = pba::cross_split_smem<D>();
-  static PerDeviceOnce once;
-  if (once_per_device(once, [&] {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      }) != cudaSuccess)
-    return PBA_ERR_CUDA;
-  return launch_clusters(kern, p, units * splits, pba::kXsThreads, splits, smem, stream) == cudaSuccess ? PBA_OK
-                                                                                                        : PBA_ERR_CUDA;
+  ClusterLaunch c(units * splits, pba::kXsThreads, splits, pba::cross_split_smem<D>(), stream);  // set up by split_room
+  return cudaLaunchKernelEx(&c.cfg, pba::pba_cross_split_kernel<D>, p) == cudaSuccess ? PBA_OK : PBA_ERR_CUDA;
 }
 
 // Whether the kernel for few rows is the faster one.  It reads keys and values
@@ -201,13 +245,22 @@ pba_status run_split(const pba_cross_desc &d, const void *q, const void *k, cons
 // against tiles: 4 x 8 heads, 64 x 4096: 20.3 and 23.1 us, 96 x 4096: 34.7 and
 // 23.1; 16 heads on 4, 32 x 8192: 14.3 and 40.7; 4 x 32 heads on 8, D = 128,
 // 32 x 2048: 36.7 and 40.3, 64 x 2048: 70.7 and 40.7.
-bool few_rows(const pba_cross_desc &d) {
+bool few_rows(const pba_cross_desc &d, const int *tiles_room) {
   if (d.H / d.Hkv * d.Nq > kMaxI32 - pba::kXsRows) return false;  // rows of a key head count in 32 bits
   const double read = double(d.B * d.Hkv * ceil_div(d.H / d.Hkv * d.Nq, pba::kXsRows)) * double(d.Nk * d.D) * 4.0;
   const int64_t units = d.B * d.H * ceil_div(d.Nq, pba::kXQTiles * pba::kXTile);
-  const int64_t splits = tile_splits(d, units);
+  const int64_t splits = tile_splits(d, units, tiles_room);
   const int64_t tiles = ceil_div(ceil_div(d.Nk, pba::kXTile), splits) * ceil_div(units * splits, 148);
   return read / 9e6 <= double(tiles) * (d.D == 128 ? 2.2 : 1.45) + 4.0;
+}
+
+template <int D>
+pba_status run_forward(const pba_cross_desc &d, const void *q, const void *k, const void *v, const int32_t *k_len,
+                       const uint8_t *mask, void *out, float *lse, cudaStream_t stream) {
+  const int *tiles = nullptr, *rows = nullptr;
+  if (tile_room<D>(tiles) != cudaSuccess || split_room<D>(rows) != cudaSuccess) return PBA_ERR_CUDA;
+  return few_rows(d, tiles) ? run_split<D>(d, q, k, v, k_len, mask, out, lse, rows, stream)
+                            : run_tiles<D>(d, q, k, v, k_len, mask, out, lse, tiles, stream);
 }
 
 template <int D>
@@ -290,13 +343,9 @@ pba_status pba_cross_attn_forward(const pba_cross_desc *desc, const void *q, con
   s = check_device();
   if (s != PBA_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream_ptr);
-  if (few_rows(d))
-    return d.D == 32   ? run_split<32>(d, q, k, v, k_len, key_mask, out, lse, st)
-           : d.D == 64 ? run_split<64>(d, q, k, v, k_len, key_mask, out, lse, st)
-                       : run_split<128>(d, q, k, v, k_len, key_mask, out, lse, st);
-  return d.D == 32   ? run_tiles<32>(d, q, k, v, k_len, key_mask, out, lse, st)
-         : d.D == 64 ? run_tiles<64>(d, q, k, v, k_len, key_mask, out, lse, st)
-                     : run_tiles<128>(d, q, k, v, k_len, key_mask, out, lse, st);
+  return d.D == 32   ? run_forward<32>(d, q, k, v, k_len, key_mask, out, lse, st)
+         : d.D == 64 ? run_forward<64>(d, q, k, v, k_len, key_mask, out, lse, st)
+                     : run_forward<128>(d, q, k, v, k_len, key_mask, out, lse, st);
 }
 
 pba_status pba_cross_attn_backward(const pba_cross_desc *desc, const void *q, const void *k, const void *v,
