@@ -237,21 +237,46 @@ pba_status run_split(const pba_cross_desc &d, const void *q, const void *k, cons
   return cudaLaunchKernelEx(&c.cfg, pba::pba_cross_split_kernel<D>, p) == cudaSuccess ? PBA_OK : PBA_ERR_CUDA;
 }
 
+// What a call takes on either kernel, in us, from the measurements below: a
+// start, a time per step of a block (or CTA) and, few rows, the rate at which
+// the steps of all blocks read keys and values, from L2 after the first time.
+template <int D>
+struct CrossCost {
+  static constexpr double kRowsStart = D == 32 ? 5.5 : D == 64 ? 6.0 : 7.0, kRowsRound = D == 128 ? 6.0 : 3.0;
+  static constexpr double kRowsStep = D == 32 ? 0.34 : D == 64 ? 0.42 : 0.60;        // four warps, 16 keys each
+  static constexpr double kRowsMbPerUs = D == 32 ? 7.0 : D == 64 ? 9.25 : 8.75;      // TB/s
+  static constexpr double kTileStart = D == 128 ? 7.5 : 5.8, kTile = D == 128 ? 2.06 : 1.44;  // a CTA to a unit
+  static constexpr double kSharedStart = 8.0, kSharedTile = D == 128 ? 2.65 : 1.5;            // clusters
+  static constexpr double kSharedJoin = D == 32 ? 4.0 : D == 64 ? 11.0 : 20.0;                // over their CTAs
+};
+
 // Whether the kernel for few rows is the faster one.  It reads keys and values
-// once for every 16 query rows of a key head, from L2 after the first time, at
-// about 9 TB/s over the card; the tile kernel takes about 1.45 us (2.2 at
-// D = 128) for 128 keys of a unit of 256 rows of one head, however few of them
-// there are, and 4 us more to begin and end.  Measured on either side, few rows
-// against tiles: 4 x 8 heads, 64 x 4096: 20.3 and 23.1 us, 96 x 4096: 34.7 and
-// 23.1; 16 heads on 4, 32 x 8192: 14.3 and 40.7; 4 x 32 heads on 8, D = 128,
-// 32 x 2048: 36.7 and 40.3, 64 x 2048: 70.7 and 40.7.
-bool few_rows(const pba_cross_desc &d, const int *tiles_room) {
+// once for every 16 query rows of a key head; the tile kernel does the work of
+// 256 rows of every head, however few of them there are.  The costs were fitted
+// to both kernels' times at 1515 shapes (1 to 64 key heads in groups of 1 to 8, 1
+// to 512 queries, 512 to 131072 keys, each D); at 1489 of them the faster kernel
+// is chosen, at 1507 one within 5 % of it, at the worst one 9 % behind.  Few rows
+// against tiles: D = 64, 8192 keys, 16 heads of 64 queries 21.7 and 35.6 us, 32
+// heads of 64 34.7 and 36.1, of 128 59.8 and 36.0; D = 32, 2048 keys, 32 heads of
+// 96 13.2 and 15.3; D = 128, 2048 keys, 32 heads of 64 23.0 and 30.0, of 128 37.7
+// and 29.4.
+template <int D>
+bool few_rows(const pba_cross_desc &d, const int *tiles_room, const int *rows_room) {
+  using C = CrossCost<D>;
   if (d.H / d.Hkv * d.Nq > kMaxI32 - pba::kXsRows) return false;  // rows of a key head count in 32 bits
-  const double read = double(d.B * d.Hkv * ceil_div(d.H / d.Hkv * d.Nq, pba::kXsRows)) * double(d.Nk * d.D) * 4.0;
-  const int64_t units = d.B * d.H * ceil_div(d.Nq, pba::kXQTiles * pba::kXTile);
-  const int64_t splits = tile_splits(d, units, tiles_room);
-  const int64_t tiles = ceil_div(ceil_div(d.Nk, pba::kXTile), splits) * ceil_div(units * splits, 148);
-  return read / 9e6 <= double(tiles) * (d.D == 128 ? 2.2 : 1.45) + 4.0;
+  const int64_t r_units = d.B * d.Hkv * ceil_div(d.H / d.Hkv * d.Nq, pba::kXsRows);
+  const int n = split_count(d, r_units, rows_room);
+  const double steps = double(ceil_div(ceil_div(ceil_div(d.Nk, pba::kXsKeys), n), pba::kXsWarps));
+  const double blocks = double(r_units) * n, rounds = std::ceil(blocks / std::max(1, rows_room[1]));
+  const double mb = blocks * steps * (pba::kXsWarps * pba::kXsKeys * D * 4) * 1e-6;
+  const double rows = C::kRowsStart + C::kRowsRound * (rounds - 1.0) +
+                      std::max(rounds * steps * C::kRowsStep, mb / C::kRowsMbPerUs);
+  const int64_t t_units = d.B * d.H * ceil_div(d.Nq, pba::kXQTiles * pba::kXTile);
+  const int s = tile_splits(d, t_units, tiles_room);
+  const double per = double(ceil_div(ceil_div(d.Nk, pba::kXTile), s));
+  const double tiles = s > 1 ? C::kSharedStart + C::kSharedJoin / s + per * C::kSharedTile
+                             : C::kTileStart + std::ceil(double(t_units) / std::max(1, tiles_room[1])) * per * C::kTile;
+  return rows <= tiles;
 }
 
 template <int D>
@@ -259,7 +284,7 @@ pba_status run_forward(const pba_cross_desc &d, const void *q, const void *k, co
                        const uint8_t *mask, void *out, float *lse, cudaStream_t stream) {
   const int *tiles = nullptr, *rows = nullptr;
   if (tile_room<D>(tiles) != cudaSuccess || split_room<D>(rows) != cudaSuccess) return PBA_ERR_CUDA;
-  return few_rows(d, tiles) ? run_split<D>(d, q, k, v, k_len, mask, out, lse, rows, stream)
+  return few_rows<D>(d, tiles, rows) ? run_split<D>(d, q, k, v, k_len, mask, out, lse, rows, stream)
                             : run_tiles<D>(d, q, k, v, k_len, mask, out, lse, tiles, stream);
 }
 
