@@ -29,8 +29,9 @@
  *   - A key takes part if its mask byte is nonzero and its bias is not -inf.
  *     A query row with no such key gets O = 0, lse = -inf (and m = -inf,
  *     l = 0 for partials); never NaN.  Values of K and V must be finite,
- *     masked keys included.  NaN or +inf in the inputs is outside the
- *     contract.
+ *     masked keys included, and NaN or +inf in the inputs is outside the
+ *     contract, unless the entry point says otherwise (pba_cross_attn_forward
+ *     does of keys and values that do not count).
  *   - A pointer may be NULL when the tensor it stands for has no element
  *     (Nq = 0 or Nk = 0); every other required pointer must be non-NULL.
  *   - Return values: PBA_OK when the launch was enqueued.  PBA_ERR_INVALID_ARG
@@ -481,7 +482,8 @@ typedef struct {
  *   key_mask [B][Nk] uint8, device, or NULL
  *   out [B][H][Nq][D] bf16, device, 16-byte aligned; lse [B][H][Nq] float or NULL
  * What keys and values that do not count hold is never used, NaN included.  A
- * query without any key gets out = 0, lse = -inf.
+ * query without any key gets out = 0, lse = -inf.  Sums are fp32; P enters the
+ * product with V as bf16, half a step of 2^-8 of each, and out is rounded once.
  */
 PBA_API pba_status pba_cross_attn_forward(const pba_cross_desc *desc, const void *q, const void *k, const void *v,
                                           const int32_t *k_len, const uint8_t *key_mask, void *out, float *lse,

@@ -783,7 +783,8 @@ def pba_cross_attn_forward(q, k, v, k_len=None, key_mask=None, out=None, lse=Non
     reads key head h // (H // Hkv)).  k_len [B] int32: keys of each sequence;
     key_mask [B,Nk] uint8 (1 = key takes part); either may be None.  Returns
     out [B,H,Nq,D] and lse [B,H,Nq] (fp32); queries without a key get 0 and
-    -inf."""
+    -inf.  Sums are fp32, the probabilities are rounded to bf16 for the product
+    with v."""
     _here((q, k, v, k_len, key_mask, out, lse), "q k v k_len key_mask out lse")
     d = _cross_desc(q, k, v, k_len, key_mask, softmax_scale)
     with _alloc_on(stream):

@@ -40,11 +40,17 @@
 // score tile (K = 16).  Selecting among the 128 scores of a row in registers
 // instead took 35 of 93 us at 2048 x 2048 keys, 32 heads, one key in ten masked.
 //
+// P is rounded to bf16, half a step of 2^-8 of each probability, because both
+// operands of the product with V have one type; the sum l is taken over the
+// unrounded fp32 values.  The output is then off by 1.3 to 1.4 times what its own
+// rounding alone leaves.
+//
 // Measured at D = 64: 2 x 16 heads, 2048 queries on 8192 keys of which padding
 // leaves four fifths, 165 us, 0.68 PFLOP/s, where the exponentials alone would
 // take 100 us and the products 68; 256 units on 148 SMs, two waves for 1.73,
-// account for most of the rest.  2 x 16 heads, 2048 x 2048: 60 us.  4 heads,
-// 256 x 8192, clusters of eight: 22 us, a CTA to a unit took 98.
+// account for most of the rest.  2 x 16 heads, 2048 x 2048, masked: D = 32 55 us,
+// D = 64 59, D = 128 88 (0.78 PFLOP/s); on 8192 keys D = 128 287 us, 0.96 PFLOP/s.
+// 4 heads, 256 x 8192, clusters of eight: 23 us, a CTA to a unit took 98.
 #pragma once
 
 #include <cooperative_groups.h>

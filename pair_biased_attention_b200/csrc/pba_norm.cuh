@@ -18,14 +18,18 @@
 // behind by the instructions per element: channels are worked on in packed
 // pairs, and a thread takes 32 bytes of every tensor where its registers allow.
 // Measured: 1024^2 rows of 128 channels, bf16, with both layer norms, gate and
-// scale (5 tensors, 1.34 GB) 237 us, 5.7 TB/s, 0.86 of a copy's rate.  With the
+// scale (5 tensors, 1.34 GB) 230 us, 5.8 TB/s, 0.89 of a copy's rate.  With the
 // parameters unpacked from L1 for every row and the rows' addresses multiplied
 // out it was 283 us, bound by instructions; three blocks of 256 threads an SM
 // were no faster, scalar arithmetic took 314 us.  The gradients at 512^2 rows
-// (8 tensors, 0.54 GB) 109 us, 4.9 TB/s.  fp32 rows: 5.4 to 5.7 TB/s either way.
+// (8 tensors, 0.54 GB) 105 us, 5.1 TB/s.  fp32 rows: 5.6 to 5.8 TB/s either way.
 // Rows of a block, where a row's sums meet at barriers and a block has one row
-// under way, are slower: 32768 rows of 768, bf16, residual and RMS norm 5.1 and
-// 4.2 TB/s forward and backward, with all parts 2.3 and 3.2.
+// under way, are slower: 32768 rows of 768, bf16, residual and RMS norm 5.2 and
+// 4.5 TB/s forward and backward, with all parts 2.4 and 3.3 (fp32 4.5 and 5.6).
+// Over 4096 channels, fp32 forward and both types backward, a block has 1024
+// threads of 64 registers, into which the parts do not fit: 660 to 992 bytes a
+// thread spill in the backward, 100 in the forward.  4096 rows of 8192, bf16, 5.9
+// and 1.4 TB/s, with all parts 2.1 and 1.1 (fp32 5.3 and 2.6, 3.2 and 2.0).
 #pragma once
 
 #include <cfloat>
@@ -107,10 +111,11 @@ __host__ __device__ constexpr int norm_word() {
 
 // A thread's channels of `kArrays` tensors, row after row.  Aligned rows run
 // through a ring in shared memory, kStages rows deep, that the thread fills with
-// asynchronous copies and reads alone: about 100 KB on their way per SM, which
-// is what it takes to keep HBM busy (one row ahead in registers, 48 KB, reached
-// 0.69 of the rate).  Other rows are read element by element when they are
-// needed.  Every tensor has a pointer that walks down its rows.
+// asynchronous copies and reads alone: with all parts 196 KB on their way per SM
+// forward and 164 KB backward (bf16, rows of up to 32 threads), a third and a
+// fifth of it for each tensor (one row ahead in registers, 48 KB, reached 0.69 of
+// HBM's rate).  Other rows are read element by element when they are needed.
+// Every tensor has a pointer that walks down its rows.
 template <typename T, bool kVec, int E, int kArrays, int kStages, int kThreads>
 struct RowStream {
   using W = typename T::Word;
@@ -518,9 +523,10 @@ using NormBwdStream = RowStream<T, kVec, kNormBwdChannels, 5, norm_bwd_stages<T,
 
 // kParts: which parts there are (norm_parts), known when the kernel is built for
 // the usual sets of them, with dh; or -1, asked at run time.  The formulas are
-// long enough for that to count: 512^2 rows of 128 channels, bf16, all parts 141
-// us asked and 109 known, residual and layer norm 108 and 77.  The forward
-// gained nothing by it.
+// long enough for that to count: 512^2 rows of 128 channels, bf16, when each set
+// was measured both ways, all parts 141 us asked and 109 known, residual and layer
+// norm 108 and 77.  Sets without dh, and a last block without pre, are asked.  The
+// forward gained nothing by it.
 __host__ __device__ constexpr int norm_parts(bool f, bool gate, bool post, bool pre) {
   return f + 2 * gate + 4 * post + 8 * pre;
 }

@@ -133,9 +133,10 @@ __device__ __forceinline__ void load_keys8(const int32_t *p, int c, int Nk, bool
 // The block's columns of the table wait in shared memory, row-contiguous, so
 // that neighbouring distances fall into neighbouring banks; bf16 keeps two
 // heads per word, one read serving both.
-// Measured at 4096 x 4096 x 16 heads, bf16, with a base: 180 us, 6.0 TB/s, 0.91
-// of a copy's rate; fp32 at 2048 x 2048 x 16 95 us, 5.7 TB/s.  Without the base's ring, its loads one head ahead in
-// registers, that was 279 us.
+// Measured at 4096 x 4096 x 16 heads, bf16, with a base: 177 us, 6.1 TB/s, 0.92
+// of a copy's rate; fp32 at 2048 x 2048 x 16 90 us, 6.0 TB/s.  Without the base's
+// ring, its loads one head ahead in registers, that was 279 us.  Rows of 2047
+// keys, bf16: 30 us against 23 for 2048, their last eight element by element.
 template <typename T, bool kVec, bool kBase>
 __global__ void __launch_bounds__(kRelposThreads) relpos_fwd_kernel(const __grid_constant__ RelposParams p) {
   constexpr bool kBf = sizeof(typename T::Word) == 2;
@@ -277,8 +278,9 @@ __global__ void __launch_bounds__(kRelposThreads) relpos_fwd_kernel(const __grid
 // every sum is fixed.  The columns are added at the end of the block, in fp32 (in
 // 64 bits that took 3 to 15 % of the call, for eight additions next to a thread's
 // 4096), the blocks' tables by relpos_grad_sum_kernel in 64 bits.
-// Measured at 4096 x 4096 x 16 heads, bf16, 66 rows with two chains: 151 us,
-// 3.6 TB/s, a little over half of HBM's rate.  Some 80 instructions per eight
+// Measured at 4096 x 4096 x 16 heads, bf16, 66 rows with two chains: 150 us,
+// 3.6 TB/s, a little over half of HBM's rate; where most pairs are near (32 x 12
+// heads x 512^2, logarithmic up to 512) 1.3 TB/s.  Some 80 instructions per eight
 // elements, a tenth of them near the diagonal, are what bounds it, with four
 // blocks to an SM by their tables; a deeper ring changed nothing.
 template <typename T, bool kVec>
