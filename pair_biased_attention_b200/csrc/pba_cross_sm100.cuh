@@ -56,7 +56,7 @@
 #include <cooperative_groups.h>
 #include <cuda.h>
 
-#include "pba_ptx.cuh"
+#include "pba_ptx_more.cuh"
 
 namespace pba {
 

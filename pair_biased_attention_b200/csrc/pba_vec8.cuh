@@ -6,7 +6,7 @@
 
 #include <cstdint>
 
-#include "pba_ptx.cuh"
+#include "pba_ptx_more.cuh"
 
 namespace pba {
 
